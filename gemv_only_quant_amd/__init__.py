@@ -428,3 +428,9 @@ def quantize(W, w_bit, group_size, symmetric=False):
                                             device=W.device)
     qmm_quantize(W, codes[W.dtype], qw, sc, qz, N, K, w_bit, group_size, symmetric)
     return qw, sc, qz
+
+
+# ------------------------------------------------ int8 x int8 (include/qmm_int8.h)
+from .int8 import (ACTIVATIONS, EXPORTS_INT8, QMM_GELU, QMM_GELU_TANH, QMM_I8, QMM_SILU,  # noqa: E402,F401
+                   quantize_tokens, w8a8_gated, w8a8_gated_backward, w8a8_gemm,
+                   w8a8_gemm_backward)

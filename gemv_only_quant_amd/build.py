@@ -28,7 +28,7 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
           "-mllvm", "-amdgpu-kernarg-preload-count=16"]
 SOURCES = ["qmm_api.cpp", "gemv_lowbit.hip", "gemv_tile.hip", "gemv_int8.hip", "repack.hip",
            "gemm_mfma.hip", "gemm_large.hip", "gemm_medium.hip", "ternary.hip", "ternary_large.hip",
-           "quantize.hip"]
+           "quantize.hip", "w8a8_api.cpp", "w8a8_quantize.hip", "w8a8_tile.hip", "w8a8_backward.hip"]
 
 
 def _stale(src, obj):
@@ -36,7 +36,7 @@ def _stale(src, obj):
         return True
     deps = [os.path.join(CSRC, src)] + [os.path.join(CSRC, h) for h in os.listdir(CSRC)
                                         if h.endswith(".h")]
-    deps.append(os.path.join(ROOT, "include", "qmm.h"))
+    deps += [os.path.join(ROOT, "include", h) for h in ("qmm.h", "qmm_int8.h")]
     return max(os.path.getmtime(d) for d in deps) > os.path.getmtime(obj)
 
 

@@ -167,6 +167,15 @@ hipError_t scratch_of_current_device(void** out) {
 }  // namespace
 
 namespace qmm {
+int set_error(int status, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof g_err, fmt, ap);
+  va_end(ap);
+  return status;
+}
+int clear_error() { return ok(); }
+
 int env_int(const char* name) {
   const char* v = getenv(name);
   if (v == nullptr || *v == '\0') return -1;

@@ -24,6 +24,11 @@ hipError_t launch_kernel(void (*k)(P...), dim3 grid, dim3 block, hipStream_t s, 
       v);
 }
 
+// Error text of the C ABI, one for each thread (qmm_last_error): sets it and
+// returns the status, or clears it and returns QMM_OK (qmm_api.cpp).
+int set_error(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int clear_error();
+
 // Arguments shared by every matmul launcher, already validated.
 struct MatmulArgs {
   const void* x;

@@ -1,0 +1,115 @@
+// w8a8_internal.h -- launchers of the int8 x int8 operators (not public).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "qmm_internal.h"
+
+namespace qmm {
+
+// Data types as in qmm.h / qmm_int8.h: 0 fp16, 1 bf16, 2 fp32, 3 int8.
+constexpr int kTypeI8 = 3;
+enum { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
+
+__host__ __device__ constexpr int64_t round_up(int64_t v, int64_t to) {
+  return (v + to - 1) / to * to;
+}
+
+// Bytes of contraction per pipeline stage of the tile kernels: operands that
+// the library lays out itself are zero-padded to whole stages.
+constexpr int kStageBytes = 256;
+
+// ---- per-token quantizer (w8a8_quantize.hip) -------------------------------
+hipError_t launch_quantize_tokens(const void* x, int x_dtype, int64_t ldx, int8_t* xq,
+                                  int64_t ldxq, float* sx, int M, int K, hipStream_t s);
+
+// ---- products of codes, forward --------------------------------------------
+struct W8A8Args {
+  const int8_t* x;
+  int64_t ldx;
+  const float* sx;
+  const int8_t* w[2];  // w[1]: the up projection (gated only)
+  const float* sw[2];
+  int64_t ldw;
+  void* y;
+  int y_dtype;
+  int64_t ldy;
+  int M, N, K;
+  bool gated;
+  int act;
+  hipStream_t stream;
+};
+hipError_t launch_w8a8(const W8A8Args& a);
+
+// ---- gradients -------------------------------------------------------------
+// What a backward pass keeps in its workspace; offsets in bytes.
+//   scal   4 floats: c1, 1 / c1, c2, 1 / c2 (powers of two, see w8a8_backward.hip)
+//   d      (M, Jp) dy sw c1 (gated: dg sg c1 | du su c1), Jp = parts * Np
+//   wt     (K, Jp) the codes of W transposed (gated: Wg | Wu), in dy's type
+//   dt     (parts * Nr, Mp) dy sx c2 transposed (rows N .. Nr of a part unused)
+//   xt     (K, Mp) the codes of x transposed, in dy's type
+// with the contracted axes zero-padded to whole stages.
+struct BackwardPlan {
+  int parts;
+  int64_t Np, Jp, Nr, Mp;
+  size_t scal, d, wt, dt, xt, bytes;
+};
+BackwardPlan plan_backward(int M, int N, int K, bool gated, bool weight_grad);
+
+struct BackwardArgs {
+  const void* dy;
+  int dtype;  // XF16 / XBF16
+  int64_t lddy;
+  const int8_t* x;
+  int64_t ldx;
+  const float* sx;
+  const int8_t* w[2];
+  const float* sw[2];
+  int64_t ldw;
+  void* dx;
+  int64_t lddx;
+  void* dw[2];
+  int64_t lddw;
+  int M, N, K;
+  bool gated;
+  int act;
+  void* ws;
+  hipStream_t stream;
+};
+hipError_t launch_backward(const BackwardArgs& a, const BackwardPlan& p);
+
+// Zeros a (rows, cols) matrix of elements of `size` bytes (empty sums).
+hipError_t launch_fill_zero(void* y, int size, int64_t ld, int rows, int cols, hipStream_t s);
+
+// ---- tile kernels (w8a8_tile.hip) -------------------------------------------
+// C (rows M of A, rows N of B) = A B^t over `kb` contracted bytes; element
+// types and what becomes of C are the kernel's.
+struct TileArgs {
+  const void* a;       // (M, kb bytes), leading dimension lda bytes
+  int64_t lda;
+  const void* b[2];    // (N, kb bytes) each
+  int64_t ldb;
+  int M, N, kb;
+  const float* sa;     // scale of each row of A (int8)
+  const float* sb[2];  // scale of each row of B (int8)
+  const float* scal;   // plain: C is multiplied by *scal
+  void* y;
+  int y_dtype;
+  int64_t ldy;
+  void* y2;            // plain: where rows M2 and up go (as rows 0 and up)
+  int M2, Mv;          // plain: rows of one output, and how many of them exist
+  int act;
+  // gradient of the gated block (int8 products with a gradient epilogue)
+  const void* dh;
+  int64_t lddh;
+  void* d;             // (M, 2 Np)
+  void* dt;            // (2 Nr, Mp) or NULL
+  int64_t Np, Nr, Mp;
+};
+hipError_t launch_tile_scale(const TileArgs& t, hipStream_t s);
+hipError_t launch_tile_gated(const TileArgs& t, hipStream_t s);
+hipError_t launch_tile_grad(const TileArgs& t, int dtype, hipStream_t s);
+hipError_t launch_tile_plain(const TileArgs& t, int dtype, hipStream_t s);
+
+}  // namespace qmm
