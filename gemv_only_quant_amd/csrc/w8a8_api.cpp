@@ -125,13 +125,17 @@ qmm_status forward(const char* fn, bool gated, const void* x, int x_dtype, int64
   a.M = M, a.N = N, a.K = K;
   a.gated = gated, a.act = act;
   a.stream = s;
+  if (x_dtype == QMM_I8) QMM_CHECK(check_vector(fn, "sx", sx));
+  else QMM_CHECK(check_workspace(fn, qmm_w8a8_workspace_bytes(M, K, x_dtype), ws, ws_bytes, 16));
+  if (qmm::rows_fits(M, K)) {
+    a.sx = sx;
+    return device_status(fn, qmm::launch_rows(a, x, x_dtype, ldx));
+  }
   if (x_dtype == QMM_I8) {
-    QMM_CHECK(check_vector(fn, "sx", sx));
     a.x = static_cast<const int8_t*>(x);
     a.ldx = ldx;
     a.sx = sx;
   } else {
-    QMM_CHECK(check_workspace(fn, qmm_w8a8_workspace_bytes(M, K, x_dtype), ws, ws_bytes, 16));
     int8_t* xq = static_cast<int8_t*>(ws);
     a.ldx = code_ld(K);
     float* scale = reinterpret_cast<float*>(xq + (size_t)M * a.ldx);

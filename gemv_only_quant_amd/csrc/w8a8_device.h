@@ -78,4 +78,182 @@ __device__ __forceinline__ bool vec4_ok(const void* p, int64_t ld, int size) {
   return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * size)) & (uintptr_t)(4 * size - 1)) == 0;
 }
 
+// The 16 bytes of a chunk that starts at contracted byte k, those from kb on
+// cleared.
+__device__ __forceinline__ u32x4_t clear_tail(u32x4_t v, int k, int kb) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int left = kb - (k + 4 * j);
+    if (left <= 0) v[j] = 0;
+    else if (left < 4) v[j] &= (1u << (8 * left)) - 1u;
+  }
+  return v;
+}
+
+// ---- quantizing rows ---------------------------------------------------------
+template <int XDT> struct Elem;
+template <> struct Elem<XF16> { typedef _Float16 type; };
+template <> struct Elem<XBF16> { typedef __bf16 type; };
+template <> struct Elem<YF32> { typedef float type; };
+
+// Largest of the wave's 64 values, in every lane (DPP: butterfly inside each
+// row of 16 lanes, then the rows' results broadcast into lane 63).
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+#define QMM_DPP_MAX(ctrl, mask)                                                        \
+  {                                                                                    \
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, mask, 0xF, false); \
+    v = o > v ? o : v;                                                                 \
+  }
+  QMM_DPP_MAX(0xB1, 0xF)   // quad_perm [1,0,3,2]
+  QMM_DPP_MAX(0x4E, 0xF)   // quad_perm [2,3,0,1]
+  QMM_DPP_MAX(0x124, 0xF)  // row_ror:4
+  QMM_DPP_MAX(0x128, 0xF)  // row_ror:8
+  QMM_DPP_MAX(0x142, 0xA)  // row_bcast:15 into rows 1 and 3
+  QMM_DPP_MAX(0x143, 0xC)  // row_bcast:31 into rows 2 and 3
+#undef QMM_DPP_MAX
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// 8 consecutive elements as loaded: one 16-byte word of 16-bit elements, two
+// of fp32 ones.
+template <int XDT> struct Raw8 { u32x4_t w[XDT == YF32 ? 2 : 1]; };
+
+// Elements k .. k + 7 of the row that buffer b ends with (zeros past its
+// end): whole 16-byte loads, or one load per element where the row does not
+// start on 16 bytes or end on them.
+template <int XDT, bool VEC>
+__device__ __forceinline__ Raw8<XDT> load8(buf_t b, int k) {
+  Raw8<XDT> r;
+  constexpr int SZ = XDT == YF32 ? 4 : 2;
+  if constexpr (VEC) {
+    r.w[0] = buf_load128(b, k * SZ);
+    if constexpr (XDT == YF32) r.w[1] = buf_load128(b, k * SZ + 16);
+  } else if constexpr (XDT == YF32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.w[j / 4][j % 4] = buf_load32(b, (k + j) * SZ);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      r.w[0][j] = buf_load16(b, (k + 2 * j) * SZ) | (buf_load16(b, (k + 2 * j + 1) * SZ) << 16);
+  }
+  return r;
+}
+// Whether whole 16-byte loads serve rows of K elements of `size` bytes.
+__host__ __device__ inline bool vec8_ok(const void* x, int64_t ld, int K, int size) {
+  return ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(ld * size) | (uintptr_t)((int64_t)K * size)) & 15) == 0;
+}
+
+template <int XDT>
+__device__ __forceinline__ void floats8(const Raw8<XDT>& r, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (XDT == YF32) {
+      const uint32_t e = r.w[j / 4][j % 4];
+      v[j] = __builtin_bit_cast(float, e);
+    } else if constexpr (XDT == XBF16) {
+      const uint32_t e = r.w[0][j / 2];
+      v[j] = __builtin_bit_cast(float, j % 2 ? e & 0xFFFF0000u : e << 16);
+    } else {
+      const uint32_t e = r.w[0][j / 2];
+      const half2_t h = __builtin_bit_cast(half2_t, e);
+      v[j] = (float)h[j % 2];
+    }
+  }
+}
+
+// Largest magnitude as bit patterns without the sign: they order as the
+// values do, NaN above infinity above what is finite.  16-bit elements are
+// compared in pairs, as they were loaded; top_f32 gives the fp32 pattern.
+template <int XDT>
+__device__ __forceinline__ uint32_t top8(const Raw8<XDT>& r, uint32_t top) {
+  if constexpr (XDT == YF32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t b = r.w[j / 4][j % 4] & 0x7FFFFFFFu;
+      top = b > top ? b : top;
+    }
+    return top;
+  } else {
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    u16x2_t t = __builtin_bit_cast(u16x2_t, top);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t b = r.w[0][j] & 0x7FFF7FFFu;
+      t = __builtin_elementwise_max(t, __builtin_bit_cast(u16x2_t, b));
+    }
+    return __builtin_bit_cast(uint32_t, t);
+  }
+}
+template <int XDT> __device__ __forceinline__ uint32_t top_f32(uint32_t top) {
+  if constexpr (XDT == YF32) return top;
+  const uint32_t lo = top & 0xFFFFu, hi = top >> 16, m = lo > hi ? lo : hi;
+  if constexpr (XDT == XBF16) return m << 16;
+  const float f = (float)__builtin_bit_cast(_Float16, (uint16_t)m);
+  return __builtin_bit_cast(uint32_t, f);
+}
+
+// A row's scale from its largest magnitude, and what its codes are formed
+// with: 1 / s, and for scales so small that this would overflow a factor
+// 2^64 on both s and x first, which is exact.
+struct RowScale {
+  float s;     // as stored: NaN where the row is not finite
+  float ss;    // s lift
+  float r;     // 1 / ss
+  float lift;  // 1 or 2^64
+  bool none;   // every code is 0
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t top) {
+  RowScale c;
+  const bool bad = top >= 0x7F800000u;
+  c.s = bad ? __builtin_nanf("") : __fdiv_rn(__builtin_bit_cast(float, top), 127.0f);
+  c.none = bad || c.s == 0.0f;
+  c.lift = c.s < 0x1p-100f ? 0x1p64f : 1.0f;
+  c.ss = c.s * c.lift;
+  c.r = __fdiv_rn(1.0f, c.none ? 1.0f : c.ss);
+  return c;
+}
+
+// rint of the exact quotient x / s, ties to even, clamped.  q = rint(x fl(1/s))
+// is at most one off; d = x - q s is exact (a fused multiply-add, and what is
+// left has no more bits than s), so 2 |d| against s decides: more than s moves
+// q one further, s itself is a tie.
+__device__ __forceinline__ float code_of(float x, float s, float r) {
+  const float q = __builtin_rintf(x * r);
+  const float d = 2.0f * __builtin_fmaf(-q, s, x);
+  const float a = fabsf(d);
+  const bool move = a > s || (a == s && ((int)q & 1));
+  return __builtin_amdgcn_fmed3f(move ? q + __builtin_copysignf(1.0f, d) : q, -127.0f, 127.0f);
+}
+
+// 8 codes of a row, packed.  f = x fl(1 / s) is within |f| 2^-22 < 2^-15 of the
+// quotient: unless one of the 8 lies within 2^-14 of a half, both round alike,
+// and adding 1.5 2^23 leaves rint(f) in the sum's low bits, its low byte the
+// code (in ordinary rows |f| < 127.5: nothing to clamp).  Else, and where the
+// row is lifted, all 8 take code_of.
+template <int XDT>
+__device__ __forceinline__ u32x2_t codes8(const Raw8<XDT>& raw, const RowScale& c) {
+  if (c.none) return u32x2_t{0u, 0u};
+  float v[8];
+  floats8<XDT>(raw, v);
+  uint32_t b[8];
+  float worst = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float f = v[j] * c.r;
+    const float t = f + 12582912.0f;
+    worst = fmaxf(worst, fabsf(f - (t - 12582912.0f)));
+    b[j] = __builtin_bit_cast(uint32_t, t);
+  }
+  if (worst > 0.5f - 0x1p-14f || c.lift != 1.0f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = (uint32_t)(int)code_of(v[j] * c.lift, c.ss, c.r);
+  }
+  // low bytes of four words, by two byte permutes and a third
+  auto pack = [](uint32_t p, uint32_t q, uint32_t r, uint32_t s) {
+    const uint32_t lo = __builtin_amdgcn_perm(q, p, 0x0C0C0400u), hi = __builtin_amdgcn_perm(s, r, 0x04000C0Cu);
+    return lo | hi;
+  };
+  return u32x2_t{pack(b[0], b[1], b[2], b[3]), pack(b[4], b[5], b[6], b[7])};
+}
+
 }  // namespace qmm

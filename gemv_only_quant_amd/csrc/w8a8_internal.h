@@ -41,6 +41,10 @@ struct W8A8Args {
   hipStream_t stream;
 };
 hipError_t launch_w8a8(const W8A8Args& a);
+// A few tokens (w8a8_rows.hip): x of any type, quantized within the launch
+// where it is not codes (a.x and a.sx then count for nothing).
+bool rows_fits(int M, int K);
+hipError_t launch_rows(const W8A8Args& a, const void* x, int x_dtype, int64_t ldx);
 
 // ---- gradients -------------------------------------------------------------
 // What a backward pass keeps in its workspace; offsets in bytes.

@@ -41,18 +41,6 @@ __device__ __forceinline__ typename Acc<KIND>::type mfma_t(const u32x4_t& a, con
                                                    __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
-// The 16 bytes of a chunk that starts at contracted byte k, those from kb on
-// cleared.
-__device__ __forceinline__ u32x4_t clear_tail(u32x4_t v, int k, int kb) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int left = kb - (k + 4 * j);
-    if (left <= 0) v[j] = 0;
-    else if (left < 4) v[j] &= (1u << (8 * left)) - 1u;
-  }
-  return v;
-}
-
 // One 16-row tile of a wave (accumulators of its NT strips) through LDS to
 // the epilogue: rows of 4 consecutive columns per lane.  `t0` is the tile's
 // LDS (16 rows of 16 NT + 4 words), n0 the wave's first output column, m0
