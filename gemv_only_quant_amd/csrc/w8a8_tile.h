@@ -1,0 +1,248 @@
+// w8a8_tile.h -- what the matrix-core kernels of the int8 x int8 operators
+// share: instruction kinds, the order of tiles, and the epilogues.
+#pragma once
+#include <type_traits>
+
+#include "w8a8_device.h"
+
+namespace qmm {
+
+enum { EPI_SCALE = 0, EPI_GATED = 1, EPI_GRAD = 2, EPI_PLAIN = 3 };
+
+// KIND: kTypeI8, XF16 or XBF16
+template <int KIND> struct Acc { typedef f32x4_t type; };
+template <> struct Acc<kTypeI8> { typedef i32x4_t type; };
+
+template <int KIND>
+__device__ __forceinline__ typename Acc<KIND>::type mfma_t(const u32x4_t& a, const u32x4_t& b,
+                                                           typename Acc<KIND>::type c) {
+  if constexpr (KIND == kTypeI8)
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a),
+                                                 __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
+  else if constexpr (KIND == XF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a),
+                                                  __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+// LDS of the epilogue: a 16-row tile of a wave is 16 rows of 16 NT words,
+// column c of row r at word c ^ 16 (r / 4 % (NT % 4 ? 2 : 4)): the four row
+// quads that the accumulators hold at once then lie in different banks, and 4
+// consecutive columns stay together.
+template <int NT> __device__ __forceinline__ constexpr int epi_word(int row, int col) {
+  return row * 16 * NT + (col ^ (16 * ((row >> 2) & (NT % 4 ? 1 : 3))));
+}
+constexpr int epi_words(int nt) { return 256 * nt; }
+// ... and after the tiles, for the gradient epilogue, one transposed tile of
+// 16-bit values: 16 rows of a column, padded to keep 16-byte reads aligned.
+constexpr int kEpiLdh = 24;
+constexpr int epi_t_words(int nt) { return 16 * nt * kEpiLdh / 2; }
+
+// Accumulators of a 16-row tile to its LDS.
+template <int KIND, int NT>
+__device__ __forceinline__ void put_tile(const typename Acc<KIND>::type (&acc)[NT], uint32_t* t0,
+                                         int lane) {
+  const int l16 = lane & 15, quad = lane >> 4;
+#pragma unroll
+  for (int s = 0; s < NT; ++s)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      // through a value: a bit cast of the vector's element itself takes
+      // element 0 whatever r is, with this compiler
+      const auto e = acc[s][r];
+      t0[epi_word<NT>(4 * quad + r, 16 * s + l16)] = __builtin_bit_cast(uint32_t, e);
+    }
+}
+
+// The epilogues, for a lane's 4 consecutive columns of the wave's output in
+// rows that lie 64 / (columns / 4) apart.  What does not change from tile to
+// tile (column scales, alignment) is read once, in init; the rows' scales are
+// taken from LDS (`sa`, the workgroup's rows) and the gradient's incoming
+// values one tile ahead: nothing in the loop over tiles waits for memory.
+template <int KIND, int EPI, int NT, int DT> struct Epilogue {
+  static constexpr bool PAIR = EPI == EPI_GATED || EPI == EPI_GRAD;
+  static constexpr int COLS = PAIR ? 8 * NT : 16 * NT;  // output columns of the wave
+  static constexpr int LPR = COLS / 4;                  // lanes per row
+  static constexpr int RPP = 64 / LPR;                  // rows per pass
+  static constexpr int PASSES = 16 / RPP;
+  typedef typename Acc<KIND>::type acc_t;
+  typedef typename Half16<DT>::type T;
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  typedef T T8 __attribute__((ext_vector_type(8)));
+
+  int lane, col, n0, n, nn;  // nn: columns of this lane that exist (may be <= 0)
+  float s0[4], s1[4];        // column scales; of the up projection
+  float k1, k2;              // PLAIN: the factor; GRAD: c1, c2
+  bool vec;
+  uint16_t dh[EPI == EPI_GRAD ? PASSES : 1][4];  // the next tile's incoming gradient
+
+  __device__ __forceinline__ void init(const TileArgs& g, int n0_, int lane_) {
+    lane = lane_, n0 = n0_;
+    col = 4 * (lane % LPR), n = n0 + col, nn = min(4, g.N - n);
+    if constexpr (EPI == EPI_PLAIN) {
+      k1 = *g.scal;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s0[j] = j < nn ? g.sb[0][n + j] : 0.f;
+        s1[j] = PAIR && j < nn ? g.sb[1][n + j] : 0.f;
+      }
+    }
+    if constexpr (EPI == EPI_GRAD) {
+      k1 = g.scal[0], k2 = g.scal[2];
+      vec = vec4_ok(g.dh, g.lddh, 2);
+    } else {
+      vec = vec4_ok(g.y, g.ldy, g.y_dtype == YF32 ? 4 : 2) && (EPI != EPI_PLAIN || vec4_ok(g.y2, 0, 2));
+    }
+  }
+
+  // Requests what the tile at row m0 will need from memory.
+  __device__ __forceinline__ void fetch(const TileArgs& g, int m0) {
+    if constexpr (EPI == EPI_GRAD) {
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int m = m0 + RPP * p + lane / LPR;
+        const uint16_t* src = static_cast<const uint16_t*>(g.dh) + (int64_t)m * g.lddh + n;
+        const bool row = m < g.M;
+        if (vec && row && nn >= 4) {
+          const u32x2_t q = *reinterpret_cast<const u32x2_t*>(src);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dh[p][j] = (uint16_t)(q[j / 2] >> (16 * (j % 2)));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dh[p][j] = row && j < nn ? src[j] : (uint16_t)0;
+        }
+      }
+    }
+  }
+
+  // The tile that put_tile wrote to t0, whose first row is m0; sa: its rows'
+  // scales; tt: the wave's transposed tile (GRAD); m1: the next tile's first row.
+  __device__ __forceinline__ void tile(const TileArgs& g, const uint32_t* t0, const float* sa,
+                                       uint32_t* ttw, int m0, int m1) {
+    if constexpr (EPI == EPI_SCALE || EPI == EPI_PLAIN || EPI == EPI_GATED) {
+      float v[PASSES][4];
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int row = RPP * p + lane / LPR;
+        const acc_t c = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, col));
+        if constexpr (EPI == EPI_PLAIN) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[p][j] = c[j] * k1;
+        } else if constexpr (EPI == EPI_SCALE) {
+          const float a = sa[row];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[p][j] = (float)c[j] * (a * s0[j]);
+        } else {
+          const acc_t u = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, COLS + col));
+          const float a = sa[row];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float d;
+            v[p][j] = act_parts(g.act, (float)c[j] * (a * s0[j]), &d) * ((float)u[j] * (a * s1[j]));
+          }
+        }
+      }
+      with_y(g.y, g.y_dtype, [&](auto* yt) {
+        typedef typename std::remove_pointer<decltype(yt)>::type Y;
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+          const int m = m0 + RPP * p + lane / LPR;
+          if (m >= g.M || nn <= 0) continue;
+          if constexpr (EPI == EPI_PLAIN) {
+            const bool second = m >= g.M2;
+            const int mo = second ? m - g.M2 : m;
+            Y* yo = second ? static_cast<Y*>(g.y2) : yt;
+            if (mo < g.Mv) store4(yo + (int64_t)mo * g.ldy + n, v[p], nn, vec);
+          } else {
+            store4(yt + (int64_t)m * g.ldy + n, v[p], nn, vec);
+          }
+        }
+      });
+    } else {
+      // dg and du in fp32, then d = (dg sg c1 | du su c1) row-major and
+      // dt = (dg sx c2 | du sx c2) transposed through LDS, zeros where a row
+      // or column only pads
+      constexpr int LDH = kEpiLdh;
+      T* tt = reinterpret_cast<T*>(ttw);
+      T* dd = static_cast<T*>(g.d);
+      float e[PASSES][4];
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[p][j] = (float)__builtin_bit_cast(T, (uint16_t)dh[p][j]);
+      fetch(g, m1);
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int row = RPP * p + lane / LPR, m = m0 + row;
+        const acc_t cg = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, col));
+        const acc_t cu = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, COLS + col));
+        const float a = sa[row];  // 0 for rows past M
+        T4 dgv = {}, duv = {};
+        T tg[4] = {}, tu[4] = {};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float gv = (float)cg[j] * (a * s0[j]), uv = (float)cu[j] * (a * s1[j]);
+          float da;
+          const float h = act_parts(g.act, gv, &da);
+          // columns past N only pad; a row's scale may be NaN, so not by a product
+          const float dg = j < nn ? e[p][j] * uv * da : 0.f, du = j < nn ? e[p][j] * h : 0.f;
+          dgv[j] = (T)(dg * (s0[j] * k1));
+          duv[j] = (T)(du * (s1[j] * k1));
+          tg[j] = (T)(dg * (a * k2));
+          tu[j] = (T)(du * (a * k2));
+          if (j >= nn) tg[j] = tu[j] = dgv[j] = duv[j] = (T)0.f;
+        }
+        if (m < g.M && n < g.Np) {  // n is a multiple of 4 and Np of 128
+          T* o = dd + (int64_t)m * (2 * g.Np) + n;
+          *reinterpret_cast<T4*>(o) = dgv;
+          *reinterpret_cast<T4*>(o + g.Np) = duv;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          tt[(col + j) * LDH + row] = tg[j];
+          tt[(COLS + col + j) * LDH + row] = tu[j];
+        }
+      }
+      if (g.dt != nullptr && m0 < g.Mp) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        T* dt = static_cast<T*>(g.dt);
+        for (int c = lane; c < 2 * COLS; c += 64) {
+          const int cn = n0 + c % COLS;
+          if (cn >= g.N) continue;
+          const T8 x = *reinterpret_cast<const T8*>(tt + c * LDH);
+          const T8 y = *reinterpret_cast<const T8*>(tt + c * LDH + 8);
+          T* o = dt + ((int64_t)(c / COLS) * g.Nr + cn) * g.Mp + m0;
+          *reinterpret_cast<T8*>(o) = x;
+          *reinterpret_cast<T8*>(o + 8) = y;
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      }
+    }
+  }
+};
+
+// The workgroup's row scales to LDS (0 for rows past M).
+template <int EPI>
+__device__ __forceinline__ void row_scales(const TileArgs& g, float* sa, int m0, int rows) {
+  if constexpr (EPI != EPI_PLAIN)
+    for (int i = threadIdx.x; i < rows; i += 256) sa[i] = m0 + i < g.M ? g.sa[m0 + i] : 0.f;
+}
+
+// Tile of work item b of n_tiles x m_tiles: consecutive items on one XCD (the
+// dispatcher deals workgroups round-robin over the 8), and among them GM row
+// tiles of a column tile before the next column, so that the workgroups of an
+// XCD that run together share rows and columns through its L2.
+__device__ __forceinline__ void tile_of(int b, int n_tiles, int m_tiles, int* mt, int* nt) {
+  constexpr int GM = 4;
+  const int total = n_tiles * m_tiles, q = total / 8, r = total % 8, x = b % 8;
+  const int w = x * q + min(x, r) + b / 8;
+  const int per = GM * n_tiles, g = w / per, i = w % per;
+  const int gm = min(GM, m_tiles - g * GM);
+  *mt = g * GM + i % gm;
+  *nt = i / gm;
+}
+
+}  // namespace qmm
