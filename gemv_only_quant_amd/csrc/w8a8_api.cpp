@@ -220,6 +220,7 @@ hipError_t launch_w8a8(const W8A8Args& a) {
   t.sb[0] = a.sw[0], t.sb[1] = a.sw[1];
   t.y = a.y, t.y_dtype = a.y_dtype, t.ldy = a.ldy;
   t.act = a.act;
+  if (skinny_fits(a.M)) return launch_skinny(t, a.gated, a.stream);
   return a.gated ? launch_tile_gated(t, a.stream) : launch_tile_scale(t, a.stream);
 }
 
