@@ -21,6 +21,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(TileArgs g) {
   constexpr int COLS = GATED ? 8 * NT : 16 * NT;  // output columns of the workgroup
   constexpr int LD = 16 * NT + 4;                 // row of the sums in LDS
   __shared__ int sums[16 * MT * LD];
+  __shared__ float scales[16 * MT + 16 * NT];  // of the tokens, then of the strips' columns
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
@@ -29,48 +30,52 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(TileArgs g) {
   const int lda = (int)g.lda, ldb = (int)g.ldb;
 
   // a buffer per 16 rows of either operand, that ends with its last row
-  struct Rows {
-    const char* base;
-    int range;
-  };
   auto rows_of = [&](const void* p, int64_t ld, int first, int limit) {
     const int n = min(16, limit - first);
-    Rows r;
-    r.base = static_cast<const char*>(p) + (int64_t)(n > 0 ? first : 0) * ld;
-    r.range = n > 0 ? (int)((n - 1) * ld) + kb16 : 0;
-    return r;
+    return make_buf(static_cast<const char*>(p) + (int64_t)(n > 0 ? first : 0) * ld,
+                    n > 0 ? (uint32_t)((n - 1) * (int)ld + kb16) : 0u);
   };
-  Rows ar[MT], br[NT];
+  buf_t ar[MT], br[NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) ar[i] = rows_of(g.a, g.lda, 16 * i, g.M);
 #pragma unroll
   for (int s = 0; s < NT; ++s)
     br[s] = GATED ? rows_of(g.b[s / (NT / 2)], g.ldb, n0 + 16 * (s % (NT / 2)), g.N)
                   : rows_of(g.b[0], g.ldb, n0 + 16 * s, g.N);
-  const int ao = l16 * lda + 16 * quad, bo = l16 * ldb + 16 * quad;
+  // A load takes 128 bytes, a whole cache line, of 8 rows: chunk quad + 4 (l16
+  // / 8) of row l16 % 8, then the same of rows 8 up.  (As operands are laid
+  // out, 16 rows x 64 bytes, a load would take half lines, and L1 gives most of
+  // them up before their other half is asked for.)  operands() makes the pair of loads
+  // the operands of two k steps: lanes 8-15 of the first and 0-7 of the second
+  // change places, by rotating rows of 16 lanes by 8.
+  const int ao = (l16 & 7) * lda + 16 * (quad + 4 * (l16 >> 3));
+  const int bo = (l16 & 7) * ldb + 16 * (quad + 4 * (l16 >> 3));
+  auto operands = [&](u32x4_t (&v)[2]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t p = v[0][j], q = v[1][j];
+      v[0][j] = (uint32_t)__builtin_amdgcn_update_dpp((int)p, (int)q, 0x128, 0xF, 0xC, false);
+      v[1][j] = (uint32_t)__builtin_amdgcn_update_dpp((int)q, (int)p, 0x128, 0xF, 0x3, false);
+    }
+  };
 
-  // item i of this wave: 128 bytes of K from byte k_of(i) on; past the end it
-  // has empty buffers, which read zeros without touching memory
+  // item i of this wave: 128 bytes of K from byte k_of(i) on; past the end its
+  // offset lies outside every buffer, which reads zeros and no memory
   struct Item {
     u32x4_t a[MT][2], b[NT][2];
   };
   auto k_of = [&](int i) { return (wave + kSkinnyWaves * (i >> 1)) * 256 + 128 * (i & 1); };
   auto load = [&](int i, Item& it) {
-    const int k = k_of(i);
-    int av = ao, bv = bo;  // opaque: the sums below become immediate offsets
-    asm volatile("" : "+v"(av), "+v"(bv));
+    const int k = k_of(i), at = k < kb ? k : 0x60000000;
+    const int av = ao + at, bv = bo + at;
 #pragma unroll
-    for (int s = 0; s < NT; ++s) {
-      const buf_t b = make_buf(br[s].base + k, k < kb && br[s].range > 0 ? (uint32_t)(br[s].range - k) : 0u);
+    for (int s = 0; s < NT; ++s)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) it.b[s][j] = buf_load128_stream(b, bv + 64 * j);
-    }
+      for (int j = 0; j < 2; ++j) it.b[s][j] = buf_load128_stream(br[s], bv + 8 * j * ldb);
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const buf_t b = make_buf(ar[t].base + k, k < kb && ar[t].range > 0 ? (uint32_t)(ar[t].range - k) : 0u);
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) it.a[t][j] = buf_load128(b, av + 64 * j);
-    }
+      for (int j = 0; j < 2; ++j) it.a[t][j] = buf_load128(ar[t], av + 8 * j * lda);
   };
   i32x4_t acc[MT][NT];
 #pragma unroll
@@ -79,6 +84,10 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(TileArgs g) {
     for (int s = 0; s < NT; ++s) acc[i][s] = i32x4_t{0, 0, 0, 0};
   auto use = [&](int i, Item& it) {
     const int k = k_of(i);
+#pragma unroll
+    for (int s = 0; s < NT; ++s) operands(it.b[s]);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) operands(it.a[t]);
     if (k + 128 > kb) {  // the codes' bytes past K (whatever B holds there meets zeros)
 #pragma unroll
       for (int t = 0; t < MT; ++t)
@@ -97,6 +106,14 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(TileArgs g) {
   load(0, x);
   load(1, y);
   for (int i = threadIdx.x; i < 16 * MT * LD; i += 64 * kSkinnyWaves) sums[i] = 0;
+  {
+    const int i = threadIdx.x;
+    if (i < 16 * MT) scales[i] = i < g.M ? g.sa[i] : 0.f;
+    else if (i < 16 * MT + 16 * NT) {
+      const int c = i - 16 * MT, n = n0 + c % COLS;
+      scales[i] = n < g.N ? g.sb[GATED ? c / COLS : 0][n] : 0.f;
+    }
+  }
   __syncthreads();
   for (int i = 0; k_of(i) < kb; i += 2) {
     use(i, x);
@@ -123,17 +140,16 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(TileArgs g) {
       const int m = i / PER_ROW, col = 4 * (i % PER_ROW), n = n0 + col;
       const int nn = min(4, g.N - n);
       if (m >= g.M || nn <= 0) continue;
-      const float a = g.sa[m];
+      const float a = scales[m];
+      const float* sc = scales + 16 * MT + col;
       const int* c = &sums[m * LD + col];
       float v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float s = j < nn ? g.sb[0][n + j] : 0.f;
-        v[j] = (float)c[j] * (a * s);
+        v[j] = (float)c[j] * (a * sc[j]);
         if constexpr (GATED) {
-          const float t = j < nn ? g.sb[1][n + j] : 0.f;
           float d;
-          v[j] = act_parts(g.act, v[j], &d) * ((float)c[COLS + j] * (a * t));
+          v[j] = act_parts(g.act, v[j], &d) * ((float)c[COLS + j] * (a * sc[COLS + j]));
         }
       }
       store4(yt + (int64_t)m * g.ldy + n, v, nn, vec);
