@@ -42,22 +42,9 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(TileArgs g) {
   for (int s = 0; s < NT; ++s)
     br[s] = GATED ? rows_of(g.b[s / (NT / 2)], g.ldb, n0 + 16 * (s % (NT / 2)), g.N)
                   : rows_of(g.b[0], g.ldb, n0 + 16 * s, g.N);
-  // A load takes 128 bytes, a whole cache line, of 8 rows: chunk quad + 4 (l16
-  // / 8) of row l16 % 8, then the same of rows 8 up.  (As operands are laid
-  // out, 16 rows x 64 bytes, a load would take half lines, and L1 gives most of
-  // them up before their other half is asked for.)  operands() makes the pair of loads
-  // the operands of two k steps: lanes 8-15 of the first and 0-7 of the second
-  // change places, by rotating rows of 16 lanes by 8.
+  // whole 128-byte lines of 8 rows per load (line_operands)
   const int ao = (l16 & 7) * lda + 16 * (quad + 4 * (l16 >> 3));
   const int bo = (l16 & 7) * ldb + 16 * (quad + 4 * (l16 >> 3));
-  auto operands = [&](u32x4_t (&v)[2]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t p = v[0][j], q = v[1][j];
-      v[0][j] = (uint32_t)__builtin_amdgcn_update_dpp((int)p, (int)q, 0x128, 0xF, 0xC, false);
-      v[1][j] = (uint32_t)__builtin_amdgcn_update_dpp((int)q, (int)p, 0x128, 0xF, 0x3, false);
-    }
-  };
 
   // item i of this wave: 128 bytes of K from byte k_of(i) on; past the end its
   // offset lies outside every buffer, which reads zeros and no memory
@@ -85,9 +72,9 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(TileArgs g) {
   auto use = [&](int i, Item& it) {
     const int k = k_of(i);
 #pragma unroll
-    for (int s = 0; s < NT; ++s) operands(it.b[s]);
+    for (int s = 0; s < NT; ++s) line_operands(it.b[s]);
 #pragma unroll
-    for (int t = 0; t < MT; ++t) operands(it.a[t]);
+    for (int t = 0; t < MT; ++t) line_operands(it.a[t]);
     if (k + 128 > kb) {  // the codes' bytes past K (whatever B holds there meets zeros)
 #pragma unroll
       for (int t = 0; t < MT; ++t)

@@ -27,6 +27,21 @@ __device__ __forceinline__ typename Acc<KIND>::type mfma_t(const u32x4_t& a, con
                                                    __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
+// Two loads of 16 rows of an operand, each 128 bytes (a whole cache line) of 8
+// rows -- chunk quad + 4 (l16 / 8) of row l16 % 8, then the same of rows 8 up --
+// made the operands of two k steps: lanes 8-15 of the first and 0-7 of the
+// second change places, by rotating rows of 16 lanes by 8.  (Loaded as operands
+// are laid out, 16 rows x 64 bytes, a load takes half lines, and L1 may have given
+// a line up before its other half is asked for.)
+__device__ __forceinline__ void line_operands(u32x4_t (&v)[2]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t p = v[0][j], q = v[1][j];
+    v[0][j] = (uint32_t)__builtin_amdgcn_update_dpp((int)p, (int)q, 0x128, 0xF, 0xC, false);
+    v[1][j] = (uint32_t)__builtin_amdgcn_update_dpp((int)q, (int)p, 0x128, 0xF, 0x3, false);
+  }
+}
+
 // LDS of the epilogue: a 16-row tile of a wave is 16 rows of 16 NT words,
 // column c of row r at word c ^ 16 (r / 4 % (NT % 4 ? 2 : 4)): the four row
 // quads that the accumulators hold at once then lie in different banks, and 4
