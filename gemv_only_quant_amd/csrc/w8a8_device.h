@@ -1,5 +1,7 @@
 // w8a8_device.h -- device helpers of the int8 x int8 kernels (gfx950).
 #pragma once
+#include <type_traits>
+
 #include "qmm_device.h"
 #include "w8a8_internal.h"
 
@@ -7,15 +9,13 @@ namespace qmm {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
-// e^v for fp32, within about two units in the last place over the whole
-// range: v log2(e) as a rounded product and its remainder (one fused multiply-add,
+// e^v, v <= 0, within about two units in the last place: v log2(e) as a rounded product and its remainder (one fused multiply-add,
 // plus the part of log2(e) that fp32 drops), 2^p (1 + r ln 2) from the
 // hardware's 2^p.  The bare 2^(v log2 e) loses |v| 2^-24 of the result.
-// Arguments are clamped to where the result is 0 or infinite anyway, so that
-// the remainder of an infinity is no NaN; a NaN stays one.
+// For v <= 0: below -200 the result is 0 anyway, and held there the remainder of
+// an infinity is no NaN.  (A NaN gives 0 or 1: callers carry it otherwise.)
 __device__ __forceinline__ float exp_f32(float v) {
-  v = v > 200.0f ? 200.0f : v;
-  v = v < -200.0f ? -200.0f : v;
+  v = fmaxf(v, -200.0f);
   const float L = 1.44269504f, Llo = 1.925963033e-8f;  // log2(e) = L + Llo
   const float p = v * L;
   const float r = __builtin_fmaf(v, L, -p) + v * Llo;
@@ -28,28 +28,44 @@ __device__ __forceinline__ float exp_f32(float v) {
 //   gelu: p = (1 + erf(v / sqrt 2)) / 2, p' = e^(-v^2 / 2) / sqrt(2 pi)
 //   gelu_tanh: (1 + tanh z) / 2 = 1 / (1 + e^-2z), z = sqrt(2 / pi) (v + 0.044715 v^3),
 //     p' = p (1 - p) 2 z'
-// 1 - p is formed as e^-t / (1 + e^-t), which keeps its leading digits; v p
-// is taken as 0 where p is, so that act(-inf) is 0 and not -inf * 0.
-__device__ __forceinline__ float act_parts(int act, float v, float* dact) {
-  if (act == ACT_GELU) {
+// With e = e^-|t|, p and 1 - p are 1 / (1 + e) and e / (1 + e), either way round:
+// both keep their leading digits.  v is held to +-1e30 where it meets a factor
+// that may be 0, so that act(-inf) is 0 and no infinity times 0 appears; NaN comes
+// back through p.
+template <int ACT>
+__device__ __forceinline__ float act_parts(float v, float* dact) {
+  const float vlo = fmaxf(v, -1e30f), vc = fminf(vlo, 1e30f);
+  if constexpr (ACT == ACT_GELU) {
     const float p = 0.5f * erfcf(v * -0.707106781f);
-    const float d = exp_f32(-0.5f * v * v) * 0.398942280f;
-    const float vd = d == 0.0f ? 0.0f : v * d;
-    *dact = p + vd;
-    return p == 0.0f ? 0.0f : v * p;
+    const float d = exp_f32(-0.5f * vc * vc) * 0.398942280f;
+    *dact = __builtin_fmaf(vc, d, p);
+    return vlo * p;
+  } else {
+    const float c2 = 1.59576912f;  // 2 sqrt(2 / pi)
+    const float t = ACT == ACT_SILU ? v : c2 * __builtin_fmaf(0.044715f * v * v, v, v);
+    const float e = exp_f32(-fabsf(t));
+    // 1 / (1 + e): the hardware's reciprocal and one Newton step
+    const float d = 1.0f + e;
+    const float r0 = __builtin_amdgcn_rcpf(d);
+    const float r = __builtin_fmaf(__builtin_fmaf(-d, r0, 1.0f), r0, r0);
+    const float lo = e * r;
+    const float p = t >= 0.0f ? r : (t < 0.0f ? lo : t);  // NaN stays
+    const float vq = vc * (r * lo);
+    if constexpr (ACT == ACT_SILU) {
+      *dact = p + vq;
+    } else {
+      const float dt = c2 * __builtin_fmaf(0.134145f * vc, vc, 1.0f);
+      *dact = p + (r * lo == 0.0f ? 0.0f : vq * dt);
+    }
+    return vlo * p;
   }
-  const float c2 = 1.59576912f;  // 2 sqrt(2 / pi)
-  const float t = act == ACT_SILU ? v : c2 * __builtin_fmaf(0.044715f * v * v, v, v);
-  const float dt = act == ACT_SILU ? 1.0f : c2 * __builtin_fmaf(0.134145f * v, v, 1.0f);
-  // with e = e^-|t|: p = 1 / (1 + e) or e / (1 + e), 1 - p the other
-  const float e = exp_f32(-fabsf(t));
-  const float r = 1.0f / (1.0f + e);
-  const float lo = e * r;
-  const float p = t >= 0.0f ? r : (t < 0.0f ? lo : t);  // NaN stays
-  const float pq = r * lo;
-  const float vd = pq == 0.0f ? 0.0f : v * pq * dt;
-  *dact = p + vd;
-  return p == 0.0f ? 0.0f : v * p;
+}
+
+// f with the activation as a constant (uniform across the launch).
+template <class F> __device__ __forceinline__ void with_act(int act, F&& f) {
+  if (act == ACT_SILU) f(std::integral_constant<int, ACT_SILU>{});
+  else if (act == ACT_GELU) f(std::integral_constant<int, ACT_GELU>{});
+  else f(std::integral_constant<int, ACT_GELU_TANH>{});
 }
 
 // The 16-bit types of gradients, by their code.

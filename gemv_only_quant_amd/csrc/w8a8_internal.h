@@ -53,11 +53,13 @@ hipError_t launch_rows(const W8A8Args& a, const void* x, int x_dtype, int64_t ld
 //   wt     (K, Jp) the codes of W transposed (gated: Wg | Wu), in dy's type
 //   dt     (parts * Nr, Mp) dy sx c2 transposed (rows N .. Nr of a part unused)
 //   xt     (K, Mp) the codes of x transposed, in dy's type
+//   part   fp32 shares of dx's product or dW's, where K is split
 // with the contracted axes zero-padded to whole stages.
 struct BackwardPlan {
   int parts;
   int64_t Np, Jp, Nr, Mp;
-  size_t scal, d, wt, dt, xt, bytes;
+  size_t scal, d, wt, dt, xt, part, bytes;
+  int dx_splits, dw_splits;
 };
 BackwardPlan plan_backward(int M, int N, int K, bool gated, bool weight_grad);
 
@@ -110,7 +112,13 @@ struct TileArgs {
   void* d;             // (M, 2 Np)
   void* dt;            // (2 Nr, Mp) or NULL
   int64_t Np, Nr, Mp;
+  // plain, few tiles: K in `splits` shares, their fp32 sums in part (splits, M, N
+  // rounded up to 4), added in a fixed order by a second launch
+  float* part;
+  int splits;
 };
+// Shares of K that launch_tile_plain wants for a product of this size (1: none).
+int plain_splits(int64_t M, int64_t N, int64_t kb);
 hipError_t launch_tile_scale(const TileArgs& t, hipStream_t s);
 hipError_t launch_tile_gated(const TileArgs& t, hipStream_t s);
 hipError_t launch_tile_grad(const TileArgs& t, int dtype, hipStream_t s);

@@ -58,7 +58,7 @@ template <int EPI> struct LargeLds {
 // (a device function beside its kernel: the host pass drops a kernel whose own
 // body has matrix-core registers in inline asm)
 template <int KIND, int EPI, int DT>
-__device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m_tiles,
+__device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m_tiles, int per,
                                            u32x4_t* lds) {
   constexpr bool PAIR = EPI == EPI_GATED || EPI == EPI_GRAD;
   constexpr int MT = kLargeMT, NT = kLargeNT;
@@ -69,31 +69,32 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
   int mt, nt;
+  // EPI_PARTIAL: column tiles of every share of K in turn, `per` stages each
   tile_of((int)blockIdx.x, n_tiles, m_tiles, &mt, &nt);
+  int k0 = 0, part = 0;
+  if constexpr (EPI == EPI_PARTIAL) {
+    const int each = (g.N + kLargeTile - 1) / kLargeTile;
+    part = nt / each;
+    k0 = part * per;
+    nt %= each;
+  }
   const int m0 = mt * kLargeTile, nw = nt * 2 * CPW;  // the workgroup's first row and column
   const int wm = wave >> 1, wn = wave & 1;
-  const int kb = g.kb, nst = (kb + kLargeStage - 1) / kLargeStage;
+  const int kb = g.kb;
+  const int all = (kb + kLargeStage - 1) / kLargeStage;
+  const int nst = EPI == EPI_PARTIAL ? min(per, all - k0) : all;
+  k0 *= kLargeStage;
   const int kb16 = (kb + 15) & ~15;
   const int lda = (int)g.lda, ldb = (int)g.ldb;
 
-  // One buffer per 16 rows of either operand that this wave moves (64 of each),
-  // from a stage's first byte to the end of the last row: the lanes' offsets are
-  // then the same few registers for all of them.
-  struct Rows {
-    const char* base;
-    int range;  // bytes, 0 where no row exists
-  };
+  // One buffer per 16 rows of either operand that this wave moves (64 of each):
+  // the lanes' offsets are then the same few registers for all of them.
   auto rows_of = [&](const void* p, int64_t ld, int first, int limit) {
     const int n = min(16, limit - first);
-    Rows r;
-    r.base = static_cast<const char*>(p) + (int64_t)(n > 0 ? first : 0) * ld;
-    r.range = n > 0 ? (int)((n - 1) * ld) + kb16 : 0;
-    return r;
+    return make_buf(static_cast<const char*>(p) + (int64_t)(n > 0 ? first : 0) * ld,
+                    n > 0 ? (uint32_t)((n - 1) * (int)ld + kb16) : 0u);
   };
-  auto at_stage = [&](const Rows& r, int st) {
-    return make_buf(r.base + st * kLargeStage, r.range > 0 ? (uint32_t)(r.range - st * kLargeStage) : 0u);
-  };
-  Rows ra[4], rb[4];
+  buf_t ra[4], rb[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     ra[i] = rows_of(g.a, g.lda, m0 + 64 * wave + 16 * i, g.M);
@@ -110,15 +111,22 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int chunk = 16 * ((lane & 7) ^ ((4 * c + (lane >> 4)) & 7));
-    ao[c] = (8 * c + (lane >> 3)) * lda + chunk;
-    bo[c] = (8 * c + (lane >> 3)) * ldb + chunk;
+    ao[c] = (8 * c + (lane >> 3)) * lda + chunk + k0;
+    bo[c] = (8 * c + (lane >> 3)) * ldb + chunk + k0;
   }
-  // load j (0 .. 15) of this wave's share of stage st
+  // load j (0 .. 15) of this wave's share of stage st, whose lanes' offsets
+  // stand in ao and bo; next_stage moves them on, past the last stage not at all
+  // (it is read again, unused)
   auto load = [&](int j, int st) {
     u32x4_t* to = lds + (2 * (st & 1) + j / 8) * OPERAND + (8 * wave + j % 8) * 64;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        at_stage(j < 8 ? ra[j / 2] : rb[j % 8 / 2], min(st, nst - 1)),  // past the end: unused
-        (__attribute__((address_space(3))) void*)to, 16, j < 8 ? ao[j % 2] : bo[j % 2], 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(j < 8 ? ra[j / 2] : rb[j % 8 / 2],
+                                             (__attribute__((address_space(3))) void*)to, 16,
+                                             j < 8 ? ao[j % 2] : bo[j % 2], 0, 0, 0);
+  };
+  auto next_stage = [&](int st) {
+    const int d = st < nst ? kLargeStage : 0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) ao[c] += d, bo[c] += d;
   };
   // operand i (0 .. 7 of A, 8 .. 15 of B) of k step k of stage st
   const int swz = (l16 >> 1) & 7;
@@ -156,6 +164,7 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   __builtin_amdgcn_s_waitcnt(kWaitMem);
   __syncthreads();
   if (nst == 1) clear_last(0);
+  next_stage(1);
 #pragma unroll
   for (int j = 0; j < 16; ++j) load(j, 1);
 #pragma unroll
@@ -187,6 +196,7 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
         __builtin_amdgcn_s_waitcnt(kWaitMem);
         __syncthreads();
         if (st + 2 == nst) clear_last(st + 1);
+        next_stage(st + 2);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -206,9 +216,11 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
 
   uint32_t* t0 = reinterpret_cast<uint32_t*>(lds) + wave * EPI_WORDS;
   const int mw = m0 + 128 * wm, rw = 128 * wm;  // the wave's first row; in the tile
+  TileArgs ge = g;
+  if constexpr (EPI == EPI_PARTIAL) ge.y = static_cast<float*>(g.y) + part * ((int64_t)g.M * g.ldy);
   Epilogue<KIND, EPI, NT, DT> epi;
-  epi.init(g, nw + wn * CPW, lane);
-  epi.fetch(g, mw);
+  epi.init(ge, nw + wn * CPW, lane);
+  epi.fetch(ge, mw);
   constexpr int G = kLargeEpiTiles;
 #pragma unroll
   for (int h = 0; h < MT / G; ++h) {
@@ -218,18 +230,19 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
 #pragma unroll 1
     for (int i = 0; i < G; ++i) {
       const int r = 16 * (h * G + i);
-      epi.tile(g, t0 + i * epi_words(NT), sa + rw + r, t0 + G * epi_words(NT), mw + r, mw + r + 16);
+      epi.tile(ge, t0 + i * epi_words(NT), sa + rw + r, t0 + G * epi_words(NT), mw + r, mw + r + 16);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 }
 
 template <int KIND, int EPI, int DT>
-__global__ __launch_bounds__(256, 1) void large_kernel(TileArgs g, int n_tiles, int m_tiles) {
+__global__ __launch_bounds__(256, 1) void large_kernel(TileArgs g, int n_tiles, int m_tiles,
+                                                       int per) {
   // one array for everything: with a second one in LDS the compiler waits for
   // all memory before LDS reads in the K loop
   __shared__ u32x4_t lds[LargeLds<EPI>::WORDS16];
-  large_body<KIND, EPI, DT>(g, n_tiles, m_tiles, lds);
+  large_body<KIND, EPI, DT>(g, n_tiles, m_tiles, per, lds);
 }
 
 // ---------------------------------------------------------------- host side
@@ -238,10 +251,16 @@ static hipError_t launch(const TileArgs& t, hipStream_t s) {
   constexpr int cols = EPI == EPI_GATED || EPI == EPI_GRAD ? kLargeTile / 2 : kLargeTile;
   const int64_t n = EPI == EPI_GRAD ? t.Np : t.N;
   const int64_t m = EPI == EPI_GRAD && t.dt != nullptr ? t.Mp : t.M;
-  const int64_t n_tiles = (n + cols - 1) / cols, m_tiles = (m + kLargeTile - 1) / kLargeTile;
+  int64_t n_tiles = (n + cols - 1) / cols;
+  const int64_t m_tiles = (m + kLargeTile - 1) / kLargeTile;
+  int per = 0;
+  if constexpr (EPI == EPI_PARTIAL) {
+    per = (t.kb / kLargeStage + t.splits - 1) / t.splits;
+    n_tiles *= t.splits;
+  }
   if (n_tiles * m_tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
   return launch_kernel(large_kernel<KIND, EPI, DT>, dim3((unsigned)(n_tiles * m_tiles)), dim3(256), s,
-                       t, (int)n_tiles, (int)m_tiles);
+                       t, (int)n_tiles, (int)m_tiles, per);
 }
 
 hipError_t launch_large_scale(const TileArgs& t, hipStream_t s) {
@@ -253,7 +272,50 @@ hipError_t launch_large_gated(const TileArgs& t, hipStream_t s) {
 hipError_t launch_large_grad(const TileArgs& t, int dtype, hipStream_t s) {
   return dtype == XF16 ? launch<kTypeI8, EPI_GRAD, XF16>(t, s) : launch<kTypeI8, EPI_GRAD, XBF16>(t, s);
 }
+
+// y = (sum of the partial products) *scal, rounded once; 4 columns per thread.
+template <int DT>
+__global__ __launch_bounds__(256) void sum_partials_kernel(TileArgs t, int blocks_per_row) {
+  typedef typename Half16<DT>::type T;
+  const int m = (int)(blockIdx.x / (unsigned)blocks_per_row);
+  const int n = ((int)(blockIdx.x % (unsigned)blocks_per_row) * 256 + (int)threadIdx.x) * 4;
+  const bool second = m >= t.M2;
+  const int mo = second ? m - t.M2 : m;
+  if (n >= t.N || mo >= t.Mv) return;
+  const int64_t ld = round_up(t.N, 4), at = (int64_t)m * ld + n;
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < t.splits; ++s)
+    v += *reinterpret_cast<const f32x4_t*>(t.part + s * (int64_t)t.M * ld + at);
+  const float k = *t.scal;
+  T* y = static_cast<T*>(second ? t.y2 : t.y) + (int64_t)mo * t.ldy + n;
+  const float o[4] = {v[0] * k, v[1] * k, v[2] * k, v[3] * k};
+  store4(y, o, min(4, t.N - n), vec4_ok(second ? t.y2 : t.y, t.ldy, 2));
+}
+
+int plain_splits(int64_t M, int64_t N, int64_t kb) {
+  const int64_t tiles = ((M + kLargeTile - 1) / kLargeTile) * ((N + kLargeTile - 1) / kLargeTile);
+  // shares of K that fill the CUs, none of them under 16 stages (1024 values)
+  int64_t s = 256 / tiles;
+  s = s < kb / kLargeStage / 16 ? s : kb / kLargeStage / 16;
+  if (s < 2) return 1;
+  // the same number of stages in all but the last, which is not empty
+  const int64_t per = (kb / kLargeStage + s - 1) / s;
+  return (int)((kb / kLargeStage + per - 1) / per);
+}
+
 hipError_t launch_large_plain(const TileArgs& t, int dtype, hipStream_t s) {
+  if (t.splits > 1) {
+    TileArgs p = t;
+    p.y = t.part;
+    p.ldy = round_up(t.N, 4);
+    p.y_dtype = YF32;
+    hipError_t e = dtype == XF16 ? launch<XF16, EPI_PARTIAL, XF16>(p, s) : launch<XBF16, EPI_PARTIAL, XBF16>(p, s);
+    if (e != hipSuccess) return e;
+    const int bpr = (t.N + 1023) / 1024;
+    const dim3 grid((unsigned)((int64_t)t.M * bpr));
+    return dtype == XF16 ? launch_kernel(sum_partials_kernel<XF16>, grid, dim3(256), s, t, bpr)
+                         : launch_kernel(sum_partials_kernel<XBF16>, grid, dim3(256), s, t, bpr);
+  }
   return dtype == XF16 ? launch<XF16, EPI_PLAIN, XF16>(t, s) : launch<XBF16, EPI_PLAIN, XBF16>(t, s);
 }
 

@@ -169,8 +169,11 @@ __global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(
     const float sa = scale[lane];
     float r = (float)s0 * (sa * __builtin_bit_cast(float, (uint32_t)s[0]));
     if constexpr (GATED) {
-      float d;
-      r = act_parts(act, r, &d) * ((float)s1 * (sa * __builtin_bit_cast(float, (uint32_t)s[P - 1])));
+      const float u = (float)s1 * (sa * __builtin_bit_cast(float, (uint32_t)s[P - 1]));
+      with_act(act, [&](auto a) {
+        float d;
+        r = act_parts<decltype(a)::value>(r, &d) * u;
+      });
     }
     with_y(y, ydt, [&](auto* yt) {
       typedef typename std::remove_pointer<decltype(yt)>::type Y;

@@ -134,11 +134,15 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(TileArgs g) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         v[j] = (float)c[j] * (a * sc[j]);
-        if constexpr (GATED) {
-          float d;
-          v[j] = act_parts(g.act, v[j], &d) * ((float)c[COLS + j] * (a * sc[COLS + j]));
-        }
       }
+      if constexpr (GATED)
+        with_act(g.act, [&](auto act) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float d;
+            v[j] = act_parts<decltype(act)::value>(v[j], &d) * ((float)c[COLS + j] * (a * sc[COLS + j]));
+          }
+        });
       store4(yt + (int64_t)m * g.ldy + n, v, nn, vec);
     }
   });

@@ -7,7 +7,7 @@
 
 namespace qmm {
 
-enum { EPI_SCALE = 0, EPI_GATED = 1, EPI_GRAD = 2, EPI_PLAIN = 3 };
+enum { EPI_SCALE = 0, EPI_GATED = 1, EPI_GRAD = 2, EPI_PLAIN = 3, EPI_PARTIAL = 4 };
 
 // KIND: kTypeI8, XF16 or XBF16
 template <int KIND> struct Acc { typedef f32x4_t type; };
@@ -98,7 +98,7 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
     col = 4 * (lane % LPR), n = n0 + col, nn = min(4, g.N - n);
     if constexpr (EPI == EPI_PLAIN) {
       k1 = *g.scal;
-    } else {
+    } else if constexpr (EPI != EPI_PARTIAL) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         s0[j] = j < nn ? g.sb[0][n + j] : 0.f;
@@ -137,7 +137,15 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
   // scales; tt: the wave's transposed tile (GRAD); m1: the next tile's first row.
   __device__ __forceinline__ void tile(const TileArgs& g, const uint32_t* t0, const float* sa,
                                        uint32_t* ttw, int m0, int m1) {
-    if constexpr (EPI == EPI_SCALE || EPI == EPI_PLAIN || EPI == EPI_GATED) {
+    if constexpr (EPI == EPI_PARTIAL) {
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int row = RPP * p + lane / LPR, m = m0 + row;
+        const acc_t c = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, col));
+        // rows of whole 4 columns: ldy is a multiple of 4 and reaches past N
+        if (m < g.M && nn > 0) *reinterpret_cast<acc_t*>(static_cast<float*>(g.y) + (int64_t)m * g.ldy + n) = c;
+      }
+    } else if constexpr (EPI == EPI_SCALE || EPI == EPI_PLAIN || EPI == EPI_GATED) {
       float v[PASSES][4];
 #pragma unroll
       for (int p = 0; p < PASSES; ++p) {
@@ -153,11 +161,14 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
         } else {
           const acc_t u = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, COLS + col));
           const float a = sa[row];
+          with_act(g.act, [&](auto act) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float d;
-            v[p][j] = act_parts(g.act, (float)c[j] * (a * s0[j]), &d) * ((float)u[j] * (a * s1[j]));
-          }
+            for (int j = 0; j < 4; ++j) {
+              float d;
+              v[p][j] = act_parts<decltype(act)::value>((float)c[j] * (a * s0[j]), &d) *
+                        ((float)u[j] * (a * s1[j]));
+            }
+          });
         }
       }
       with_y(g.y, g.y_dtype, [&](auto* yt) {
@@ -189,38 +200,35 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
 #pragma unroll
         for (int j = 0; j < 4; ++j) e[p][j] = (float)__builtin_bit_cast(T, (uint16_t)dh[p][j]);
       fetch(g, m1);
+      with_act(g.act, [&](auto act) {
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        const int row = RPP * p + lane / LPR, m = m0 + row;
-        const acc_t cg = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, col));
-        const acc_t cu = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, COLS + col));
-        const float a = sa[row];  // 0 for rows past M
-        T4 dgv = {}, duv = {};
-        T tg[4] = {}, tu[4] = {};
+        for (int p = 0; p < PASSES; ++p) {
+          const int row = RPP * p + lane / LPR, m = m0 + row;
+          const acc_t cg = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, col));
+          const acc_t cu = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, COLS + col));
+          const float a = sa[row];  // 0 for rows past M
+          const float ak = a * k2;
+          T4 dgv, duv;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float gv = (float)cg[j] * (a * s0[j]), uv = (float)cu[j] * (a * s1[j]);
-          float da;
-          const float h = act_parts(g.act, gv, &da);
-          // columns past N only pad; a row's scale may be NaN, so not by a product
-          const float dg = j < nn ? e[p][j] * uv * da : 0.f, du = j < nn ? e[p][j] * h : 0.f;
-          dgv[j] = (T)(dg * (s0[j] * k1));
-          duv[j] = (T)(du * (s1[j] * k1));
-          tg[j] = (T)(dg * (a * k2));
-          tu[j] = (T)(du * (a * k2));
-          if (j >= nn) tg[j] = tu[j] = dgv[j] = duv[j] = (T)0.f;
+          for (int j = 0; j < 4; ++j) {
+            const float gv = (float)cg[j] * (a * s0[j]), uv = (float)cu[j] * (a * s1[j]);
+            float da;
+            const float h = act_parts<decltype(act)::value>(gv, &da);
+            const float dg = e[p][j] * uv * da, du = e[p][j] * h;
+            // columns past N only pad: zeros, whatever the row's scale is
+            const bool ok = j < nn;
+            dgv[j] = (T)(ok ? dg * (s0[j] * k1) : 0.f);
+            duv[j] = (T)(ok ? du * (s1[j] * k1) : 0.f);
+            tt[(col + j) * LDH + row] = (T)(ok ? dg * ak : 0.f);
+            tt[(COLS + col + j) * LDH + row] = (T)(ok ? du * ak : 0.f);
+          }
+          if (m < g.M && n < g.Np) {  // n is a multiple of 4 and Np of 128
+            T* o = dd + (int64_t)m * (2 * g.Np) + n;
+            *reinterpret_cast<T4*>(o) = dgv;
+            *reinterpret_cast<T4*>(o + g.Np) = duv;
+          }
         }
-        if (m < g.M && n < g.Np) {  // n is a multiple of 4 and Np of 128
-          T* o = dd + (int64_t)m * (2 * g.Np) + n;
-          *reinterpret_cast<T4*>(o) = dgv;
-          *reinterpret_cast<T4*>(o + g.Np) = duv;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          tt[(col + j) * LDH + row] = tg[j];
-          tt[(COLS + col + j) * LDH + row] = tu[j];
-        }
-      }
+      });
       if (g.dt != nullptr && m0 < g.Mp) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         T* dt = static_cast<T*>(g.dt);
@@ -242,7 +250,7 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
 // The workgroup's row scales to LDS (0 for rows past M).
 template <int EPI>
 __device__ __forceinline__ void row_scales(const TileArgs& g, float* sa, int m0, int rows) {
-  if constexpr (EPI != EPI_PLAIN)
+  if constexpr (EPI != EPI_PLAIN && EPI != EPI_PARTIAL)
     for (int i = threadIdx.x; i < rows; i += 256) sa[i] = m0 + i < g.M ? g.sa[m0 + i] : 0.f;
 }
 

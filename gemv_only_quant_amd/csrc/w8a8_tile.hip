@@ -139,9 +139,9 @@ static hipError_t launch_tile(const TileArgs& t, hipStream_t s) {
 // tiles, 66 / 90; 333 x 1008 x 2777, 22 tiles, 28 / 18).
 static bool many_rows(const TileArgs& t, int cols) {
   static const int want = env_int("QMM_TILE_LARGE");
-  if (want >= 0) return want > 0;
+  if (want >= 0 && t.splits <= 1) return want > 0;
   const int64_t tiles = (((int64_t)t.M + 255) / 256) * (((int64_t)t.N + cols - 1) / cols);
-  return tiles >= 64;
+  return t.splits > 1 || tiles >= 64;
 }
 
 hipError_t launch_tile_scale(const TileArgs& t, hipStream_t s) {
