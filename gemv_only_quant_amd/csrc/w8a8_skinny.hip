@@ -1,27 +1,46 @@
 // w8a8_skinny.hip -- int8 x int8 products of a decode batch (5 to 64 tokens,
 // plain and gated) on v_mfma_i32_16x16x64_i8: bound by reading the weights.
 //
-// A workgroup of 8 waves owns all tokens (MT 16-row tiles) and NT strips of 16
-// columns; its waves split K in turns of 256 bytes, so that rows whose stride
-// is a power of two spread over the L2's channels, and add their whole sums in
-// LDS at the end (integers: any order gives the same).  Weights and codes go
-// from memory straight into operands, 128 bytes of each row at a time (whole
-// cache lines), two such items in flight; the codes are read again by every
-// workgroup, from L2, NT strips per reading.  No barrier before the end.
+// A workgroup owns all tokens (MT 16-row tiles) and NT strips of 16 columns; its
+// waves split K in turns of 256 bytes, so that rows whose stride is a power of two
+// spread over the L2's channels, and add their whole sums in LDS at the end
+// (integers: any order gives the same).  A wave's weights and codes come in items
+// of 128 bytes of every row, by loads straight to its own part of LDS, D items in
+// flight, and are read from there as operands: no barrier before the end.
+//   Why through LDS: operands as the matrix cores want them have neighbouring
+// lanes in different rows, and the address units then take a load's 64 lanes one
+// by one (64 rows x 4096 x 14336: 22.8 us, bound by that); 8 lanes on a 128-byte
+// line take a quarter of the time.
 #include <type_traits>
 
 #include "w8a8_tile.h"
 
 namespace qmm {
 
-constexpr int kSkinnyWaves = 8;
+// LDS of a workgroup: the waves' rings; in their place at the end the sums; then
+// the scales of the tokens and of the strips' columns.
+constexpr int kSkinnyLds = 144 << 10;
+constexpr int kSkinnyWaves = 4;
+template <int MT, int NT> struct SkinnyPlan {
+  static constexpr int WV = kSkinnyWaves;
+  static constexpr int ITEM = (MT + NT) * 2048;  // bytes
+  static constexpr int FIT = kSkinnyLds / (WV * ITEM);
+  static constexpr int D = FIT < 2 ? 2 : (FIT > 4 ? 4 : FIT);
+  static constexpr int LD = 16 * NT + 4;  // row of the sums
+  static constexpr int RING = WV * D * ITEM, SUMS = 16 * MT * LD * 4;
+  static constexpr int BYTES = (RING > SUMS ? RING : SUMS) + (16 * MT + 16 * NT) * 4;
+  static_assert(BYTES <= 160 << 10, "LDS of a CU");
+};
 
+// (a device function beside its kernel: the host pass drops a kernel whose own
+// body has loads straight to LDS)
 template <int MT, int NT, bool GATED>
-__global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(TileArgs g) {
+__device__ __forceinline__ void skinny_body(const TileArgs& g, u32x4_t* lds) {
+  typedef SkinnyPlan<MT, NT> P;
   constexpr int COLS = GATED ? 8 * NT : 16 * NT;  // output columns of the workgroup
-  constexpr int LD = 16 * NT + 4;                 // row of the sums in LDS
-  __shared__ int sums[16 * MT * LD];
-  __shared__ float scales[16 * MT + 16 * NT];  // of the tokens, then of the strips' columns
+  constexpr int WV = kSkinnyWaves, LD = P::LD, D = P::D, UNITS = 2 * (MT + NT);
+  int* sums = reinterpret_cast<int*>(lds);
+  float* scales = reinterpret_cast<float*>(lds) + (P::RING > P::SUMS ? P::RING : P::SUMS) / 4;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
@@ -35,64 +54,50 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(TileArgs g) {
     return make_buf(static_cast<const char*>(p) + (int64_t)(n > 0 ? first : 0) * ld,
                     n > 0 ? (uint32_t)((n - 1) * (int)ld + kb16) : 0u);
   };
-  buf_t ar[MT], br[NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) ar[i] = rows_of(g.a, g.lda, 16 * i, g.M);
+  buf_t rows[MT + NT];
 #pragma unroll
   for (int s = 0; s < NT; ++s)
-    br[s] = GATED ? rows_of(g.b[s / (NT / 2)], g.ldb, n0 + 16 * (s % (NT / 2)), g.N)
-                  : rows_of(g.b[0], g.ldb, n0 + 16 * s, g.N);
-  // whole 128-byte lines of 8 rows per load (line_operands)
-  const int ao = (l16 & 7) * lda + 16 * (quad + 4 * (l16 >> 3));
-  const int bo = (l16 & 7) * ldb + 16 * (quad + 4 * (l16 >> 3));
+    rows[s] = GATED ? rows_of(g.b[s / (NT / 2)], g.ldb, n0 + 16 * (s % (NT / 2)), g.N)
+                    : rows_of(g.b[0], g.ldb, n0 + 16 * s, g.N);
+#pragma unroll
+  for (int i = 0; i < MT; ++i) rows[NT + i] = rows_of(g.a, g.lda, 16 * i, g.M);
 
-  // item i of this wave: 128 bytes of K from byte k_of(i) on; past the end its
-  // offset lies outside every buffer, which reads zeros and no memory
-  struct Item {
-    u32x4_t a[MT][2], b[NT][2];
-  };
-  auto k_of = [&](int i) { return (wave + kSkinnyWaves * (i >> 1)) * 256 + 128 * (i & 1); };
-  auto load = [&](int i, Item& it) {
+  // Item i of this wave: 128 bytes of K from byte k_of(i) on.  A load (1 KiB) is 8
+  // rows of a strip; chunk c of row r lies at slot 8 r + (c ^ (r / 2 % 8)), so lane
+  // p of the strip's half h fetches chunk (p % 8) ^ (r / 2 % 8) of row r = 8 h + p /
+  // 8.  Past the end the offset lies outside every buffer: nothing is read.
+  auto k_of = [&](int i) { return (wave + WV * (i >> 1)) * 256 + 128 * (i & 1); };
+  int ao[2], bo[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int chunk = 16 * ((lane & 7) ^ ((4 * h + (lane >> 4)) & 7));
+    ao[h] = (8 * h + (lane >> 3)) * lda + chunk;
+    bo[h] = (8 * h + (lane >> 3)) * ldb + chunk;
+  }
+  u32x4_t* ring = lds + wave * (P::RING / WV / 16);
+  auto load = [&](int i, int slot) {
     const int k = k_of(i), at = k < kb ? k : 0x60000000;
-    const int av = ao + at, bv = bo + at;
+    auto to = [&](int u) {
+      return (__attribute__((address_space(3))) void*)(ring + slot * (P::ITEM / 16) + 64 * u);
+    };
 #pragma unroll
-    for (int s = 0; s < NT; ++s)
+    for (int u = 0; u < 2 * NT; ++u)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rows[u / 2], to(u), 16, bo[u % 2] + at, 0, 0, kStream);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) it.b[s][j] = buf_load128_stream(br[s], bv + 8 * j * ldb);
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) it.a[t][j] = buf_load128(ar[t], av + 8 * j * lda);
+    for (int u = 2 * NT; u < UNITS; ++u)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rows[u / 2], to(u), 16, ao[u % 2] + at, 0, 0, 0);
+  };
+  // operand j (k step) of strip s of the item in `slot`
+  const int swz = (l16 >> 1) & 7;
+  auto frag = [&](int s, int j, int slot) {
+    return ring[slot * (P::ITEM / 16) + 128 * s + 8 * l16 + ((4 * j + quad) ^ swz)];
   };
   i32x4_t acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int s = 0; s < NT; ++s) acc[i][s] = i32x4_t{0, 0, 0, 0};
-  auto use = [&](int i, Item& it) {
-    const int k = k_of(i);
-#pragma unroll
-    for (int s = 0; s < NT; ++s) line_operands(it.b[s]);
-#pragma unroll
-    for (int t = 0; t < MT; ++t) line_operands(it.a[t]);
-    if (k + 128 > kb) {  // the codes' bytes past K (whatever B holds there meets zeros)
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) it.a[t][j] = clear_tail(it.a[t][j], k + 64 * j + 16 * quad, kb);
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int s = 0; s < NT; ++s) acc[t][s] = mfma_t<kTypeI8>(it.a[t][j], it.b[s][j], acc[t][s]);
-  };
 
-  Item x, y;
-  load(0, x);
-  load(1, y);
-  for (int i = threadIdx.x; i < 16 * MT * LD; i += 64 * kSkinnyWaves) sums[i] = 0;
   {
     const int i = threadIdx.x;
     if (i < 16 * MT) scales[i] = i < g.M ? g.sa[i] : 0.f;
@@ -101,13 +106,52 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(TileArgs g) {
       scales[i] = n < g.N ? g.sb[GATED ? c / COLS : 0][n] : 0.f;
     }
   }
-  __syncthreads();
-  for (int i = 0; k_of(i) < kb; i += 2) {
-    use(i, x);
-    load(i + 2, x);
-    use(i + 1, y);
-    load(i + 3, y);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, d);
+
+  // vmcnt(N) with the other counters at maximum
+  constexpr int LEFT = (D - 1) * UNITS;
+  static_assert(LEFT < 64, "loads in flight");
+  constexpr int kWaitItem = (LEFT & 15) | ((LEFT >> 4) << 14) | 0x0F70;
+  for (int i = 0; k_of(i) < kb; i += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      // (items past the end are read and multiplied as zeros: their operands of
+      // A are cleared below)
+      const int k = k_of(i + d);
+      __builtin_amdgcn_s_waitcnt(kWaitItem);
+      __builtin_amdgcn_sched_barrier(0);
+      u32x4_t a[MT][2], b[NT][2];
+#pragma unroll
+      for (int s = 0; s < NT; ++s)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) b[s][j] = frag(s, j, d);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) a[t][j] = frag(NT + t, j, d);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot is free
+      __builtin_amdgcn_sched_barrier(0);
+      load(i + d + D, d);
+      if (k + 128 > kb) {  // the codes' bytes past K (whatever B holds there meets zeros)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) a[t][j] = clear_tail(a[t][j], k + 64 * j + 16 * quad, kb);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int s = 0; s < NT; ++s) acc[t][s] = mfma_t<kTypeI8>(a[t][j], b[s][j], acc[t][s]);
+    }
   }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load may land in the sums
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * MT * LD; i += 64 * WV) sums[i] = 0;
+  __syncthreads();
 #pragma unroll
   for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -123,7 +167,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(TileArgs g) {
   with_y(g.y, g.y_dtype, [&](auto* yt) {
     typedef typename std::remove_pointer<decltype(yt)>::type Y;
     const bool vec = vec4_ok(yt, g.ldy, (int)sizeof(Y));
-    for (int i = threadIdx.x; i < 16 * MT * PER_ROW; i += 64 * kSkinnyWaves) {
+    for (int i = threadIdx.x; i < 16 * MT * PER_ROW; i += 64 * WV) {
       const int m = i / PER_ROW, col = 4 * (i % PER_ROW), n = n0 + col;
       const int nn = min(4, g.N - n);
       if (m >= g.M || nn <= 0) continue;
@@ -148,6 +192,14 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(TileArgs g) {
   });
 }
 
+template <int MT, int NT, bool GATED>
+__global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(TileArgs g) {
+  // one array for everything: with a second one in LDS the compiler waits for
+  // all memory before it reads any
+  __shared__ u32x4_t lds[(SkinnyPlan<MT, NT>::BYTES + 15) / 16];
+  skinny_body<MT, NT, GATED>(g, lds);
+}
+
 // ---------------------------------------------------------------- host side
 bool skinny_fits(int M) { return M <= 64; }
 
@@ -158,17 +210,16 @@ static hipError_t launch_skinny_k(const TileArgs& t, hipStream_t s) {
                        dim3(64 * kSkinnyWaves), s, t);
 }
 
+// Strips per workgroup: 4 share each reading of the codes where that leaves at
+// least 192 workgroups (codes, us, 4 / 2 / 1 strips: 64 rows x 4096 x 14336 17.9 /
+// 24.5 / 34.2; 16 rows 14.9 / 16.8 / 17.0), else 2 with more than 16 rows, 1 with
+// up to 16 (8 x 8192 x 8192 18.9 / 16.5 / 14.0, 16 x 14336 x 1024 24.5 / 15.1 / 10.9)
+// or where 2 leave too few.  A pair of products has at least one strip of each.
 template <int MT, bool GATED>
 static hipError_t launch_skinny_m(const TileArgs& t, hipStream_t s) {
-  // strips per workgroup: more share each reading of the codes, fewer make
-  // more workgroups
-  static const int want = env_int("QMM_SKINNY8_NT");
   constexpr int W = GATED ? 8 : 16;
-  int nt = 4;
-  while (nt > (GATED ? 2 : 1) && t.N / (W * nt) < 192) nt /= 2;
-  if (want > 0) nt = want;
-  if (nt == 4) return launch_skinny_k<MT, 4, GATED>(t, s);
-  if (nt == 2 || GATED) return launch_skinny_k<MT, 2, GATED>(t, s);
+  if (t.N / (4 * W) >= 192) return launch_skinny_k<MT, 4, GATED>(t, s);
+  if (GATED || (MT > 1 && t.N / (2 * W) >= 192)) return launch_skinny_k<MT, 2, GATED>(t, s);
   if constexpr (!GATED) return launch_skinny_k<MT, 1, GATED>(t, s);
   return hipErrorInvalidValue;
 }
