@@ -28,7 +28,7 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
           "-mllvm", "-amdgpu-kernarg-preload-count=16"]
 SOURCES = ["qmm_api.cpp", "gemv_lowbit.hip", "gemv_tile.hip", "gemv_int8.hip", "repack.hip",
            "gemm_mfma.hip", "gemm_large.hip", "gemm_medium.hip", "ternary.hip", "ternary_large.hip",
-           "quantize.hip", "w8a8_api.cpp", "w8a8_quantize.hip", "w8a8_rows.hip", "w8a8_skinny.hip", "w8a8_tile.hip",
+           "quantize.hip", "w8a8_api.cpp", "w8a8_quantize.hip", "w8a8_rows.hip", "w8a8_skinny.hip",
            "w8a8_large.hip", "w8a8_backward.hip"]
 
 

@@ -126,10 +126,4 @@ hipError_t launch_tile_plain(const TileArgs& t, int dtype, hipStream_t s);
 // A decode batch (w8a8_skinny.hip).
 bool skinny_fits(int M);
 hipError_t launch_skinny(const TileArgs& t, bool gated, hipStream_t s);
-// The same with 256-row tiles (w8a8_large.hip).
-hipError_t launch_large_scale(const TileArgs& t, hipStream_t s);
-hipError_t launch_large_gated(const TileArgs& t, hipStream_t s);
-hipError_t launch_large_grad(const TileArgs& t, int dtype, hipStream_t s);
-hipError_t launch_large_plain(const TileArgs& t, int dtype, hipStream_t s);
-
 }  // namespace qmm

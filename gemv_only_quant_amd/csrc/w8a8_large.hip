@@ -1,5 +1,18 @@
-// w8a8_large.hip -- the products of w8a8_tile.hip for many rows: 256 x 256
-// tiles, bound by the matrix cores.
+// w8a8_large.hip -- C = A B^t on the matrix cores for more rows than a decode batch:
+// int8 codes (v_mfma_i32_16x16x64_i8, exact sums) and the 16-bit operands of
+// gradients (v_mfma_f32_16x16x32_{f16,bf16}).  Both operands have the contracted
+// axis contiguous, and one 16-byte chunk per lane is one operand of either kind of
+// MFMA (16 int8 or 8 16-bit values), so one kernel moves bytes and only the
+// instruction differs.  Epilogues (w8a8_tile.h):
+//   SCALE    y = C sa[m] sb[n]
+//   GATED    h = act(g) u for two products g, u of the same left operand
+//   GRAD     dg = dh u act'(g), du = dh act(g), left as 16-bit operands of the
+//            gradients' products, once row-major and once transposed
+//   PLAIN    y = C * (a power of two), 16-bit
+//   PARTIAL  fp32 sums of a share of the contraction, added by a second launch
+//
+// Tiles of 256 x 256 (W = 8), bound by the matrix cores, as described here; 128 x
+// 128 (W = 4, two workgroups per CU) where the former are too few.
 //
 //  * one workgroup per CU, 4 waves as 2 x 2; a wave owns 128 rows x 128 columns
 //    = 8 x 8 MFMA tiles, 256 accumulators per lane pinned to the matrix-core
@@ -24,10 +37,9 @@
 
 namespace qmm {
 
-constexpr int kLargeMT = 8, kLargeNT = 8;  // 16 x 16 tiles of a wave
-constexpr int kLargeTile = 256;            // rows and columns of B of a workgroup
-constexpr int kLargeStage = 128;           // contracted bytes per stage
-constexpr int kLargeEpiTiles = 4;          // row tiles of a wave in the epilogue's LDS at once
+// W: 16 x 16 tiles of a wave in each direction; a workgroup's tile is 32 W rows
+// and columns of B
+constexpr int kLargeStage = 128;  // contracted bytes per stage
 static constexpr int kWaitMem = 0x0070;    // s_waitcnt vmcnt(0) lgkmcnt(0)
 
 // MFMA with its accumulator pinned to the AGPRs (left to itself the register
@@ -46,24 +58,25 @@ __device__ __forceinline__ void mfma_pinned(typename Acc<KIND>::type& c, const u
 // LDS of a workgroup in 16-byte words: two stages of both operands, and in
 // their place later the epilogue's tiles (4 waves of as many words each); then
 // the row scales.
-template <int EPI> struct LargeLds {
-  static constexpr int EPI_WORDS =
-      kLargeEpiTiles * epi_words(kLargeNT) + (EPI == EPI_GRAD ? epi_t_words(kLargeNT) : 0);
-  static constexpr int OPERAND = kLargeTile * kLargeStage / 16;  // one operand of a stage
+template <int EPI, int W> struct LargeLds {
+  static constexpr int G = EPI == EPI_GRAD ? 2 : 4;  // row tiles of a wave in LDS at once
+  static constexpr int EPI_WORDS = G * epi_words(W) + (EPI == EPI_GRAD ? epi_t_words(W) : 0);
+  static constexpr int OPERAND = 32 * W * kLargeStage / 16;  // one operand of a stage
   static constexpr int STAGES = 4 * OPERAND;
   static constexpr int SCALES = STAGES > EPI_WORDS ? STAGES : EPI_WORDS;
-  static constexpr int WORDS16 = SCALES + kLargeTile / 4;
+  static constexpr int WORDS16 = SCALES + 32 * W / 4;
 };
 
 // (a device function beside its kernel: the host pass drops a kernel whose own
 // body has matrix-core registers in inline asm)
-template <int KIND, int EPI, int DT>
+template <int KIND, int EPI, int W, int DT>
 __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m_tiles, int per,
                                            u32x4_t* lds) {
   constexpr bool PAIR = EPI == EPI_GATED || EPI == EPI_GRAD;
-  constexpr int MT = kLargeMT, NT = kLargeNT;
+  constexpr int MT = W, NT = W, TILE = 32 * W, HALF = 16 * W;
+  typedef LargeLds<EPI, W> L;
   constexpr int CPW = PAIR ? 8 * NT : 16 * NT;  // output columns per wave
-  constexpr int OPERAND = LargeLds<EPI>::OPERAND, EPI_WORDS = LargeLds<EPI>::EPI_WORDS;
+  constexpr int OPERAND = L::OPERAND, EPI_WORDS = L::EPI_WORDS;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -73,12 +86,12 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   tile_of((int)blockIdx.x, n_tiles, m_tiles, &mt, &nt);
   int k0 = 0, part = 0;
   if constexpr (EPI == EPI_PARTIAL) {
-    const int each = (g.N + kLargeTile - 1) / kLargeTile;
+    const int each = (g.N + TILE - 1) / TILE;
     part = nt / each;
     k0 = part * per;
     nt %= each;
   }
-  const int m0 = mt * kLargeTile, nw = nt * 2 * CPW;  // the workgroup's first row and column
+  const int m0 = mt * TILE, nw = nt * 2 * CPW;  // the workgroup's first row and column
   const int wm = wave >> 1, wn = wave & 1;
   const int kb = g.kb;
   const int all = (kb + kLargeStage - 1) / kLargeStage;
@@ -87,20 +100,21 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   const int kb16 = (kb + 15) & ~15;
   const int lda = (int)g.lda, ldb = (int)g.ldb;
 
-  // One buffer per 16 rows of either operand that this wave moves (64 of each):
+  // One buffer per 16 rows of either operand that this wave moves (8 W of each):
   // the lanes' offsets are then the same few registers for all of them.
   auto rows_of = [&](const void* p, int64_t ld, int first, int limit) {
     const int n = min(16, limit - first);
     return make_buf(static_cast<const char*>(p) + (int64_t)(n > 0 ? first : 0) * ld,
                     n > 0 ? (uint32_t)((n - 1) * (int)ld + kb16) : 0u);
   };
-  buf_t ra[4], rb[4];
+  constexpr int PIECES = W / 2;
+  buf_t ra[PIECES], rb[PIECES];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    ra[i] = rows_of(g.a, g.lda, m0 + 64 * wave + 16 * i, g.M);
-    // strip 4 wave + i of the 16: NT for each half of the workgroup's columns; of a
+  for (int i = 0; i < PIECES; ++i) {
+    ra[i] = rows_of(g.a, g.lda, m0 + 16 * (PIECES * wave + i), g.M);
+    // strip PIECES wave + i: NT for each half of the workgroup's columns; of a
     // pair of products, half of them the first's and half the second's
-    const int s = 4 * wave + i, half = s / NT, k = s % NT;
+    const int s = PIECES * wave + i, half = s / NT, k = s % NT;
     rb[i] = PAIR ? rows_of(g.b[k / (NT / 2)], g.ldb, nw + half * CPW + 16 * (k % (NT / 2)), g.N)
                  : rows_of(g.b[0], g.ldb, nw + half * CPW + 16 * k, g.N);
   }
@@ -114,29 +128,29 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
     ao[c] = (8 * c + (lane >> 3)) * lda + chunk + k0;
     bo[c] = (8 * c + (lane >> 3)) * ldb + chunk + k0;
   }
-  // load j (0 .. 15) of this wave's share of stage st, whose lanes' offsets
+  // load j (W of A, then W of B) of this wave's share of stage st, whose lanes' offsets
   // stand in ao and bo; next_stage moves them on, past the last stage not at all
   // (it is read again, unused)
   auto load = [&](int j, int st) {
-    u32x4_t* to = lds + (2 * (st & 1) + j / 8) * OPERAND + (8 * wave + j % 8) * 64;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(j < 8 ? ra[j / 2] : rb[j % 8 / 2],
+    u32x4_t* to = lds + (2 * (st & 1) + j / W) * OPERAND + (W * wave + j % W) * 64;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(j < W ? ra[j / 2] : rb[j % W / 2],
                                              (__attribute__((address_space(3))) void*)to, 16,
-                                             j < 8 ? ao[j % 2] : bo[j % 2], 0, 0, 0);
+                                             j < W ? ao[j % 2] : bo[j % 2], 0, 0, 0);
   };
   auto next_stage = [&](int st) {
     const int d = st < nst ? kLargeStage : 0;
 #pragma unroll
     for (int c = 0; c < 2; ++c) ao[c] += d, bo[c] += d;
   };
-  // operand i (0 .. 7 of A, 8 .. 15 of B) of k step k of stage st
+  // operand i (W of A, then W of B) of k step k of stage st
   const int swz = (l16 >> 1) & 7;
-  const int oa = (128 * wm + l16) * 8, ob = OPERAND + (128 * wn + l16) * 8;
+  const int oa = (HALF * wm + l16) * 8, ob = OPERAND + (HALF * wn + l16) * 8;
   auto frag = [&](int i, int k, int st) {
-    return lds[2 * (st & 1) * OPERAND + (i < 8 ? oa + 128 * i : ob + 128 * (i - 8)) + ((4 * k + quad) ^ swz)];
+    return lds[2 * (st & 1) * OPERAND + (i < W ? oa + 128 * i : ob + 128 * (i - W)) + ((4 * k + quad) ^ swz)];
   };
 
-  float* sa = reinterpret_cast<float*>(lds + LargeLds<EPI>::SCALES);
-  row_scales<EPI>(g, sa, m0, kLargeTile);
+  float* sa = reinterpret_cast<float*>(lds + L::SCALES);
+  row_scales<EPI>(g, sa, m0, TILE);
 
   typedef typename Acc<KIND>::type acc_t;
   acc_t acc[MT][NT];
@@ -151,45 +165,51 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   auto clear_last = [&](int st) {
     if (KIND != kTypeI8 || kb % kLargeStage == 0) return;
     const int at = kb % kLargeStage, r = threadIdx.x;  // a row per thread
-    for (int c = at / 16; c < 8; ++c) {
+    for (int c = r < TILE ? at / 16 : 8; c < 8; ++c) {
       u32x4_t* p = lds + 2 * (st & 1) * OPERAND + 8 * r + (c ^ ((r >> 1) & 7));
       *p = clear_tail(*p, 16 * c, at);
     }
     __syncthreads();
   };
 
-  u32x4_t f[2][16];  // operands of the two k steps
+  u32x4_t f[2][2 * W];  // operands of the two k steps
 #pragma unroll
-  for (int j = 0; j < 16; ++j) load(j, 0);
+  for (int j = 0; j < 2 * W; ++j) load(j, 0);
   __builtin_amdgcn_s_waitcnt(kWaitMem);
   __syncthreads();
   if (nst == 1) clear_last(0);
   next_stage(1);
 #pragma unroll
-  for (int j = 0; j < 16; ++j) load(j, 1);
+  for (int j = 0; j < 2 * W; ++j) load(j, 1);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) f[0][i] = frag(i, 0, 0);
+  for (int i = 0; i < 2 * W; ++i) f[0][i] = frag(i, 0, 0);
 
 #pragma unroll 1
   for (int st = 0; st < nst; ++st) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      // 16 groups of 4 MFMAs; the next k step's operands are read in the first 8,
-      // two with each, and in the second k step the loads go out
+      // groups of 4 MFMAs; the next k step's operands are read in the first half
+      // of them, in the order of their first use, and in the second k step the
+      // loads go out
+      constexpr int GROUPS = W * W / 4, READS = 2 * W, PER = 2 * READS / GROUPS;
 #pragma unroll
-      for (int t = 0; t < 16; ++t) {
-        if (t < 8) {
+      for (int t = 0; t < GROUPS; ++t) {
+        if (t < GROUPS / 2) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            // in the order of their first use: B's first half with A's first
-            const int q = 2 * t + h, i = q < 5 ? (q == 0 ? 0 : 7 + q) : (q < 9 ? 7 + q : q - 8);
+          for (int h = 0; h < PER; ++h) {
+            const int q = PER * t + h, i = q == 0 ? 0 : (q <= W ? W + q - 1 : q - W);
             f[k ^ 1][i] = frag(i, k ^ 1, st + k);
           }
         }
-        if (k == 1) load(t, st + 2);
+        if (k == 1) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-          mfma_pinned<KIND>(acc[t / 2][4 * (t % 2) + s], f[k][t / 2], f[k][8 + 4 * (t % 2) + s]);
+          for (int j = t * READS / GROUPS; j < (t + 1) * READS / GROUPS; ++j) load(j, st + 2);
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const int i = t * 4 / W, c = t * 4 % W + s;
+          mfma_pinned<KIND>(acc[i][c], f[k][i], f[k][W + c]);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
       if (k == 0) {
@@ -215,13 +235,13 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   __builtin_amdgcn_sched_barrier(0);
 
   uint32_t* t0 = reinterpret_cast<uint32_t*>(lds) + wave * EPI_WORDS;
-  const int mw = m0 + 128 * wm, rw = 128 * wm;  // the wave's first row; in the tile
+  const int mw = m0 + HALF * wm, rw = HALF * wm;  // the wave's first row; in the tile
   TileArgs ge = g;
   if constexpr (EPI == EPI_PARTIAL) ge.y = static_cast<float*>(g.y) + part * ((int64_t)g.M * g.ldy);
   Epilogue<KIND, EPI, NT, DT> epi;
   epi.init(ge, nw + wn * CPW, lane);
   epi.fetch(ge, mw);
-  constexpr int G = kLargeEpiTiles;
+  constexpr int G = L::G;
 #pragma unroll
   for (int h = 0; h < MT / G; ++h) {
 #pragma unroll
@@ -236,40 +256,66 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   }
 }
 
-template <int KIND, int EPI, int DT>
-__global__ __launch_bounds__(256, 1) void large_kernel(TileArgs g, int n_tiles, int m_tiles,
-                                                       int per) {
+template <int KIND, int EPI, int W, int DT>
+__global__ __launch_bounds__(256, W == 8 ? 1 : 2) void large_kernel(TileArgs g, int n_tiles,
+                                                                    int m_tiles, int per) {
   // one array for everything: with a second one in LDS the compiler waits for
   // all memory before LDS reads in the K loop
-  __shared__ u32x4_t lds[LargeLds<EPI>::WORDS16];
-  large_body<KIND, EPI, DT>(g, n_tiles, m_tiles, per, lds);
+  __shared__ u32x4_t lds[LargeLds<EPI, W>::WORDS16];
+  large_body<KIND, EPI, W, DT>(g, n_tiles, m_tiles, per, lds);
 }
 
 // ---------------------------------------------------------------- host side
-template <int KIND, int EPI, int DT>
-static hipError_t launch(const TileArgs& t, hipStream_t s) {
-  constexpr int cols = EPI == EPI_GATED || EPI == EPI_GRAD ? kLargeTile / 2 : kLargeTile;
-  const int64_t n = EPI == EPI_GRAD ? t.Np : t.N;
-  const int64_t m = EPI == EPI_GRAD && t.dt != nullptr ? t.Mp : t.M;
+// Tiles of a product with tiles of 32 W, in n (pairs of products: half as many
+// columns) and m.
+static int64_t tiles_of(int64_t m, int64_t n, bool pair, int w) {
+  const int64_t rows = 32 * w, cols = pair ? 16 * w : 32 * w;
+  return ((m + rows - 1) / rows) * ((n + cols - 1) / cols);
+}
+
+// Whether 256 x 256 tiles serve a product better than 128 x 128 ones, in units
+// of the time of a round of the former: of the latter a CU runs two at once,
+// 0.77 together, 0.35 where each has a CU to itself.
+static bool large_tiles(int64_t m, int64_t n, bool pair) {
+  static const int want = env_int("QMM_TILE_LARGE");
+  if (want >= 0) return want > 0;
+  const int64_t t8 = tiles_of(m, n, pair, 8), t4 = tiles_of(m, n, pair, 4);
+  const double small = t4 <= 256 ? 0.35 : 0.77 * (double)((t4 + 511) / 512);
+  return (double)((t8 + 255) / 256) <= small;
+}
+
+template <int KIND, int EPI, int W, int DT>
+static hipError_t launch_w(const TileArgs& t, int64_t m, int64_t n, hipStream_t s) {
+  constexpr int rows = 32 * W, cols = EPI == EPI_GATED || EPI == EPI_GRAD ? 16 * W : 32 * W;
   int64_t n_tiles = (n + cols - 1) / cols;
-  const int64_t m_tiles = (m + kLargeTile - 1) / kLargeTile;
+  const int64_t m_tiles = (m + rows - 1) / rows;
   int per = 0;
   if constexpr (EPI == EPI_PARTIAL) {
     per = (t.kb / kLargeStage + t.splits - 1) / t.splits;
     n_tiles *= t.splits;
   }
   if (n_tiles * m_tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
-  return launch_kernel(large_kernel<KIND, EPI, DT>, dim3((unsigned)(n_tiles * m_tiles)), dim3(256), s,
-                       t, (int)n_tiles, (int)m_tiles, per);
+  return launch_kernel(large_kernel<KIND, EPI, W, DT>, dim3((unsigned)(n_tiles * m_tiles)), dim3(256),
+                       s, t, (int)n_tiles, (int)m_tiles, per);
 }
 
-hipError_t launch_large_scale(const TileArgs& t, hipStream_t s) {
+template <int KIND, int EPI, int DT>
+static hipError_t launch(const TileArgs& t, hipStream_t s) {
+  // the gradient epilogue also writes the padding of its operands
+  const int64_t n = EPI == EPI_GRAD ? t.Np : t.N;
+  const int64_t m = EPI == EPI_GRAD && t.dt != nullptr ? t.Mp : t.M;
+  if constexpr (EPI == EPI_PARTIAL) return launch_w<KIND, EPI, 8, DT>(t, m, n, s);
+  return large_tiles(m, n, EPI == EPI_GATED || EPI == EPI_GRAD) ? launch_w<KIND, EPI, 8, DT>(t, m, n, s)
+                                                                : launch_w<KIND, EPI, 4, DT>(t, m, n, s);
+}
+
+hipError_t launch_tile_scale(const TileArgs& t, hipStream_t s) {
   return launch<kTypeI8, EPI_SCALE, XF16>(t, s);
 }
-hipError_t launch_large_gated(const TileArgs& t, hipStream_t s) {
+hipError_t launch_tile_gated(const TileArgs& t, hipStream_t s) {
   return launch<kTypeI8, EPI_GATED, XF16>(t, s);
 }
-hipError_t launch_large_grad(const TileArgs& t, int dtype, hipStream_t s) {
+hipError_t launch_tile_grad(const TileArgs& t, int dtype, hipStream_t s) {
   return dtype == XF16 ? launch<kTypeI8, EPI_GRAD, XF16>(t, s) : launch<kTypeI8, EPI_GRAD, XBF16>(t, s);
 }
 
@@ -293,7 +339,7 @@ __global__ __launch_bounds__(256) void sum_partials_kernel(TileArgs t, int block
 }
 
 int plain_splits(int64_t M, int64_t N, int64_t kb) {
-  const int64_t tiles = ((M + kLargeTile - 1) / kLargeTile) * ((N + kLargeTile - 1) / kLargeTile);
+  const int64_t tiles = tiles_of(M, N, false, 8);
   // shares of K that fill the CUs, none of them under 16 stages (1024 values)
   int64_t s = 256 / tiles;
   s = s < kb / kLargeStage / 16 ? s : kb / kLargeStage / 16;
@@ -303,7 +349,7 @@ int plain_splits(int64_t M, int64_t N, int64_t kb) {
   return (int)((kb / kLargeStage + per - 1) / per);
 }
 
-hipError_t launch_large_plain(const TileArgs& t, int dtype, hipStream_t s) {
+hipError_t launch_tile_plain(const TileArgs& t, int dtype, hipStream_t s) {
   if (t.splits > 1) {
     TileArgs p = t;
     p.y = t.part;

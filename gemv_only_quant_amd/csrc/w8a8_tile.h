@@ -50,10 +50,10 @@ template <int NT> __device__ __forceinline__ constexpr int epi_word(int row, int
   return row * 16 * NT + (col ^ (16 * ((row >> 2) & (NT % 4 ? 1 : 3))));
 }
 constexpr int epi_words(int nt) { return 256 * nt; }
-// ... and after the tiles, for the gradient epilogue, one transposed tile of
-// 16-bit values: 16 rows of a column, padded to keep 16-byte reads aligned.
-constexpr int kEpiLdh = 24;
-constexpr int epi_t_words(int nt) { return 16 * nt * kEpiLdh / 2; }
+// ... and after the tiles, for the gradient epilogue, 64 rows transposed, of
+// 16-bit values: a column's 64 rows are 128 bytes, 8 chunks, chunk c of column n
+// at c ^ (n / 4 % 8), so that a wave's stores of one row pair meet two to a bank.
+constexpr int epi_t_words(int nt) { return 16 * nt * 32; }
 
 // Accumulators of a 16-row tile to its LDS.
 template <int KIND, int NT>
@@ -87,6 +87,12 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
   typedef T T4 __attribute__((ext_vector_type(4)));
   typedef T T8 __attribute__((ext_vector_type(8)));
 
+  // row of this lane in pass p: in the gradient epilogue two passes take
+  // neighbouring rows
+  __device__ __forceinline__ int row_of(int p) const {
+    return EPI == EPI_GRAD ? 2 * RPP * (p / 2) + 2 * (lane / LPR) + p % 2 : RPP * p + lane / LPR;
+  }
+
   int lane, col, n0, n, nn;  // nn: columns of this lane that exist (may be <= 0)
   float s0[4], s1[4];        // column scales; of the up projection
   float k1, k2;              // PLAIN: the factor; GRAD: c1, c2
@@ -118,7 +124,7 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
     if constexpr (EPI == EPI_GRAD) {
 #pragma unroll
       for (int p = 0; p < PASSES; ++p) {
-        const int m = m0 + RPP * p + lane / LPR;
+        const int m = m0 + row_of(p);
         const uint16_t* src = static_cast<const uint16_t*>(g.dh) + (int64_t)m * g.lddh + n;
         const bool row = m < g.M;
         if (vec && row && nn >= 4) {
@@ -134,7 +140,8 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
   }
 
   // The tile that put_tile wrote to t0, whose first row is m0; sa: its rows'
-  // scales; tt: the wave's transposed tile (GRAD); m1: the next tile's first row.
+  // scales; tt: the wave's transposed rows (GRAD), which leave with every fourth
+  // tile (m0 from a multiple of 64 on); m1: the next tile's first row.
   __device__ __forceinline__ void tile(const TileArgs& g, const uint32_t* t0, const float* sa,
                                        uint32_t* ttw, int m0, int m1) {
     if constexpr (EPI == EPI_PARTIAL) {
@@ -191,8 +198,6 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
       // dg and du in fp32, then d = (dg sg c1 | du su c1) row-major and
       // dt = (dg sx c2 | du sx c2) transposed through LDS, zeros where a row
       // or column only pads
-      constexpr int LDH = kEpiLdh;
-      T* tt = reinterpret_cast<T*>(ttw);
       T* dd = static_cast<T*>(g.d);
       float e[PASSES][4];
 #pragma unroll
@@ -200,46 +205,63 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
 #pragma unroll
         for (int j = 0; j < 4; ++j) e[p][j] = (float)__builtin_bit_cast(T, (uint16_t)dh[p][j]);
       fetch(g, m1);
+      const int part = (m0 / 16) % 4;  // of the 64 transposed rows
       with_act(g.act, [&](auto act) {
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-          const int row = RPP * p + lane / LPR, m = m0 + row;
-          const acc_t cg = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, col));
-          const acc_t cu = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, COLS + col));
-          const float a = sa[row];  // 0 for rows past M
-          const float ak = a * k2;
-          T4 dgv, duv;
+        for (int p = 0; p < PASSES; p += 2) {
+          // two neighbouring rows at once: their transposed values go to LDS
+          // in pairs
+          T tg[2][4], tu[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = row_of(p + h), m = m0 + row;
+            const acc_t cg = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, col));
+            const acc_t cu = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, COLS + col));
+            const float a = sa[row];  // 0 for rows past M
+            const float ak = a * k2;
+            T4 dgv, duv;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float gv = (float)cg[j] * (a * s0[j]), uv = (float)cu[j] * (a * s1[j]);
+              float da;
+              const float r = act_parts<decltype(act)::value>(gv, &da);
+              const float dg = e[p + h][j] * uv * da, du = e[p + h][j] * r;
+              // columns past N only pad: zeros, whatever the row's scale is
+              const bool ok = j < nn;
+              dgv[j] = (T)(ok ? dg * (s0[j] * k1) : 0.f);
+              duv[j] = (T)(ok ? du * (s1[j] * k1) : 0.f);
+              tg[h][j] = (T)(ok ? dg * ak : 0.f);
+              tu[h][j] = (T)(ok ? du * ak : 0.f);
+            }
+            if (m < g.M && n < g.Np) {  // n is a multiple of 4 and Np of 128
+              T* o = dd + (int64_t)m * (2 * g.Np) + n;
+              *reinterpret_cast<T4*>(o) = dgv;
+              *reinterpret_cast<T4*>(o + g.Np) = duv;
+            }
+          }
+          const int r = 16 * part + row_of(p);  // even
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float gv = (float)cg[j] * (a * s0[j]), uv = (float)cu[j] * (a * s1[j]);
-            float da;
-            const float h = act_parts<decltype(act)::value>(gv, &da);
-            const float dg = e[p][j] * uv * da, du = e[p][j] * h;
-            // columns past N only pad: zeros, whatever the row's scale is
-            const bool ok = j < nn;
-            dgv[j] = (T)(ok ? dg * (s0[j] * k1) : 0.f);
-            duv[j] = (T)(ok ? du * (s1[j] * k1) : 0.f);
-            tt[(col + j) * LDH + row] = (T)(ok ? dg * ak : 0.f);
-            tt[(COLS + col + j) * LDH + row] = (T)(ok ? du * ak : 0.f);
-          }
-          if (m < g.M && n < g.Np) {  // n is a multiple of 4 and Np of 128
-            T* o = dd + (int64_t)m * (2 * g.Np) + n;
-            *reinterpret_cast<T4*>(o) = dgv;
-            *reinterpret_cast<T4*>(o + g.Np) = duv;
+            typedef T T2 __attribute__((ext_vector_type(2)));
+            const int c0 = col + j, c1 = COLS + col + j;
+            ttw[c0 * 32 + 4 * ((r >> 3) ^ ((c0 >> 2) & 7)) + ((r & 7) >> 1)] =
+                __builtin_bit_cast(uint32_t, (T2{tg[0][j], tg[1][j]}));
+            ttw[c1 * 32 + 4 * ((r >> 3) ^ ((c1 >> 2) & 7)) + ((r & 7) >> 1)] =
+                __builtin_bit_cast(uint32_t, (T2{tu[0][j], tu[1][j]}));
           }
         }
       });
-      if (g.dt != nullptr && m0 < g.Mp) {
+      if (part == 3 && g.dt != nullptr && m0 < g.Mp) {
+        // whole 128-byte lines: 8 lanes on a column's 64 rows
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         T* dt = static_cast<T*>(g.dt);
-        for (int c = lane; c < 2 * COLS; c += 64) {
-          const int cn = n0 + c % COLS;
+#pragma unroll 4
+        for (int it = 0; it < 2 * COLS / 8; ++it) {
+          const int c = 8 * it + lane / 8, cn = n0 + c % COLS;
           if (cn >= g.N) continue;
-          const T8 x = *reinterpret_cast<const T8*>(tt + c * LDH);
-          const T8 y = *reinterpret_cast<const T8*>(tt + c * LDH + 8);
-          T* o = dt + ((int64_t)(c / COLS) * g.Nr + cn) * g.Mp + m0;
-          *reinterpret_cast<T8*>(o) = x;
-          *reinterpret_cast<T8*>(o + 8) = y;
+          const u32x4_t x = *reinterpret_cast<const u32x4_t*>(ttw + c * 32 + 4 * ((lane & 7) ^ ((c >> 2) & 7)));
+          T* o = dt + ((int64_t)(c / COLS) * g.Nr + cn) * g.Mp + (m0 - 48) + 8 * (lane & 7);
+          *reinterpret_cast<u32x4_t*>(o) = x;
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       }
