@@ -40,7 +40,8 @@ namespace qmm {
 // W: 16 x 16 tiles of a wave in each direction; a workgroup's tile is 32 W rows
 // and columns of B
 constexpr int kLargeStage = 128;  // contracted bytes per stage
-static constexpr int kWaitMem = 0x0070;    // s_waitcnt vmcnt(0) lgkmcnt(0)
+// s_waitcnt vmcnt(n) lgkmcnt(0)
+static constexpr int wait_mem(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0070; }
 
 // MFMA with its accumulator pinned to the AGPRs (left to itself the register
 // allocator moves 256 live accumulators between the register files).
@@ -55,26 +56,26 @@ __device__ __forceinline__ void mfma_pinned(typename Acc<KIND>::type& c, const u
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
 
-// LDS of a workgroup in 16-byte words: two stages of both operands, and in
+// LDS of a workgroup in 16-byte words: NB stages of both operands, and in
 // their place later the epilogue's tiles (4 waves of as many words each); then
 // the row scales.
-template <int EPI, int W> struct LargeLds {
+template <int EPI, int W, int NB> struct LargeLds {
   static constexpr int G = EPI == EPI_GRAD ? 2 : 4;  // row tiles of a wave in LDS at once
   static constexpr int EPI_WORDS = G * epi_words(W) + (EPI == EPI_GRAD ? epi_t_words(W) : 0);
   static constexpr int OPERAND = 32 * W * kLargeStage / 16;  // one operand of a stage
-  static constexpr int STAGES = 4 * OPERAND;
+  static constexpr int STAGES = 2 * NB * OPERAND;
   static constexpr int SCALES = STAGES > EPI_WORDS ? STAGES : EPI_WORDS;
   static constexpr int WORDS16 = SCALES + 32 * W / 4;
 };
 
 // (a device function beside its kernel: the host pass drops a kernel whose own
 // body has matrix-core registers in inline asm)
-template <int KIND, int EPI, int W, int DT>
+template <int KIND, int EPI, int W, int NB, int DT>
 __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m_tiles, int per,
                                            u32x4_t* lds) {
   constexpr bool PAIR = EPI == EPI_GATED || EPI == EPI_GRAD;
   constexpr int MT = W, NT = W, TILE = 32 * W, HALF = 16 * W;
-  typedef LargeLds<EPI, W> L;
+  typedef LargeLds<EPI, W, NB> L;
   constexpr int CPW = PAIR ? 8 * NT : 16 * NT;  // output columns per wave
   constexpr int OPERAND = L::OPERAND, EPI_WORDS = L::EPI_WORDS;
 
@@ -132,7 +133,7 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   // stand in ao and bo; next_stage moves them on, past the last stage not at all
   // (it is read again, unused)
   auto load = [&](int j, int st) {
-    u32x4_t* to = lds + (2 * (st & 1) + j / W) * OPERAND + (W * wave + j % W) * 64;
+    u32x4_t* to = lds + (2 * (st % NB) + j / W) * OPERAND + (W * wave + j % W) * 64;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(j < W ? ra[j / 2] : rb[j % W / 2],
                                              (__attribute__((address_space(3))) void*)to, 16,
                                              j < W ? ao[j % 2] : bo[j % 2], 0, 0, 0);
@@ -146,7 +147,7 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   const int swz = (l16 >> 1) & 7;
   const int oa = (HALF * wm + l16) * 8, ob = OPERAND + (HALF * wn + l16) * 8;
   auto frag = [&](int i, int k, int st) {
-    return lds[2 * (st & 1) * OPERAND + (i < W ? oa + 128 * i : ob + 128 * (i - W)) + ((4 * k + quad) ^ swz)];
+    return lds[2 * (st % NB) * OPERAND + (i < W ? oa + 128 * i : ob + 128 * (i - W)) + ((4 * k + quad) ^ swz)];
   };
 
   float* sa = reinterpret_cast<float*>(lds + L::SCALES);
@@ -166,7 +167,7 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
     if (KIND != kTypeI8 || kb % kLargeStage == 0) return;
     const int at = kb % kLargeStage, r = threadIdx.x;  // a row per thread
     for (int c = r < TILE ? at / 16 : 8; c < 8; ++c) {
-      u32x4_t* p = lds + 2 * (st & 1) * OPERAND + 8 * r + (c ^ ((r >> 1) & 7));
+      u32x4_t* p = lds + 2 * (st % NB) * OPERAND + 8 * r + (c ^ ((r >> 1) & 7));
       *p = clear_tail(*p, 16 * c, at);
     }
     __syncthreads();
@@ -174,13 +175,14 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
 
   u32x4_t f[2][2 * W];  // operands of the two k steps
 #pragma unroll
-  for (int j = 0; j < 2 * W; ++j) load(j, 0);
-  __builtin_amdgcn_s_waitcnt(kWaitMem);
+  for (int q = 0; q < NB; ++q) {
+    if (q > 0) next_stage(q);
+#pragma unroll
+    for (int j = 0; j < 2 * W; ++j) load(j, q);
+  }
+  __builtin_amdgcn_s_waitcnt(wait_mem((NB - 1) * 2 * W));
   __syncthreads();
   if (nst == 1) clear_last(0);
-  next_stage(1);
-#pragma unroll
-  for (int j = 0; j < 2 * W; ++j) load(j, 1);
 #pragma unroll
   for (int i = 0; i < 2 * W; ++i) f[0][i] = frag(i, 0, 0);
 
@@ -203,7 +205,7 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
         }
         if (k == 1) {
 #pragma unroll
-          for (int j = t * READS / GROUPS; j < (t + 1) * READS / GROUPS; ++j) load(j, st + 2);
+          for (int j = t * READS / GROUPS; j < (t + 1) * READS / GROUPS; ++j) load(j, st + NB);
         }
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
@@ -213,15 +215,15 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
         __builtin_amdgcn_sched_barrier(0);
       }
       if (k == 0) {
-        __builtin_amdgcn_s_waitcnt(kWaitMem);
+        __builtin_amdgcn_s_waitcnt(wait_mem((NB - 2) * 2 * W));
         __syncthreads();
         if (st + 2 == nst) clear_last(st + 1);
-        next_stage(st + 2);
+        next_stage(st + NB);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
-  __builtin_amdgcn_s_waitcnt(kWaitMem);
+  __builtin_amdgcn_s_waitcnt(wait_mem(0));
   __syncthreads();  // every wave has left the stages: their LDS becomes the epilogue's
   // the accumulators were last written by MFMAs that the compiler does not see
   // as such: give them their latency, then pass each through an empty asm
@@ -256,13 +258,13 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   }
 }
 
-template <int KIND, int EPI, int W, int DT>
-__global__ __launch_bounds__(256, W == 8 ? 1 : 2) void large_kernel(TileArgs g, int n_tiles,
+template <int KIND, int EPI, int W, int NB, int DT>
+__global__ __launch_bounds__(256, W == 4 && NB == 2 ? 2 : 1) void large_kernel(TileArgs g, int n_tiles,
                                                                     int m_tiles, int per) {
   // one array for everything: with a second one in LDS the compiler waits for
   // all memory before LDS reads in the K loop
-  __shared__ u32x4_t lds[LargeLds<EPI, W>::WORDS16];
-  large_body<KIND, EPI, W, DT>(g, n_tiles, m_tiles, per, lds);
+  __shared__ u32x4_t lds[LargeLds<EPI, W, NB>::WORDS16];
+  large_body<KIND, EPI, W, NB, DT>(g, n_tiles, m_tiles, per, lds);
 }
 
 // ---------------------------------------------------------------- host side
@@ -274,17 +276,17 @@ static int64_t tiles_of(int64_t m, int64_t n, bool pair, int w) {
 }
 
 // Whether 256 x 256 tiles serve a product better than 128 x 128 ones, in units
-// of the time of a round of the former: of the latter a CU runs two at once,
-// 0.77 together, 0.35 where each has a CU to itself.
+// of the time of a round of the former (K = 4096: 54 us).  Of the latter a CU
+// runs two at once (42 us together), or where there are at most 256, one with
+// twice the stages in flight (24 us).  So 1024 x 4096 x 4096 takes 25 us and not
+// 54, 512 x 4096 x 11008 42 and not 56, 1024 x 4096 x 11008 56 and not 73.
 static bool large_tiles(int64_t m, int64_t n, bool pair) {
-  static const int want = env_int("QMM_TILE_LARGE");
-  if (want >= 0) return want > 0;
   const int64_t t8 = tiles_of(m, n, pair, 8), t4 = tiles_of(m, n, pair, 4);
-  const double small = t4 <= 256 ? 0.35 : 0.77 * (double)((t4 + 511) / 512);
+  const double small = t4 <= 256 ? 0.45 : 0.77 * (double)((t4 + 511) / 512);
   return (double)((t8 + 255) / 256) <= small;
 }
 
-template <int KIND, int EPI, int W, int DT>
+template <int KIND, int EPI, int W, int NB, int DT>
 static hipError_t launch_w(const TileArgs& t, int64_t m, int64_t n, hipStream_t s) {
   constexpr int rows = 32 * W, cols = EPI == EPI_GATED || EPI == EPI_GRAD ? 16 * W : 32 * W;
   int64_t n_tiles = (n + cols - 1) / cols;
@@ -295,7 +297,7 @@ static hipError_t launch_w(const TileArgs& t, int64_t m, int64_t n, hipStream_t 
     n_tiles *= t.splits;
   }
   if (n_tiles * m_tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
-  return launch_kernel(large_kernel<KIND, EPI, W, DT>, dim3((unsigned)(n_tiles * m_tiles)), dim3(256),
+  return launch_kernel(large_kernel<KIND, EPI, W, NB, DT>, dim3((unsigned)(n_tiles * m_tiles)), dim3(256),
                        s, t, (int)n_tiles, (int)m_tiles, per);
 }
 
@@ -304,9 +306,11 @@ static hipError_t launch(const TileArgs& t, hipStream_t s) {
   // the gradient epilogue also writes the padding of its operands
   const int64_t n = EPI == EPI_GRAD ? t.Np : t.N;
   const int64_t m = EPI == EPI_GRAD && t.dt != nullptr ? t.Mp : t.M;
-  if constexpr (EPI == EPI_PARTIAL) return launch_w<KIND, EPI, 8, DT>(t, m, n, s);
-  return large_tiles(m, n, EPI == EPI_GATED || EPI == EPI_GRAD) ? launch_w<KIND, EPI, 8, DT>(t, m, n, s)
-                                                                : launch_w<KIND, EPI, 4, DT>(t, m, n, s);
+  if constexpr (EPI == EPI_PARTIAL) return launch_w<KIND, EPI, 8, 2, DT>(t, m, n, s);
+  constexpr bool pair = EPI == EPI_GATED || EPI == EPI_GRAD;
+  if (large_tiles(m, n, pair)) return launch_w<KIND, EPI, 8, 2, DT>(t, m, n, s);
+  return tiles_of(m, n, pair, 4) <= 256 ? launch_w<KIND, EPI, 4, 4, DT>(t, m, n, s)
+                                        : launch_w<KIND, EPI, 4, 2, DT>(t, m, n, s);
 }
 
 hipError_t launch_tile_scale(const TileArgs& t, hipStream_t s) {
