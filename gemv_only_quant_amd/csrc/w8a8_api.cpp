@@ -245,6 +245,7 @@ qmm_status qmm_quantize_tokens(const void* x, int x_dtype, int64_t ldx, int8_t* 
 
 size_t qmm_w8a8_workspace_bytes(int M, int K, int x_dtype) {
   if (M <= 0 || K <= 0 || K >= kMaxK || !value_type(x_dtype)) return 0;
+  if (qmm::rows_fits(M, K)) return 0;  // quantized in LDS
   return (size_t)M * code_ld(K) + (size_t)M * 4;
 }
 

@@ -94,7 +94,8 @@ template <int XDT>
 static hipError_t launch_q_type(const void* x, int64_t ldx, int8_t* xq, int64_t ldxq, float* sx,
                                 int M, int K, hipStream_t s) {
   // a wave per row up to 512 elements, else a workgroup, the row held in
-  // registers up to 16384 elements
+  // registers up to 16384 elements (4096 x 4096 bf16: 4 waves to a row 13.9 us,
+  // 2 waves 15.3, 1 wave 17.5; 4096 x 11008 28.1 us, 4.8 TB/s)
   if (K <= 512) return launch_q<XDT, 1, 1>(x, ldx, xq, ldxq, sx, M, K, s);
   if (K <= 2048) return launch_q<XDT, 4, 1>(x, ldx, xq, ldxq, sx, M, K, s);
   if (K <= 4096) return launch_q<XDT, 4, 2>(x, ldx, xq, ldxq, sx, M, K, s);

@@ -72,8 +72,9 @@ QMM_API qmm_status qmm_quantize_tokens(const void* x, int x_dtype, int64_t ldx, 
 
 /* Scratch for activations that the call quantizes itself (x_dtype other than
  * QMM_I8): codes and scales.  Device memory, 16-byte aligned, any contents;
- * in use until the call's work on the stream is done.  0 for QMM_I8 and for
- * invalid arguments. */
+ * in use until the call's work on the stream is done.  0 for QMM_I8, for a few
+ * tokens (which are quantized within the product's launch) and for invalid
+ * arguments. */
 QMM_API size_t qmm_w8a8_workspace_bytes(int M, int K, int x_dtype);
 
 /*

@@ -18,8 +18,10 @@ SIZES = [(1, 1, 1), (1, 17, 33), (1, 300, 1024), (2, 64, 4096), (3, 64, 64), (4,
          (5, 100, 257), (8, 96, 528), (15, 48, 3000), (16, 130, 1000), (17, 33, 128), (33, 515, 260),
          (64, 256, 512), (65, 129, 300), (100, 1024, 96), (200, 70, 96), (257, 260, 784),
          (300, 520, 1040), (513, 700, 2064),
-         # enough 256 x 256 tiles for the many-row kernel, ragged in every axis
-         (2100, 2100, 300), (2300, 1900, 145), (4090, 1030, 1024)]
+         # more 128 x 128 tiles than CUs, then enough 256 x 256 ones, ragged in every axis
+         (2100, 2100, 300), (2300, 1900, 145), (4090, 1030, 1024), (2950, 2900, 145), (1500, 2900, 200),
+         # the longest rows that a few tokens' codes are kept in LDS for, and longer
+         (4, 48, 16384), (1, 40, 65536), (2, 20, 40000), (4, 36, 16400)]
 
 
 def grad_in(m, n, seed, t):
@@ -238,7 +240,8 @@ GRAD_SIZES = [(1, 1, 1), (1, 64, 33), (3, 17, 64), (16, 130, 200), (64, 128, 256
               (130, 300, 70), (257, 260, 500), (300, 520, 1040), (129, 700, 2064),
               # many rows (dx, and the gated block's g and u); contractions long enough to be
               # split over workgroups (dW in the first and last, dx in the second)
-              (2100, 70, 2100), (70, 2100, 130), (1000, 2060, 90), (4200, 40, 60)]
+              (2100, 70, 2100), (70, 2100, 130), (1000, 2060, 90), (4200, 40, 60), (2950, 40, 2900),
+              (1500, 2900, 90)]
 
 
 @pytest.mark.parametrize("m,n,k", GRAD_SIZES)

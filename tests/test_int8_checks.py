@@ -118,6 +118,8 @@ def test_nothing_to_do(fn, over):
 
 def test_workspace_sizes():
     assert L.qmm_w8a8_workspace_bytes(3, 100, 1) == 3 * 112 + 12
+    assert L.qmm_w8a8_workspace_bytes(3, 4096, 1) == 0  # a few tokens: quantized within the launch
+    assert L.qmm_w8a8_workspace_bytes(5, 4096, 1) == 5 * 4096 + 20
     assert L.qmm_w8a8_workspace_bytes(3, 100, 3) == 0 and L.qmm_w8a8_workspace_bytes(0, 100, 1) == 0
     assert L.qmm_w8a8_workspace_bytes(3, 1 << 17, 1) == 0
     need = L.qmm_w8a8_backward_workspace_bytes
