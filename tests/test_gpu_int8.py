@@ -431,3 +431,31 @@ def test_other_stream_and_repeat(m):
     torch.cuda.current_stream().wait_stream(s)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ together
+def _example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "int8_feed_forward.py")
+    spec = importlib.util.spec_from_file_location("int8_feed_forward", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+def test_layer_is_the_same_for_one_token_and_many():
+    """The sums are whole numbers and every kernel rounds the same steps, so a
+    token's output does not depend on what is computed beside it."""
+    layer = _example().FeedForward(512, 700)
+    x = u8.tokens(600, 512, seed=5, dtype=torch.bfloat16).cuda()
+    whole = layer.serve(x)
+    for a, b in ((0, 1), (3, 6), (10, 30), (40, 100), (100, 400)):
+        assert torch.equal(layer.serve(x[a:b]), whole[a:b]), (a, b)
+
+
+def test_layer_trains():
+    losses = _example().train(tokens=256, width=256, hidden=704, steps=12, rate=0.3, log=lambda *_: None)
+    assert all(math.isfinite(v) for v in losses)
+    assert losses[-1] < 0.7 * losses[0], losses
