@@ -1,18 +1,21 @@
 // w8a8_backward.hip -- gradients of the int8 x int8 product and of the gated
 // block on it.
 //
-//   dx[m, k] = sum_j D[m, j] Wt[k, j]      D  = dy sw c1 (gated: dg sg c1 | du su c1)
-//   dW[n, k] = sum_m Dt[n, m] xt[k, m]     Dt = (dy sx c2)^t (gated: dg's, then du's)
+//   dx[m, k] = sum_j D[m, j] W[j, k]       D  = dy sw c1 (gated: dg sg c1 | du su c1)
+//   dW[n, k] = sum_m Dt[n, m] xq[m, k]     Dt = (dy sx c2)^t (gated: dg's, then du's)
 //
-// Wt and xt are the codes alone, transposed: they are exact in a 16-bit
-// type, so each product has one rounding, that of D or Dt.  c1 and c2 are
-// the powers of two that bring the largest weight (token) scale to [1/2, 1):
-// with scales of 1e-3 and fp16 gradients the products would else lie among
-// its subnormals.  They leave again, exactly, as the fp32 sums are stored.
+// The right operands are the codes alone, as they lie in memory: they are exact
+// in a 16-bit type, so each product has one rounding, that of D or Dt, and the
+// product's kernel transposes and converts them on their way from LDS (a pass
+// that wrote them transposed in 16 bits took 28 us for each 4096 x 11008, a tenth of the
+// time at 4096 tokens and a quarter at 512).  c1 and c2 are the powers of two that
+// bring the largest weight (token) scale to [1/2, 1): with scales of 1e-3 and fp16
+// gradients the products would else lie among its subnormals.  They leave again,
+// exactly, as the fp32 sums are stored.
 //
-// Steps: the powers of two (one workgroup); Wt and xt; D and Dt -- from dy by
-// scaling, or for the gated block by the gradient epilogue of the int8 product,
-// which makes g and u again; then the two products.
+// Steps: the powers of two (one workgroup); D and Dt -- from dy by scaling, or for
+// the gated block by the gradient epilogue of the int8 product, which makes g and u
+// again; then the two products.
 #include <type_traits>
 
 #include "w8a8_device.h"
@@ -58,42 +61,6 @@ __global__ __launch_bounds__(1024) void scale_powers_kernel(const float* __restr
     e = e < 26 ? 26 : (e > 226 ? 226 : e);
     out[2 * i] = __builtin_bit_cast(float, (uint32_t)(253 - e) << 23);
     out[2 * i + 1] = __builtin_bit_cast(float, (uint32_t)(e + 1) << 23);
-  }
-}
-
-// (R, C) int8 -> (C, ldo) 16-bit transposed, columns from R up to the next
-// multiple of 128 zero.  A workgroup moves 128 rows x 64 columns through LDS:
-// 64-byte pieces of rows in, 256-byte pieces of the transposed rows out.
-template <int DT>
-__global__ __launch_bounds__(256) void transpose_codes_kernel(const int8_t* __restrict__ q,
-                                                              int64_t ldq, int R, int C,
-                                                              void* __restrict__ out, int64_t ldo,
-                                                              int c_tiles) {
-  typedef typename Half16<DT>::type T;
-  typedef T T8 __attribute__((ext_vector_type(8)));
-  __shared__ int8_t t[64][132];
-  const int c0 = (int)(blockIdx.x % (unsigned)c_tiles) * 64;
-  const int64_t r0 = (int64_t)(blockIdx.x / (unsigned)c_tiles) * 128;
-  const int tid = threadIdx.x;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int row = (tid >> 2) + 64 * h, col = 16 * (tid & 3);
-    u32x4_t v = {0u, 0u, 0u, 0u};
-    if (r0 + row < R && c0 + col < C)
-      v = *reinterpret_cast<const u32x4_t*>(q + (r0 + row) * ldq + c0 + col);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) t[col + j][row] = (int8_t)(v[j / 4] >> (8 * (j % 4)));
-  }
-  __syncthreads();
-  T* o = static_cast<T*>(out);
-#pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const int c = (tid >> 4) + 16 * h, r = 8 * (tid & 15);
-    if (c0 + c >= C) continue;
-    T8 v;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (T)(float)t[c][r + j];
-    *reinterpret_cast<T8*>(o + (int64_t)(c0 + c) * ldo + r0 + r) = v;
   }
 }
 
@@ -196,11 +163,7 @@ BackwardPlan plan_backward(int M, int N, int K, bool gated, bool weight_grad) {
     return here;
   };
   p.d = put((int64_t)M * p.Jp);
-  p.wt = put((int64_t)K * p.Jp);
-  if (weight_grad) {
-    p.dt = put(p.parts * p.Nr * p.Mp);
-    p.xt = put((int64_t)K * p.Mp);
-  }
+  if (weight_grad) p.dt = put(p.parts * p.Nr * p.Mp);
   // fp32 sums of a product whose contraction is split; dx and dW in turn
   p.dx_splits = plain_splits(M, K, 2 * p.Jp);
   p.dw_splits = weight_grad ? plain_splits(p.parts * p.Nr, K, 2 * p.Mp) : 1;
@@ -220,22 +183,6 @@ static hipError_t backward(const BackwardArgs& a, const BackwardPlan& p) {
   hipError_t e = launch_kernel(scale_powers_kernel, dim3(1), dim3(1024), a.stream, a.sw[0],
                                a.gated ? a.sw[1] : nullptr, wgrad ? a.sx : nullptr, a.N, a.M, scal);
   if (e != hipSuccess) return e;
-  auto transpose = [&](const int8_t* q, int64_t ldq, int R, void* out, int64_t cols, int64_t ldo) {
-    // `cols`, a multiple of 128, of the output's rows of ldo elements
-    const int c_tiles = (a.K + 63) / 64;
-    const int64_t blocks = c_tiles * ((cols + 127) / 128);
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    return launch_kernel(transpose_codes_kernel<DT>, dim3((unsigned)blocks), dim3(256), a.stream, q,
-                         ldq, R, a.K, out, ldo, c_tiles);
-  };
-  for (int i = 0; i < p.parts; ++i) {
-    e = transpose(a.w[i], a.ldw, a.N, ws + p.wt + (size_t)i * p.Np * 2, p.Np, p.Jp);
-    if (e != hipSuccess) return e;
-  }
-  if (wgrad) {
-    e = transpose(a.x, a.ldx, a.M, ws + p.xt, p.Mp, p.Mp);
-    if (e != hipSuccess) return e;
-  }
   if (a.gated) {
     TileArgs t{};
     t.a = a.x;
@@ -266,8 +213,9 @@ static hipError_t backward(const BackwardArgs& a, const BackwardPlan& p) {
   TileArgs t{};  // dx
   t.a = ws + p.d;
   t.lda = 2 * p.Jp;
-  t.b[0] = ws + p.wt;
-  t.ldb = 2 * p.Jp;
+  t.b[0] = a.w[0], t.b[1] = a.w[1];
+  t.ldb = a.ldw;
+  t.brows = a.N, t.bpad = (int)p.Np;
   t.M = t.M2 = t.Mv = a.M;
   t.N = a.K;
   t.kb = (int)(2 * p.Jp);
@@ -282,8 +230,9 @@ static hipError_t backward(const BackwardArgs& a, const BackwardPlan& p) {
 
   t.a = ws + p.dt;  // dW: rows 0 .. Nr of the first weight, then the second's
   t.lda = 2 * p.Mp;
-  t.b[0] = ws + p.xt;
-  t.ldb = 2 * p.Mp;
+  t.b[0] = a.x;
+  t.ldb = a.ldx;
+  t.brows = a.M, t.bpad = (int)p.Mp;
   t.M = (int)(p.parts * p.Nr);
   t.M2 = (int)p.Nr;
   t.Mv = a.N;

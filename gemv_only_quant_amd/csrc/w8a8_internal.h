@@ -50,15 +50,13 @@ hipError_t launch_rows(const W8A8Args& a, const void* x, int x_dtype, int64_t ld
 // What a backward pass keeps in its workspace; offsets in bytes.
 //   scal   4 floats: c1, 1 / c1, c2, 1 / c2 (powers of two, see w8a8_backward.hip)
 //   d      (M, Jp) dy sw c1 (gated: dg sg c1 | du su c1), Jp = parts * Np
-//   wt     (K, Jp) the codes of W transposed (gated: Wg | Wu), in dy's type
 //   dt     (parts * Nr, Mp) dy sx c2 transposed (rows N .. Nr of a part unused)
-//   xt     (K, Mp) the codes of x transposed, in dy's type
 //   part   fp32 shares of dx's product or dW's, where K is split
 // with the contracted axes zero-padded to whole stages.
 struct BackwardPlan {
   int parts;
   int64_t Np, Jp, Nr, Mp;
-  size_t scal, d, wt, dt, xt, part, bytes;
+  size_t scal, d, dt, part, bytes;
   int dx_splits, dw_splits;
 };
 BackwardPlan plan_backward(int M, int N, int K, bool gated, bool weight_grad);
@@ -94,8 +92,9 @@ hipError_t launch_fill_zero(void* y, int size, int64_t ld, int rows, int cols, h
 struct TileArgs {
   const void* a;       // (M, kb bytes), leading dimension lda bytes
   int64_t lda;
-  const void* b[2];    // (N, kb bytes) each
-  int64_t ldb;
+  const void* b[2];    // int8: (N, kb bytes) each.  16-bit: codes (brows, N) each, the
+  int64_t ldb;         // contracted axis their rows, each padded to bpad of it
+  int brows, bpad;
   int M, N, kb;
   const float* sa;     // scale of each row of A (int8)
   const float* sb[2];  // scale of each row of B (int8)

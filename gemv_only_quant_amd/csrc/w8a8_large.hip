@@ -56,14 +56,72 @@ __device__ __forceinline__ void mfma_pinned(typename Acc<KIND>::type& c, const u
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
 
+// 8 codes of a column as exact 16-bit values, pairs in order.
+template <int KIND> __device__ __forceinline__ u32x4_t code_operand(u32x2_t q) {
+  u32x4_t o;
+  if constexpr (KIND == XF16) {
+    // u = q + 128 under the fp16 exponent of 1024 gives 1024 + u; less 1152 it is q
+    const half2_t off = {(_Float16)-1152.0f, (_Float16)-1152.0f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t u = q[j / 2] ^ 0x80808080u;
+      const uint32_t p = __builtin_amdgcn_perm(0x64646464u, u, j % 2 ? 0x04030402u : 0x04010400u);
+      o[j] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, p) + off);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w = q[j / 2];
+      const int sh = 16 * (j % 2);
+      const bf16x2_t p = {(__bf16)(float)(int8_t)(w >> sh), (__bf16)(float)(int8_t)(w >> (sh + 8))};
+      o[j] = __builtin_bit_cast(uint32_t, p);
+    }
+  }
+  return o;
+}
+
+// A buffer descriptor (make_buf's) as the four words it consists of, and a load
+// of 16 bytes per lane through it straight to LDS, the wave's 1 KiB from `to` on.
+// Written out for the kernels that read LDS transposed: before such a read the
+// compiler waits for every load to LDS that it knows to be in flight, while the
+// kernel's own waits and barriers say when they have arrived.  (It has no register
+// to write.)
+__device__ __forceinline__ u32x4_t buf_words(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return u32x4_t{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu, bytes, 0x00020000u};
+}
+__device__ __forceinline__ void load_to_lds(const u32x4_t& buf, int off, u32x4_t* to) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)to;
+  // the wait states cover a descriptor word that a vector instruction has just
+  // written (a spilled one's reload), for which a load has to stand back 5
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at),
+               "v"(off), "s"(buf)
+               : "memory", "m0");
+}
+
+template <bool WORDS> struct LdsLoad {
+  typedef u32x4_t buf;
+  static __device__ __forceinline__ buf make(const void* p, uint32_t n) { return buf_words(p, n); }
+  static __device__ __forceinline__ void go(const buf& b, int off, u32x4_t* to) { load_to_lds(b, off, to); }
+};
+template <> struct LdsLoad<false> {
+  typedef buf_t buf;
+  static __device__ __forceinline__ buf make(const void* p, uint32_t n) { return make_buf(p, n); }
+  static __device__ __forceinline__ void go(const buf& b, int off, u32x4_t* to) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
+  }
+};
+
 // LDS of a workgroup in 16-byte words: NB stages of both operands, and in
 // their place later the epilogue's tiles (4 waves of as many words each); then
 // the row scales.
-template <int EPI, int W, int NB> struct LargeLds {
+template <int KIND, int EPI, int W, int NB> struct LargeLds {
+  static constexpr int MT = KIND == kTypeI8 ? W : 2 * W, NT = KIND == kTypeI8 ? W : W / 2;
   static constexpr int G = EPI == EPI_GRAD ? 2 : 4;  // row tiles of a wave in LDS at once
-  static constexpr int EPI_WORDS = G * epi_words(W) + (EPI == EPI_GRAD ? epi_t_words(W) : 0);
-  static constexpr int OPERAND = 32 * W * kLargeStage / 16;  // one operand of a stage
-  static constexpr int STAGES = 2 * NB * OPERAND;
+  static constexpr int EPI_WORDS = G * epi_words(NT) + (EPI == EPI_GRAD ? epi_t_words(NT) : 0);
+  static constexpr int A = 32 * W * kLargeStage / 16;      // A of a stage
+  static constexpr int B = KIND == kTypeI8 ? A : A / 2;    // B: as A, or codes
+  static constexpr int STAGES = NB * (A + B);
   static constexpr int SCALES = STAGES > EPI_WORDS ? STAGES : EPI_WORDS;
   static constexpr int WORDS16 = SCALES + 32 * W / 4;
 };
@@ -74,10 +132,11 @@ template <int KIND, int EPI, int W, int NB, int DT>
 __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m_tiles, int per,
                                            u32x4_t* lds) {
   constexpr bool PAIR = EPI == EPI_GATED || EPI == EPI_GRAD;
-  constexpr int MT = W, NT = W, TILE = 32 * W, HALF = 16 * W;
-  typedef LargeLds<EPI, W, NB> L;
+  typedef LargeLds<KIND, EPI, W, NB> L;
+  constexpr int MT = L::MT, NT = L::NT, TILE = 32 * W;
+  constexpr bool CODES = KIND != kTypeI8;  // B is int8 codes, the contracted axis its rows
   constexpr int CPW = PAIR ? 8 * NT : 16 * NT;  // output columns per wave
-  constexpr int OPERAND = L::OPERAND, EPI_WORDS = L::EPI_WORDS;
+  constexpr int STAGE = L::A + L::B, EPI_WORDS = L::EPI_WORDS;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -92,8 +151,9 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
     k0 = part * per;
     nt %= each;
   }
-  const int m0 = mt * TILE, nw = nt * 2 * CPW;  // the workgroup's first row and column
-  const int wm = wave >> 1, wn = wave & 1;
+  const int m0 = mt * TILE, nw = nt * (PAIR ? TILE / 2 : TILE);  // the workgroup's first row and column
+  // waves as 2 x 2, or side by side where B is codes: each is then converted once
+  const int wm = CODES ? 0 : wave >> 1, wn = CODES ? wave : wave & 1;
   const int kb = g.kb;
   const int all = (kb + kLargeStage - 1) / kLargeStage;
   const int nst = EPI == EPI_PARTIAL ? min(per, all - k0) : all;
@@ -103,22 +163,35 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
 
   // One buffer per 16 rows of either operand that this wave moves (8 W of each):
   // the lanes' offsets are then the same few registers for all of them.
+  typedef LdsLoad<CODES> Load;
   auto rows_of = [&](const void* p, int64_t ld, int first, int limit) {
     const int n = min(16, limit - first);
-    return make_buf(static_cast<const char*>(p) + (int64_t)(n > 0 ? first : 0) * ld,
-                    n > 0 ? (uint32_t)((n - 1) * (int)ld + kb16) : 0u);
+    return Load::make(static_cast<const char*>(p) + (int64_t)(n > 0 ? first : 0) * ld,
+                     n > 0 ? (uint32_t)((n - 1) * (int)ld + kb16) : 0u);
   };
   constexpr int PIECES = W / 2;
-  buf_t ra[PIECES], rb[PIECES];
+  typename Load::buf ra[PIECES], rb[PIECES];
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
     ra[i] = rows_of(g.a, g.lda, m0 + 16 * (PIECES * wave + i), g.M);
     // strip PIECES wave + i: NT for each half of the workgroup's columns; of a
     // pair of products, half of them the first's and half the second's
     const int s = PIECES * wave + i, half = s / NT, k = s % NT;
-    rb[i] = PAIR ? rows_of(g.b[k / (NT / 2)], g.ldb, nw + half * CPW + 16 * (k % (NT / 2)), g.N)
-                 : rows_of(g.b[0], g.ldb, nw + half * CPW + 16 * k, g.N);
+    if constexpr (!CODES)
+      rb[i] = PAIR ? rows_of(g.b[k / (NT / 2)], g.ldb, nw + half * CPW + 16 * (k % (NT / 2)), g.N)
+                   : rows_of(g.b[0], g.ldb, nw + half * CPW + 16 * k, g.N);
   }
+  // Codes: this wave moves 16 of a stage's 64 rows, the workgroup's columns of
+  // each.  Rows come in parts of g.brows that exist, padded to g.bpad (what is
+  // read for the padding meets zeros of A, whatever codes it is); columns past N
+  // feed outputs that are not stored.
+  auto code_rows = [&](int st) {
+    const int j = 64 * st + 16 * wave, part = j >= g.bpad ? 1 : 0, r = j - part * g.bpad;
+    const int n = min(16, g.brows - r);
+    const int cols = (min(TILE, g.N - nw) + 15) & ~15;
+    return buf_words(static_cast<const char*>(g.b[part]) + (int64_t)(n > 0 ? r : 0) * ldb + nw,
+                     n > 0 ? (uint32_t)((n - 1) * ldb + cols) : 0u);
+  };
 
   // Load unit u (1 KiB) is rows 8 u .. + 7: lane p's 16 bytes land at slot 64 u +
   // p, so it fetches chunk (p % 8) ^ (r / 2 % 8) of row r = 8 u + p / 8.
@@ -129,25 +202,52 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
     ao[c] = (8 * c + (lane >> 3)) * lda + chunk + k0;
     bo[c] = (8 * c + (lane >> 3)) * ldb + chunk + k0;
   }
-  // load j (W of A, then W of B) of this wave's share of stage st, whose lanes' offsets
-  // stand in ao and bo; next_stage moves them on, past the last stage not at all
-  // (it is read again, unused)
+  // Codes in LDS: chunk c (of 2 W) of row r at c ^ code_swz(r); a load unit is 32
+  // / W rows.
+  constexpr int CH = 2 * W, CODE_UNITS = W / 2;
+  auto code_swz = [](int r) { return W == 8 ? r & 15 : (r >> 1) & 7; };
+  int co[CODES ? CODE_UNITS : 1];
+  if constexpr (CODES) {
+#pragma unroll
+    for (int u = 0; u < CODE_UNITS; ++u) {
+      const int r = 64 / CH * u + lane / CH;  // of the wave's 16
+      co[u] = r * ldb + 16 * ((lane % CH) ^ code_swz(r));
+    }
+  }
+  // load j (W of A, then B's) of this wave's share of stage st, whose lanes'
+  // offsets stand in ao and bo; next_stage moves them on, past the last stage not
+  // at all (it is read again, unused)
+  constexpr int LOADS = W + (CODES ? CODE_UNITS : W);
+  u32x4_t cb = {0u, 0u, 0u, 0u};
+  if constexpr (CODES) cb = code_rows(k0 / kLargeStage);
   auto load = [&](int j, int st) {
-    u32x4_t* to = lds + (2 * (st % NB) + j / W) * OPERAND + (W * wave + j % W) * 64;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(j < W ? ra[j / 2] : rb[j % W / 2],
-                                             (__attribute__((address_space(3))) void*)to, 16,
-                                             j < W ? ao[j % 2] : bo[j % 2], 0, 0, 0);
+    u32x4_t* at = lds + st % NB * STAGE;
+    if (j < W) Load::go(ra[j / 2], ao[j % 2], at + (W * wave + j) * 64);
+    else if constexpr (CODES) Load::go(cb, co[j - W], at + L::A + (CODE_UNITS * wave + j - W) * 64);
+    else Load::go(rb[(j - W) / 2], bo[j % 2], at + L::A + (W * wave + j - W) * 64);
   };
   auto next_stage = [&](int st) {
     const int d = st < nst ? kLargeStage : 0;
 #pragma unroll
     for (int c = 0; c < 2; ++c) ao[c] += d, bo[c] += d;
+    if constexpr (CODES) cb = code_rows(k0 / kLargeStage + min(st, nst - 1));
   };
-  // operand i (W of A, then W of B) of k step k of stage st
+  // operand i (MT of A, then NT of B) of k step k of stage st
   const int swz = (l16 >> 1) & 7;
-  const int oa = (HALF * wm + l16) * 8, ob = OPERAND + (HALF * wn + l16) * 8;
+  const int oa = (16 * MT * wm + l16) * 8, ob = L::A + (16 * NT * wn + l16) * 8;
   auto frag = [&](int i, int k, int st) {
-    return lds[2 * (st % NB) * OPERAND + (i < W ? oa + 128 * i : ob + 128 * (i - W)) + ((4 * k + quad) ^ swz)];
+    return lds[st % NB * STAGE + (i < MT ? oa + 128 * i : ob + 128 * (i - MT)) + ((4 * k + quad) ^ swz)];
+  };
+  // Codes of strip c and k step k: 8 rows' bytes of a column per lane.  The LDS
+  // transposes 8 x 8 bytes within 16 lanes: lane i of them names 8 columns (i % 2)
+  // of row i / 2, lane l receives column l of the 8 rows.
+  auto code_frag = [&](int c, int k, int st) {
+    const int r = 32 * k + 8 * quad + (l16 >> 1);
+    const char* at = reinterpret_cast<const char*>(lds + st % NB * STAGE + L::A) + r * (32 * W) +
+                     16 * ((NT * wn + c) ^ code_swz(r)) + 8 * (l16 & 1);
+    typedef int i32x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+        (__attribute__((address_space(3))) i32x2_t*)at));
   };
 
   float* sa = reinterpret_cast<float*>(lds + L::SCALES);
@@ -167,55 +267,73 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
     if (KIND != kTypeI8 || kb % kLargeStage == 0) return;
     const int at = kb % kLargeStage, r = threadIdx.x;  // a row per thread
     for (int c = r < TILE ? at / 16 : 8; c < 8; ++c) {
-      u32x4_t* p = lds + 2 * (st % NB) * OPERAND + 8 * r + (c ^ ((r >> 1) & 7));
+      u32x4_t* p = lds + st % NB * STAGE + 8 * r + (c ^ ((r >> 1) & 7));
       *p = clear_tail(*p, 16 * c, at);
     }
     __syncthreads();
   };
 
-  u32x4_t f[2][2 * W];  // operands of the two k steps
+  u32x4_t f[2][MT + NT];  // operands of the two k steps
+  u32x2_t raw[NT];
 #pragma unroll
   for (int q = 0; q < NB; ++q) {
     if (q > 0) next_stage(q);
 #pragma unroll
-    for (int j = 0; j < 2 * W; ++j) load(j, q);
+    for (int j = 0; j < LOADS; ++j) load(j, q);
   }
-  __builtin_amdgcn_s_waitcnt(wait_mem((NB - 1) * 2 * W));
+  __builtin_amdgcn_s_waitcnt(wait_mem((NB - 1) * LOADS));
   __syncthreads();
   if (nst == 1) clear_last(0);
 #pragma unroll
-  for (int i = 0; i < 2 * W; ++i) f[0][i] = frag(i, 0, 0);
+  for (int i = 0; i < MT + NT; ++i) {
+    if (CODES && i >= MT) f[0][i] = code_operand<KIND>(code_frag(i - MT, 0, 0));
+    else f[0][i] = frag(i, 0, 0);
+  }
 
 #pragma unroll 1
   for (int st = 0; st < nst; ++st) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       // groups of 4 MFMAs; the next k step's operands are read in the first half
-      // of them, in the order of their first use, and in the second k step the
-      // loads go out
-      constexpr int GROUPS = W * W / 4, READS = 2 * W, PER = 2 * READS / GROUPS;
+      // of them, in the order of their first use (codes in the first quarter,
+      // and made operands between the MFMAs of the rest), and in the second k
+      // step the loads go out
+      constexpr int GROUPS = W * W / 4, PER = 4 * W / GROUPS, Q = GROUPS / 4;
 #pragma unroll
       for (int t = 0; t < GROUPS; ++t) {
-        if (t < GROUPS / 2) {
+        if (!CODES && t < GROUPS / 2) {
 #pragma unroll
           for (int h = 0; h < PER; ++h) {
             const int q = PER * t + h, i = q == 0 ? 0 : (q <= W ? W + q - 1 : q - W);
             f[k ^ 1][i] = frag(i, k ^ 1, st + k);
           }
         }
+        if (CODES && t < Q) {
+#pragma unroll
+          for (int c = t * NT / Q; c < (t + 1) * NT / Q; ++c) raw[c] = code_frag(c, k ^ 1, st + k);
+        }
+        if (CODES && t < 2 * Q) {
+#pragma unroll
+          for (int i = t * MT / (2 * Q); i < (t + 1) * MT / (2 * Q); ++i) f[k ^ 1][i] = frag(i, k ^ 1, st + k);
+        }
+        if (CODES && t >= Q) {
+#pragma unroll
+          for (int c = (t - Q) * NT / (3 * Q); c < (t - Q + 1) * NT / (3 * Q); ++c)
+            f[k ^ 1][MT + c] = code_operand<KIND>(raw[c]);
+        }
         if (k == 1) {
 #pragma unroll
-          for (int j = t * READS / GROUPS; j < (t + 1) * READS / GROUPS; ++j) load(j, st + NB);
+          for (int j = t * LOADS / GROUPS; j < (t + 1) * LOADS / GROUPS; ++j) load(j, st + NB);
         }
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          const int i = t * 4 / W, c = t * 4 % W + s;
-          mfma_pinned<KIND>(acc[i][c], f[k][i], f[k][W + c]);
+          const int i = (4 * t + s) / NT, c = (4 * t + s) % NT;
+          mfma_pinned<KIND>(acc[i][c], f[k][i], f[k][MT + c]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
       if (k == 0) {
-        __builtin_amdgcn_s_waitcnt(wait_mem((NB - 2) * 2 * W));
+        __builtin_amdgcn_s_waitcnt(wait_mem((NB - 2) * LOADS));
         __syncthreads();
         if (st + 2 == nst) clear_last(st + 1);
         next_stage(st + NB);
@@ -237,7 +355,7 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   __builtin_amdgcn_sched_barrier(0);
 
   uint32_t* t0 = reinterpret_cast<uint32_t*>(lds) + wave * EPI_WORDS;
-  const int mw = m0 + HALF * wm, rw = HALF * wm;  // the wave's first row; in the tile
+  const int mw = m0 + 16 * MT * wm, rw = 16 * MT * wm;  // the wave's first row; in the tile
   TileArgs ge = g;
   if constexpr (EPI == EPI_PARTIAL) ge.y = static_cast<float*>(g.y) + part * ((int64_t)g.M * g.ldy);
   Epilogue<KIND, EPI, NT, DT> epi;
@@ -263,7 +381,7 @@ __global__ __launch_bounds__(256, W == 4 && NB == 2 ? 2 : 1) void large_kernel(T
                                                                     int m_tiles, int per) {
   // one array for everything: with a second one in LDS the compiler waits for
   // all memory before LDS reads in the K loop
-  __shared__ u32x4_t lds[LargeLds<EPI, W, NB>::WORDS16];
+  __shared__ u32x4_t lds[LargeLds<KIND, EPI, W, NB>::WORDS16];
   large_body<KIND, EPI, W, NB, DT>(g, n_tiles, m_tiles, per, lds);
 }
 
