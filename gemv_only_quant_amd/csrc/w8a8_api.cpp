@@ -24,6 +24,7 @@ bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(
 
 constexpr int64_t kMaxLd = int64_t(1) << 22;  // 256 rows stay within 32-bit byte offsets
 constexpr int kMaxK = 1 << 17;                // sums of code products fit 32 bits
+constexpr int kMaxRows = INT32_MAX - 1024;    // indices within the last tile stay ints
 
 int type_size(int t) { return t == QMM_F32 ? 4 : 2; }
 
@@ -32,6 +33,8 @@ qmm_status check_sizes(const char* fn, int M, int N, int K) {
     QMM_REFUSE(QMM_ERR_ARG, "%s: negative size M=%d N=%d K=%d", fn, M, N, K);
   if (K >= kMaxK)
     QMM_REFUSE(QMM_ERR_UNSUPPORTED, "%s: K=%d too large for exact 32-bit sums (K < %d)", fn, K, kMaxK);
+  if (M > kMaxRows || N > kMaxRows)
+    QMM_REFUSE(QMM_ERR_UNSUPPORTED, "%s: M=%d or N=%d too large (at most %d)", fn, M, N, kMaxRows);
   return QMM_OK;
 }
 
@@ -147,6 +150,11 @@ qmm_status forward(const char* fn, bool gated, const void* x, int x_dtype, int64
   return device_status(fn, qmm::launch_w8a8(a));
 }
 
+// the contracted axes become leading dimensions of 16-bit operands
+bool backward_fits(int M, int N, bool gated) {
+  return (int64_t)N * (gated ? 2 : 1) < kMaxLd / 2 - 256 && M < kMaxLd / 2 - 256;
+}
+
 qmm_status backward(const char* fn, bool gated, const void* dy, int dtype, int64_t lddy,
                     const int8_t* x, int64_t ldx, const float* sx, const int8_t* const (&w)[2],
                     const float* const (&sw)[2], int64_t ldw, void* dx, int64_t lddx,
@@ -156,8 +164,7 @@ qmm_status backward(const char* fn, bool gated, const void* dy, int dtype, int64
     QMM_REFUSE(QMM_ERR_ARG, "%s: dtype must be QMM_F16 or QMM_BF16 (got %d)", fn, dtype);
   if (gated) QMM_CHECK(check_act(fn, act));
   QMM_CHECK(check_sizes(fn, M, N, K));
-  // the contracted axes become leading dimensions of 16-bit operands
-  if ((int64_t)N * (gated ? 2 : 1) >= kMaxLd / 2 - 256 || M >= kMaxLd / 2 - 256)
+  if (!backward_fits(M, N, gated))
     QMM_REFUSE(QMM_ERR_UNSUPPORTED, "%s: M=%d or N=%d too large", fn, M, N);
   const bool wgrad = dw[0] != nullptr;
   if (gated && (dw[1] != nullptr) != wgrad)
@@ -244,7 +251,7 @@ qmm_status qmm_quantize_tokens(const void* x, int x_dtype, int64_t ldx, int8_t* 
 }
 
 size_t qmm_w8a8_workspace_bytes(int M, int K, int x_dtype) {
-  if (M <= 0 || K <= 0 || K >= kMaxK || !value_type(x_dtype)) return 0;
+  if (M <= 0 || M > kMaxRows || K <= 0 || K >= kMaxK || !value_type(x_dtype)) return 0;
   if (qmm::rows_fits(M, K)) return 0;  // quantized in LDS
   return (size_t)M * code_ld(K) + (size_t)M * 4;
 }
@@ -265,7 +272,7 @@ qmm_status qmm_w8a8_gated(const void* x, int x_dtype, int64_t ldx, const float* 
 }
 
 size_t qmm_w8a8_backward_workspace_bytes(int M, int N, int K, int gated, int weight_grad) {
-  if (M <= 0 || N <= 0 || K <= 0 || K >= kMaxK) return 0;
+  if (M <= 0 || N <= 0 || K <= 0 || K >= kMaxK || !backward_fits(M, N, gated != 0)) return 0;
   return qmm::plan_backward(M, N, K, gated != 0, weight_grad != 0).bytes;
 }
 

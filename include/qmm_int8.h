@@ -31,7 +31,9 @@
  *    faster.
  *  - Leading dimensions stay below 2^22 elements (2^22 bytes for int8), K
  *    below 2^17: sums of K products of codes then fit 32 bits and are exact
- *    whole numbers, whatever the order (QMM_ERR_UNSUPPORTED beyond).
+ *    whole numbers, whatever the order; M and N at most 2^31 - 1025, in the
+ *    backward calls M, N (gated: 2 N) below 2^21 - 256 (QMM_ERR_UNSUPPORTED
+ *    beyond).
  *  - Outputs are fully overwritten (the elements of their rows; nothing
  *    between rows is touched) and must not overlap inputs.  An empty sum is
  *    zero: K == 0 writes y = 0, M == 0 writes dW = 0, N == 0 writes dx = 0.

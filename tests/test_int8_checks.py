@@ -127,6 +127,19 @@ def test_workspace_sizes():
     assert 0 < need(100, 200, 300, 0, 0) < need(100, 200, 300, 0, 1) < need(100, 200, 300, 1, 1)
 
 
+@pytest.mark.parametrize("fn,over", [(quant, dict(M=2 ** 31 - 1024)), (gemm, dict(M=2 ** 31 - 1024)),
+                                     (gemm, dict(N=2 ** 31 - 1, ldy=1 << 21)), (gated, dict(M=2 ** 31 - 1)),
+                                     (gated_bwd, dict(N=1 << 20, lddh=1 << 20))])
+def test_sizes_whose_indices_leave_their_types(fn, over):
+    assert fn(**over) == UNS and "too large" in qmm.qmm_last_error()
+
+
+def test_no_workspace_for_sizes_that_are_refused():
+    assert L.qmm_w8a8_workspace_bytes(2 ** 31 - 1024, 64, 1) == 0
+    need = L.qmm_w8a8_backward_workspace_bytes
+    assert need(1 << 21, 8, 8, 0, 0) == 0 and need(8, 1 << 20, 8, 1, 0) == 0 < need(8, 1 << 20, 8, 0, 0)
+
+
 def raises(fn, text, status=ARG):
     with pytest.raises(qmm.QmmError) as e:
         fn()
