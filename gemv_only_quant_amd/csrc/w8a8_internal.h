@@ -16,9 +16,9 @@ __host__ __device__ constexpr int64_t round_up(int64_t v, int64_t to) {
   return (v + to - 1) / to * to;
 }
 
-// Bytes of contraction per pipeline stage of the tile kernels: operands that
-// the library lays out itself are zero-padded to whole stages.
-constexpr int kStageBytes = 256;
+// Bytes of contraction per stage of the tile kernels: operands that the library
+// lays out itself are zero-padded to whole stages.
+constexpr int kStageBytes = 128;
 
 // ---- per-token quantizer (w8a8_quantize.hip) -------------------------------
 hipError_t launch_quantize_tokens(const void* x, int x_dtype, int64_t ldx, int8_t* xq,
@@ -86,8 +86,8 @@ hipError_t launch_backward(const BackwardArgs& a, const BackwardPlan& p);
 // Zeros a (rows, cols) matrix of elements of `size` bytes (empty sums).
 hipError_t launch_fill_zero(void* y, int size, int64_t ld, int rows, int cols, hipStream_t s);
 
-// ---- tile kernels (w8a8_tile.hip) -------------------------------------------
-// C (rows M of A, rows N of B) = A B^t over `kb` contracted bytes; element
+// ---- tile kernels (w8a8_large.hip) ------------------------------------------
+// C (rows M of A, rows N of B) = A B^t over `kb` contracted bytes of A; element
 // types and what becomes of C are the kernel's.
 struct TileArgs {
   const void* a;       // (M, kb bytes), leading dimension lda bytes

@@ -1,9 +1,8 @@
-// w8a8_large.hip -- C = A B^t on the matrix cores for more rows than a decode batch:
-// int8 codes (v_mfma_i32_16x16x64_i8, exact sums) and the 16-bit operands of
-// gradients (v_mfma_f32_16x16x32_{f16,bf16}).  Both operands have the contracted
-// axis contiguous, and one 16-byte chunk per lane is one operand of either kind of
-// MFMA (16 int8 or 8 16-bit values), so one kernel moves bytes and only the
-// instruction differs.  Epilogues (w8a8_tile.h):
+// w8a8_large.hip -- products on the matrix cores for more rows than a decode batch:
+// C = A B^t of int8 codes (v_mfma_i32_16x16x64_i8, exact sums), both with the
+// contracted axis contiguous, and the gradients' C = A B of 16-bit values by int8
+// codes (v_mfma_f32_16x16x32_{f16,bf16}), the contracted axis the codes' rows.
+// Epilogues (w8a8_tile.h):
 //   SCALE    y = C sa[m] sb[n]
 //   GATED    h = act(g) u for two products g, u of the same left operand
 //   GRAD     dg = dh u act'(g), du = dh act(g), left as 16-bit operands of the
@@ -11,14 +10,15 @@
 //   PLAIN    y = C * (a power of two), 16-bit
 //   PARTIAL  fp32 sums of a share of the contraction, added by a second launch
 //
-// Tiles of 256 x 256 (W = 8), bound by the matrix cores, as described here; 128 x
-// 128 (W = 4, two workgroups per CU) where the former are too few.
+// Tiles of 256 x 256 (W = 8), bound by the matrix cores (2.7e15 operations/s of int8
+// over many rounds, at the 1.8 GHz that the power limit leaves), as described here;
+// 128 x 128 (W = 4, two workgroups per CU) where the former are too few.
 //
 //  * one workgroup per CU, 4 waves as 2 x 2; a wave owns 128 rows x 128 columns
 //    = 8 x 8 MFMA tiles, 256 accumulators per lane pinned to the matrix-core
 //    (AGPR) registers;
-//  * a stage is 128 contracted bytes (128 int8 or 64 16-bit values), two MFMA k
-//    steps.  Both operands' tiles of a stage, 32 KiB each, are shared through
+//  * a stage is 128 contracted bytes of A (128 int8 or 64 16-bit values), two MFMA
+//    k steps.  Both operands' tiles of a stage, 32 KiB each, are shared through
 //    double-buffered LDS, filled by buffer loads straight to LDS: whole 128-byte
 //    lines, 8 lanes each, 8 rows per load.  Read from LDS they are conflict-free
 //    ds_read_b128: chunk c of row r lies at slot 8 r + (c ^ (r / 2 % 8));
@@ -31,15 +31,20 @@
 // slower: neighbouring lanes then lie in different rows, and the address units take
 // the 64 lanes one by one; 256 x 256 with the waves side by side and half the
 // tile, two workgroups per CU, 24%.)
+//  * 16-bit: B's stage is 64 rows of 256 codes, 16 KiB, transposed by LDS reads of 8
+//    x 8 bytes, and made 16-bit values between the MFMAs.  The waves lie side by
+//    side, 256 rows x 64 columns, so that each code is converted once and not
+//    twice (1.0e15 operations/s at 4096 x 22016 x 4096, the library's product of
+//    16-bit values 1.56e15).
 // Every address is in the offset that the buffer's range is checked against:
-// rows past M and columns past N read zeros.
+// rows past M and columns past N read zeros (codes of columns past N: anything, for
+// outputs that are not stored).
 #include "w8a8_tile.h"
 
 namespace qmm {
 
 // W: 16 x 16 tiles of a wave in each direction; a workgroup's tile is 32 W rows
 // and columns of B
-constexpr int kLargeStage = 128;  // contracted bytes per stage
 // s_waitcnt vmcnt(n) lgkmcnt(0)
 static constexpr int wait_mem(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0070; }
 
@@ -119,7 +124,7 @@ template <int KIND, int EPI, int W, int NB> struct LargeLds {
   static constexpr int MT = KIND == kTypeI8 ? W : 2 * W, NT = KIND == kTypeI8 ? W : W / 2;
   static constexpr int G = EPI == EPI_GRAD ? 2 : 4;  // row tiles of a wave in LDS at once
   static constexpr int EPI_WORDS = G * epi_words(NT) + (EPI == EPI_GRAD ? epi_t_words(NT) : 0);
-  static constexpr int A = 32 * W * kLargeStage / 16;      // A of a stage
+  static constexpr int A = 32 * W * kStageBytes / 16;      // A of a stage
   static constexpr int B = KIND == kTypeI8 ? A : A / 2;    // B: as A, or codes
   static constexpr int STAGES = NB * (A + B);
   static constexpr int SCALES = STAGES > EPI_WORDS ? STAGES : EPI_WORDS;
@@ -155,9 +160,9 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   // waves as 2 x 2, or side by side where B is codes: each is then converted once
   const int wm = CODES ? 0 : wave >> 1, wn = CODES ? wave : wave & 1;
   const int kb = g.kb;
-  const int all = (kb + kLargeStage - 1) / kLargeStage;
+  const int all = (kb + kStageBytes - 1) / kStageBytes;
   const int nst = EPI == EPI_PARTIAL ? min(per, all - k0) : all;
-  k0 *= kLargeStage;
+  k0 *= kStageBytes;
   const int kb16 = (kb + 15) & ~15;
   const int lda = (int)g.lda, ldb = (int)g.ldb;
 
@@ -219,7 +224,7 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   // at all (it is read again, unused)
   constexpr int LOADS = W + (CODES ? CODE_UNITS : W);
   u32x4_t cb = {0u, 0u, 0u, 0u};
-  if constexpr (CODES) cb = code_rows(k0 / kLargeStage);
+  if constexpr (CODES) cb = code_rows(k0 / kStageBytes);
   auto load = [&](int j, int st) {
     u32x4_t* at = lds + st % NB * STAGE;
     if (j < W) Load::go(ra[j / 2], ao[j % 2], at + (W * wave + j) * 64);
@@ -227,10 +232,10 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
     else Load::go(rb[(j - W) / 2], bo[j % 2], at + L::A + (W * wave + j - W) * 64);
   };
   auto next_stage = [&](int st) {
-    const int d = st < nst ? kLargeStage : 0;
+    const int d = st < nst ? kStageBytes : 0;
 #pragma unroll
     for (int c = 0; c < 2; ++c) ao[c] += d, bo[c] += d;
-    if constexpr (CODES) cb = code_rows(k0 / kLargeStage + min(st, nst - 1));
+    if constexpr (CODES) cb = code_rows(k0 / kStageBytes + min(st, nst - 1));
   };
   // operand i (MT of A, then NT of B) of k step k of stage st
   const int swz = (l16 >> 1) & 7;
@@ -264,8 +269,8 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   // by the workgroup, before that stage is read (whatever B holds there then
   // meets zeros; 16-bit operands come padded)
   auto clear_last = [&](int st) {
-    if (KIND != kTypeI8 || kb % kLargeStage == 0) return;
-    const int at = kb % kLargeStage, r = threadIdx.x;  // a row per thread
+    if (KIND != kTypeI8 || kb % kStageBytes == 0) return;
+    const int at = kb % kStageBytes, r = threadIdx.x;  // a row per thread
     for (int c = r < TILE ? at / 16 : 8; c < 8; ++c) {
       u32x4_t* p = lds + st % NB * STAGE + 8 * r + (c ^ ((r >> 1) & 7));
       *p = clear_tail(*p, 16 * c, at);
@@ -411,7 +416,7 @@ static hipError_t launch_w(const TileArgs& t, int64_t m, int64_t n, hipStream_t 
   const int64_t m_tiles = (m + rows - 1) / rows;
   int per = 0;
   if constexpr (EPI == EPI_PARTIAL) {
-    per = (t.kb / kLargeStage + t.splits - 1) / t.splits;
+    per = (t.kb / kStageBytes + t.splits - 1) / t.splits;
     n_tiles *= t.splits;
   }
   if (n_tiles * m_tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
@@ -464,11 +469,11 @@ int plain_splits(int64_t M, int64_t N, int64_t kb) {
   const int64_t tiles = tiles_of(M, N, false, 8);
   // shares of K that fill the CUs, none of them under 16 stages (1024 values)
   int64_t s = 256 / tiles;
-  s = s < kb / kLargeStage / 16 ? s : kb / kLargeStage / 16;
+  s = s < kb / kStageBytes / 16 ? s : kb / kStageBytes / 16;
   if (s < 2) return 1;
   // the same number of stages in all but the last, which is not empty
-  const int64_t per = (kb / kLargeStage + s - 1) / s;
-  return (int)((kb / kLargeStage + per - 1) / per);
+  const int64_t per = (kb / kStageBytes + s - 1) / s;
+  return (int)((kb / kStageBytes + per - 1) / per);
 }
 
 hipError_t launch_tile_plain(const TileArgs& t, int dtype, hipStream_t s) {

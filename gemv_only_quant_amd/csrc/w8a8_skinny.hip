@@ -145,7 +145,9 @@ __device__ __forceinline__ void skinny_body(const TileArgs& g, u32x4_t* lds) {
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
-          for (int s = 0; s < NT; ++s) acc[t][s] = mfma_t<kTypeI8>(a[t][j], b[s][j], acc[t][s]);
+          for (int s = 0; s < NT; ++s) acc[t][s] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a[t][j]),
+                                                              __builtin_bit_cast(i32x4_t, b[s][j]),
+                                                              acc[t][s], 0, 0, 0);
     }
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load may land in the sums

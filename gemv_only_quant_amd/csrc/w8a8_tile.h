@@ -1,5 +1,5 @@
 // w8a8_tile.h -- what the matrix-core kernels of the int8 x int8 operators
-// share: instruction kinds, the order of tiles, and the epilogues.
+// share: accumulators, the order of tiles, and the epilogues.
 #pragma once
 #include <type_traits>
 
@@ -12,35 +12,6 @@ enum { EPI_SCALE = 0, EPI_GATED = 1, EPI_GRAD = 2, EPI_PLAIN = 3, EPI_PARTIAL = 
 // KIND: kTypeI8, XF16 or XBF16
 template <int KIND> struct Acc { typedef f32x4_t type; };
 template <> struct Acc<kTypeI8> { typedef i32x4_t type; };
-
-template <int KIND>
-__device__ __forceinline__ typename Acc<KIND>::type mfma_t(const u32x4_t& a, const u32x4_t& b,
-                                                           typename Acc<KIND>::type c) {
-  if constexpr (KIND == kTypeI8)
-    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a),
-                                                 __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
-  else if constexpr (KIND == XF16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a),
-                                                  __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
-}
-
-// Two loads of 16 rows of an operand, each 128 bytes (a whole cache line) of 8
-// rows -- chunk quad + 4 (l16 / 8) of row l16 % 8, then the same of rows 8 up --
-// made the operands of two k steps: lanes 8-15 of the first and 0-7 of the
-// second change places, by rotating rows of 16 lanes by 8.  (Loaded as operands
-// are laid out, 16 rows x 64 bytes, a load takes half lines, and L1 may have given
-// a line up before its other half is asked for.)
-__device__ __forceinline__ void line_operands(u32x4_t (&v)[2]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t p = v[0][j], q = v[1][j];
-    v[0][j] = (uint32_t)__builtin_amdgcn_update_dpp((int)p, (int)q, 0x128, 0xF, 0xC, false);
-    v[1][j] = (uint32_t)__builtin_amdgcn_update_dpp((int)q, (int)p, 0x128, 0xF, 0x3, false);
-  }
-}
 
 // LDS of the epilogue: a 16-row tile of a wave is 16 rows of 16 NT words,
 // column c of row r at word c ^ 16 (r / 4 % (NT % 4 ? 2 : 4)): the four row
@@ -85,7 +56,6 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
   typedef typename Acc<KIND>::type acc_t;
   typedef typename Half16<DT>::type T;
   typedef T T4 __attribute__((ext_vector_type(4)));
-  typedef T T8 __attribute__((ext_vector_type(8)));
 
   // row of this lane in pass p: in the gradient epilogue two passes take
   // neighbouring rows
@@ -226,14 +196,15 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
               float da;
               const float r = act_parts<decltype(act)::value>(gv, &da);
               const float dg = e[p + h][j] * uv * da, du = e[p + h][j] * r;
-              // columns past N only pad: zeros, whatever the row's scale is
-              const bool ok = j < nn;
+              // rows past M and columns past N only pad: zeros, whatever the
+              // scales are
+              const bool ok = j < nn && m < g.M;
               dgv[j] = (T)(ok ? dg * (s0[j] * k1) : 0.f);
               duv[j] = (T)(ok ? du * (s1[j] * k1) : 0.f);
               tg[h][j] = (T)(ok ? dg * ak : 0.f);
               tu[h][j] = (T)(ok ? du * ak : 0.f);
             }
-            if (m < g.M && n < g.Np) {  // n is a multiple of 4 and Np of 128
+            if (m < g.M && n < g.Np) {  // n is a multiple of 4 and Np of 64
               T* o = dd + (int64_t)m * (2 * g.Np) + n;
               *reinterpret_cast<T4*>(o) = dgv;
               *reinterpret_cast<T4*>(o + g.Np) = duv;

@@ -336,6 +336,46 @@ def test_gemm_backward_against_differences():
         assert (_along(f, v) - have).abs() <= (b * v.abs()).sum() + 1e-6 * (o.double().cpu() * v).abs().sum()
 
 
+@pytest.mark.parametrize("m", [3, 70, 300])
+def test_gradients_that_are_not_finite_stay_in_their_rows(m):
+    """An infinity in one incoming gradient reaches that token's dx and that
+    column's dW, and nothing else."""
+    n, k, t = 90, 130, torch.bfloat16
+    q, sx = u8.quantize_ref(u8.tokens(m, k, seed=1))
+    wg, sg = u8.weight(n, k, seed=2)
+    wu, su = u8.weight(n, k, seed=3)
+    qc = u8.codes(m, k, torch.Generator().manual_seed(0))
+    qc.copy_(q)
+    dy = grad_in(m, n, 4, t)
+    dy[m // 2, 7] = math.inf
+    args = (u8.cuda(qc), sx.cuda(), u8.cuda(wg), sg.cuda())
+    dx, dw = qmm.w8a8_gemm_backward(dy.cuda(), *args)
+    gx, gw, uw = qmm.w8a8_gated_backward(dy.cuda(), *args, u8.cuda(wu), su.cuda())
+    for o, bad in ((dx, m // 2), (gx, m // 2), (dw, 7), (gw, 7), (uw, 7)):
+        fine = torch.isfinite(o).all(1)
+        assert not fine[bad] and int(fine.sum()) == o.shape[0] - 1
+
+
+@pytest.mark.parametrize("m", [1, 65])
+def test_infinite_scale_stays_in_its_column(m):
+    """An up projection's infinite scale: du of that column is finite, and so is dWu;
+    dWg of it is infinite with the sign of its sum (every term has it), not NaN for the
+    tokens that only pad a tile."""
+    n, k, t = 20, 16, torch.bfloat16
+    q = torch.full((m, k), 5, dtype=torch.int8)
+    sx = torch.full((m,), 0.125)
+    wg = torch.ones((n, k), dtype=torch.int8)
+    sw = torch.full((n,), 0.25)
+    su = sw.clone()
+    su[7] = math.inf
+    dh = torch.full((m, n), 0.5, dtype=t)
+    dx, gw, uw = qmm.w8a8_gated_backward(dh.cuda(), q.cuda(), sx.cuda(), wg.cuda(), sw.cuda(), wg.cuda(),
+                                         su.cuda())
+    assert torch.isfinite(uw).all() and not torch.isfinite(dx).any()
+    fine = torch.isfinite(gw).all(1)
+    assert int(fine.sum()) == n - 1 and (gw[7] == math.inf).all()
+
+
 def test_backward_small_scales_in_fp16():
     """Scales of 1e-7: dy sw would be subnormal in fp16 without the power of two."""
     m, n, k, t = 40, 64, 64, torch.float16
