@@ -173,11 +173,11 @@ BackwardPlan plan_backward(int M, int N, int K, bool gated, bool weight_grad) {
   p.d = put((int64_t)M * p.Jp);
   if (weight_grad) p.dt = put(p.parts * p.Nr * p.Mp);
   // fp32 sums of a product whose contraction is split; dx and dW in turn
-  p.dx_splits = plain_splits(M, K, 2 * p.Jp);
-  p.dw_splits = weight_grad ? plain_splits(p.parts * p.Nr, K, 2 * p.Mp) : 1;
+  p.dx = plain_plan(M, K, 2 * p.Jp);
+  p.dw = plain_plan(p.parts * p.Nr, K, 2 * p.Mp);
   const int64_t ld = round_up(K, 4);
-  const int64_t px = p.dx_splits > 1 ? p.dx_splits * M * ld : 0;
-  const int64_t pw = p.dw_splits > 1 ? p.dw_splits * p.parts * p.Nr * ld : 0;
+  const int64_t px = p.dx.splits > 1 ? p.dx.splits * M * ld : 0;
+  const int64_t pw = weight_grad && p.dw.splits > 1 ? p.dw.splits * p.parts * p.Nr * ld : 0;
   p.part = put(2 * (px > pw ? px : pw));
   p.bytes = at;
   return p;
@@ -229,7 +229,7 @@ static hipError_t backward(const BackwardArgs& a, const BackwardPlan& p) {
   t.kb = (int)(2 * p.Jp);
   t.scal = scal + 1;
   t.part = reinterpret_cast<float*>(ws + p.part);
-  t.splits = p.dx_splits;
+  t.plan = p.dx;
   t.y = a.dx;
   t.y_dtype = DT;
   t.ldy = a.lddx;
@@ -246,7 +246,7 @@ static hipError_t backward(const BackwardArgs& a, const BackwardPlan& p) {
   t.Mv = a.N;
   t.kb = (int)(2 * p.Mp);
   t.scal = scal + 3;
-  t.splits = p.dw_splits;
+  t.plan = p.dw;
   t.y = a.dw[0];
   t.y2 = a.dw[1];
   t.ldy = a.lddw;

@@ -53,11 +53,18 @@ hipError_t launch_rows(const W8A8Args& a, const void* x, int x_dtype, int64_t ld
 //   dt     (parts * Nr, Mp) dy sx c2 transposed (rows N .. Nr of a part unused)
 //   part   fp32 shares of dx's product or dW's, where K is split
 // with the contracted axes zero-padded to whole stages.
+// How launch_tile_plain makes a product: tiles of 32 w (8 or 4), the contraction in
+// `splits` shares (1: whole; more with w = 4 alone).
+struct PlainPlan {
+  int w, splits;
+};
+PlainPlan plain_plan(int64_t M, int64_t N, int64_t kb);
+
 struct BackwardPlan {
   int parts;
   int64_t Np, Jp, Nr, Mp;
   size_t scal, d, dt, part, bytes;
-  int dx_splits, dw_splits;
+  PlainPlan dx, dw;
 };
 BackwardPlan plan_backward(int M, int N, int K, bool gated, bool weight_grad);
 
@@ -111,13 +118,11 @@ struct TileArgs {
   void* d;             // (M, 2 Np)
   void* dt;            // (2 Nr, Mp) or NULL
   int64_t Np, Nr, Mp;
-  // plain, few tiles: K in `splits` shares, their fp32 sums in part (splits, M, N
-  // rounded up to 4), added in a fixed order by a second launch
+  // plain: the shares' fp32 sums, where K is split, lie in part (splits, M, N rounded
+  // up to 4) and are added in a fixed order by a second launch
+  PlainPlan plan;
   float* part;
-  int splits;
 };
-// Shares of K that launch_tile_plain wants for a product of this size (1: none).
-int plain_splits(int64_t M, int64_t N, int64_t kb);
 hipError_t launch_tile_scale(const TileArgs& t, hipStream_t s);
 hipError_t launch_tile_gated(const TileArgs& t, hipStream_t s);
 hipError_t launch_tile_grad(const TileArgs& t, int dtype, hipStream_t s);

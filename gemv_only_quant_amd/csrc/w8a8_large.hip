@@ -398,15 +398,20 @@ static int64_t tiles_of(int64_t m, int64_t n, bool pair, int w) {
   return ((m + rows - 1) / rows) * ((n + cols - 1) / cols);
 }
 
-// Whether 256 x 256 tiles serve a product better than 128 x 128 ones, in units
-// of the time of a round of the former (K = 4096: 54 us).  Of the latter a CU
-// runs two at once (42 us together), or where there are at most 256, one with
-// twice the stages in flight (24 us).  So 1024 x 4096 x 4096 takes 25 us and not
-// 54, 512 x 4096 x 11008 42 and not 56, 1024 x 4096 x 11008 56 and not 73.
-static bool large_tiles(int64_t m, int64_t n, bool pair) {
+// Whether 256 x 256 tiles serve a product of codes better than 128 x 128 ones, by
+// the time in us that its tiles take, st stages each: of the former a CU runs one, in
+// rounds; of the latter two at once, or in the last round and where there are at
+// most 256, one, with twice the stages in flight.  (us, 256 / 128: 4096 x 4096 x
+// 11008 169 / 190, 1024 x 4096 x 11008 55 / 59; 2048 x 4096 x 8448 104 / 90, gated
+// 4096 x 512 x 11008 141 / 110, 512 x 11008 x 4096 103 / 44.)
+static bool large_tiles(int64_t m, int64_t n, bool pair, int64_t kb) {
   const int64_t t8 = tiles_of(m, n, pair, 8), t4 = tiles_of(m, n, pair, 4);
-  const double small = t4 <= 256 ? 0.45 : 0.77 * (double)((t4 + 511) / 512);
-  return (double)((t8 + 255) / 256) <= small;
+  const double st = (double)((kb + kStageBytes - 1) / kStageBytes);
+  const double two = 2 * (0.43 * st + 3.6), one = 0.6 * st + 4;
+  const int64_t last = t4 % 512;
+  const double large = (double)((t8 + 255) / 256) * (1.17 * st + 17.7);
+  const double small = 3 + (double)(t4 / 512) * two + (last == 0 ? 0 : last <= 256 ? one : two);
+  return large <= small;
 }
 
 template <int KIND, int EPI, int W, int NB, int DT>
@@ -416,8 +421,8 @@ static hipError_t launch_w(const TileArgs& t, int64_t m, int64_t n, hipStream_t 
   const int64_t m_tiles = (m + rows - 1) / rows;
   int per = 0;
   if constexpr (EPI == EPI_PARTIAL) {
-    per = (t.kb / kStageBytes + t.splits - 1) / t.splits;
-    n_tiles *= t.splits;
+    per = (t.kb / kStageBytes + t.plan.splits - 1) / t.plan.splits;
+    n_tiles *= t.plan.splits;
   }
   if (n_tiles * m_tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
   return launch_kernel(large_kernel<KIND, EPI, W, NB, DT>, dim3((unsigned)(n_tiles * m_tiles)), dim3(256),
@@ -429,9 +434,8 @@ static hipError_t launch(const TileArgs& t, hipStream_t s) {
   // the gradient epilogue also writes the padding of its operands
   const int64_t n = EPI == EPI_GRAD ? t.Np : t.N;
   const int64_t m = EPI == EPI_GRAD && t.dt != nullptr ? t.Mp : t.M;
-  if constexpr (EPI == EPI_PARTIAL) return launch_w<KIND, EPI, 8, 2, DT>(t, m, n, s);
   constexpr bool pair = EPI == EPI_GATED || EPI == EPI_GRAD;
-  if (large_tiles(m, n, pair)) return launch_w<KIND, EPI, 8, 2, DT>(t, m, n, s);
+  if (large_tiles(m, n, pair, t.kb)) return launch_w<KIND, EPI, 8, 2, DT>(t, m, n, s);
   return tiles_of(m, n, pair, 4) <= 256 ? launch_w<KIND, EPI, 4, 4, DT>(t, m, n, s)
                                         : launch_w<KIND, EPI, 4, 2, DT>(t, m, n, s);
 }
@@ -457,7 +461,7 @@ __global__ __launch_bounds__(256) void sum_partials_kernel(TileArgs t, int block
   if (n >= t.N || mo >= t.Mv) return;
   const int64_t ld = round_up(t.N, 4), at = (int64_t)m * ld + n;
   f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < t.splits; ++s)
+  for (int s = 0; s < t.plan.splits; ++s)
     v += *reinterpret_cast<const f32x4_t*>(t.part + s * (int64_t)t.M * ld + at);
   const float k = *t.scal;
   T* y = static_cast<T*>(second ? t.y2 : t.y) + (int64_t)mo * t.ldy + n;
@@ -465,31 +469,47 @@ __global__ __launch_bounds__(256) void sum_partials_kernel(TileArgs t, int block
   store4(y, o, min(4, t.N - n), vec4_ok(second ? t.y2 : t.y, t.ldy, 2));
 }
 
-int plain_splits(int64_t M, int64_t N, int64_t kb) {
-  const int64_t tiles = tiles_of(M, N, false, 8);
-  // shares of K that fill the CUs, none of them under 16 stages (1024 values)
-  int64_t s = 256 / tiles;
-  s = s < kb / kStageBytes / 16 ? s : kb / kStageBytes / 16;
-  if (s < 2) return 1;
-  // the same number of stages in all but the last, which is not empty
-  const int64_t per = (kb / kStageBytes + s - 1) / s;
-  return (int)((kb / kStageBytes + per - 1) / per);
+// By the time in us that either way takes.  256 x 256 tiles, in rounds of 256, are the
+// faster ones where many stages fill whole rounds (4096 x 4096 x 22016 contracted:
+// 683 against 809 us, 8192 x 4096 x 11008 639 against 721); of 128 x 128 tiles two or
+// more run on a CU, one's epilogue beside another's products, and the last of them
+// are not waited for as long (22016 x 4096 x 512 131 against 178 us, 8192 x 8192 x
+// 1024 145 against 167, 4096 x 11008 x 4096 331 against 342).  Where they leave CUs
+// idle the contraction is split, at the price of writing and adding fp32 sums (128 x
+// 4096 x 22016 254 -> 46 us with 16 shares, 2048 x 1024 x 14336 191 -> 92 with 4, 64
+// x 2048 x 2048 33 -> 19 with 8; 2048 x 2048 x 300 not: 18 -> 32 with 2).
+PlainPlan plain_plan(int64_t M, int64_t N, int64_t kb) {
+  const int64_t all = kb / kStageBytes, t8 = tiles_of(M, N, false, 8), t4 = tiles_of(M, N, false, 4);
+  const double large = (double)((t8 + 255) / 256) * (1.8 * (double)all + 9);
+  PlainPlan p{8, 1};
+  double best = large;
+  for (int64_t s = 1; s <= 32 && (s == 1 || (t4 * s <= 512 && 3 * s <= all)); ++s) {
+    // the same number of stages in all shares but the last, which is not empty
+    const int64_t per = (all + s - 1) / s, shares = (all + per - 1) / per, wgs = t4 * shares;
+    const double turns = wgs < 512 ? 2 : (double)wgs / 256;
+    double us = wgs <= 256 ? 0.8 * (double)per + 2 : turns * (0.52 * (double)per + 1);
+    if (shares > 1) us += 5 + (double)(shares * M * N) * 1e-6;
+    if (us < best) best = us, p = PlainPlan{4, (int)shares};
+  }
+  return p;
+}
+
+template <int DT> static hipError_t tile_plain(const TileArgs& t, hipStream_t s) {
+  if (t.plan.splits == 1)
+    return t.plan.w == 8 ? launch_w<DT, EPI_PLAIN, 8, 2, DT>(t, t.M, t.N, s)
+                         : launch_w<DT, EPI_PLAIN, 4, 2, DT>(t, t.M, t.N, s);
+  TileArgs p = t;
+  p.y = t.part;
+  p.ldy = round_up(t.N, 4);
+  p.y_dtype = YF32;
+  const hipError_t e = launch_w<DT, EPI_PARTIAL, 4, 2, DT>(p, t.M, t.N, s);
+  if (e != hipSuccess) return e;
+  const int bpr = (t.N + 1023) / 1024;
+  return launch_kernel(sum_partials_kernel<DT>, dim3((unsigned)((int64_t)t.M * bpr)), dim3(256), s, t, bpr);
 }
 
 hipError_t launch_tile_plain(const TileArgs& t, int dtype, hipStream_t s) {
-  if (t.splits > 1) {
-    TileArgs p = t;
-    p.y = t.part;
-    p.ldy = round_up(t.N, 4);
-    p.y_dtype = YF32;
-    hipError_t e = dtype == XF16 ? launch<XF16, EPI_PARTIAL, XF16>(p, s) : launch<XBF16, EPI_PARTIAL, XBF16>(p, s);
-    if (e != hipSuccess) return e;
-    const int bpr = (t.N + 1023) / 1024;
-    const dim3 grid((unsigned)((int64_t)t.M * bpr));
-    return dtype == XF16 ? launch_kernel(sum_partials_kernel<XF16>, grid, dim3(256), s, t, bpr)
-                         : launch_kernel(sum_partials_kernel<XBF16>, grid, dim3(256), s, t, bpr);
-  }
-  return dtype == XF16 ? launch<XF16, EPI_PLAIN, XF16>(t, s) : launch<XBF16, EPI_PLAIN, XBF16>(t, s);
+  return dtype == XF16 ? tile_plain<XF16>(t, s) : tile_plain<XBF16>(t, s);
 }
 
 }  // namespace qmm

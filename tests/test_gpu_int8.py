@@ -336,6 +336,24 @@ def test_gemm_backward_against_differences():
         assert (_along(f, v) - have).abs() <= (b * v.abs()).sum() + 1e-6 * (o.double().cpu() * v).abs().sum()
 
 
+# whole rounds of 256 x 256 tiles: of g and u made again; of dx (the contraction over
+# both weights); of dW (the rows of both)
+@pytest.mark.parametrize("m,n,k,t", [(4000, 2000, 1000, "bf16"), (4000, 650, 4090, "fp16"),
+                                     (1300, 2000, 4090, "bf16")])
+def test_gated_backward_in_the_largest_tiles(m, n, k, t):
+    test_gated_backward(m, n, k, "silu", t)
+
+
+@pytest.mark.parametrize("m,n,k,t", [(4000, 1300, 4090, "bf16"), (1300, 4000, 4090, "fp16")])
+def test_gemm_backward_in_the_largest_tiles(m, n, k, t):
+    test_gemm_backward(m, n, k, t)
+
+
+def test_forward_in_the_largest_tiles():
+    test_gemm(4090, 4000, 1000, "codes", "bf16")
+    test_gated(4090, 2000, 1000, "silu", "codes", "fp32")
+
+
 @pytest.mark.parametrize("m", [3, 70, 300])
 def test_gradients_that_are_not_finite_stay_in_their_rows(m):
     """An infinity in one incoming gradient reaches that token's dx and that
