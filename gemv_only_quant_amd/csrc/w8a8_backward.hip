@@ -11,9 +11,11 @@
 // time at 4096 tokens and a quarter at 512).  c1 and c2 are the powers of two that
 // bring the largest weight (token) scale to [1/2, 1): with scales of 1e-3 and fp16
 // gradients the products would else lie among its subnormals.  They leave again,
-// exactly, as the fp32 sums are stored.
+// exactly, as the fp32 sums are stored.  bf16 has fp32's range: there both are 1, and
+// neither the launch that finds them nor the factors are needed (4096 tokens: linear
+// 11008 x 4096 692 -> 663 us, gated 4096 x 11008 1763 -> 1709).
 //
-// Steps: the powers of two (one workgroup); D and Dt -- from dy by scaling, or for
+// Steps: the powers of two (fp16, one workgroup); D and Dt -- from dy by scaling, or for
 // the gated block by the gradient epilogue of the int8 product, which makes g and u
 // again; then the two products.
 #include <type_traits>
@@ -89,7 +91,7 @@ __global__ __launch_bounds__(256) void scale_grad_kernel(
   const int tid = threadIdx.x;
   const T* src = static_cast<const T*>(dy);
   const bool vec = vec4_ok(dy, lddy, 2);
-  const float c1 = scal[0], c2 = scal[2];
+  const float c1 = DT == XF16 ? scal[0] : 1.f, c2 = DT == XF16 ? scal[2] : 1.f;
   const int col = 4 * (tid & 15), n = n0 + col;
   float s[4];
 #pragma unroll
@@ -188,8 +190,10 @@ static hipError_t backward(const BackwardArgs& a, const BackwardPlan& p) {
   char* ws = static_cast<char*>(a.ws);
   float* scal = reinterpret_cast<float*>(ws + p.scal);
   const bool wgrad = a.dw[0] != nullptr;
-  hipError_t e = launch_kernel(scale_powers_kernel, dim3(1), dim3(1024), a.stream, a.sw[0],
-                               a.gated ? a.sw[1] : nullptr, wgrad ? a.sx : nullptr, a.N, a.M, scal);
+  hipError_t e = hipSuccess;
+  if (DT == XF16)
+    e = launch_kernel(scale_powers_kernel, dim3(1), dim3(1024), a.stream, a.sw[0],
+                      a.gated ? a.sw[1] : nullptr, wgrad ? a.sx : nullptr, a.N, a.M, scal);
   if (e != hipSuccess) return e;
   if (a.gated) {
     TileArgs t{};

@@ -48,7 +48,8 @@ hipError_t launch_rows(const W8A8Args& a, const void* x, int x_dtype, int64_t ld
 
 // ---- gradients -------------------------------------------------------------
 // What a backward pass keeps in its workspace; offsets in bytes.
-//   scal   4 floats: c1, 1 / c1, c2, 1 / c2 (powers of two, see w8a8_backward.hip)
+//   scal   4 floats: c1, 1 / c1, c2, 1 / c2 (powers of two, fp16 alone, see
+//          w8a8_backward.hip)
 //   d      (M, Jp) dy sw c1 (gated: dg sg c1 | du su c1), Jp = parts * Np
 //   dt     (parts * Nr, Mp) dy sx c2 transposed (rows N .. Nr of a part unused)
 //   part   fp32 shares of dx's product or dW's, where K is split
@@ -105,7 +106,7 @@ struct TileArgs {
   int M, N, kb;
   const float* sa;     // scale of each row of A (int8)
   const float* sb[2];  // scale of each row of B (int8)
-  const float* scal;   // plain: C is multiplied by *scal
+  const float* scal;   // plain: C is multiplied by *scal (fp16)
   void* y;
   int y_dtype;
   int64_t ldy;

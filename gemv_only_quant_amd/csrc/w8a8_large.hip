@@ -450,7 +450,7 @@ hipError_t launch_tile_grad(const TileArgs& t, int dtype, hipStream_t s) {
   return dtype == XF16 ? launch<kTypeI8, EPI_GRAD, XF16>(t, s) : launch<kTypeI8, EPI_GRAD, XBF16>(t, s);
 }
 
-// y = (sum of the partial products) *scal, rounded once; 4 columns per thread.
+// y = (sum of the partial products) *scal (fp16), rounded once; 4 columns per thread.
 template <int DT>
 __global__ __launch_bounds__(256) void sum_partials_kernel(TileArgs t, int blocks_per_row) {
   typedef typename Half16<DT>::type T;
@@ -463,7 +463,7 @@ __global__ __launch_bounds__(256) void sum_partials_kernel(TileArgs t, int block
   f32x4_t v = {0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < t.plan.splits; ++s)
     v += *reinterpret_cast<const f32x4_t*>(t.part + s * (int64_t)t.M * ld + at);
-  const float k = *t.scal;
+  const float k = DT == XF16 ? *t.scal : 1.f;
   T* y = static_cast<T*>(second ? t.y2 : t.y) + (int64_t)mo * t.ldy + n;
   const float o[4] = {v[0] * k, v[1] * k, v[2] * k, v[3] * k};
   store4(y, o, min(4, t.N - n), vec4_ok(second ? t.y2 : t.y, t.ldy, 2));

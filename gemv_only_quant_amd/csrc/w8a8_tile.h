@@ -73,7 +73,7 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
     lane = lane_, n0 = n0_;
     col = 4 * (lane % LPR), n = n0 + col, nn = min(4, g.N - n);
     if constexpr (EPI == EPI_PLAIN) {
-      k1 = *g.scal;
+      k1 = DT == XF16 ? *g.scal : 1.f;
     } else if constexpr (EPI != EPI_PARTIAL) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -82,7 +82,7 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
       }
     }
     if constexpr (EPI == EPI_GRAD) {
-      k1 = g.scal[0], k2 = g.scal[2];
+      k1 = DT == XF16 ? g.scal[0] : 1.f, k2 = DT == XF16 ? g.scal[2] : 1.f;
       vec = vec4_ok(g.dh, g.lddh, 2);
     } else {
       vec = vec4_ok(g.y, g.ldy, g.y_dtype == YF32 ? 4 : 2) && (EPI != EPI_PLAIN || vec4_ok(g.y2, 0, 2));

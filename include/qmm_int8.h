@@ -109,8 +109,8 @@ QMM_API size_t qmm_w8a8_backward_workspace_bytes(int M, int N, int K, int gated,
  * both of dy's type (QMM_F16 or QMM_BF16).  dx[m][k] = sum_n dy[m][n] sw[n]
  * W[n][k]; dW[n][k] = sum_m dy[m][n] sx[m] xq[m][k].  Products are formed on
  * the matrix cores from operands of dy's type (the codes are exact in it;
- * dy sw and dy sx are each rounded to it once, after a power of two has been
- * taken out of the scales, so that small scales do not leave fp16's range),
+ * dy sw and dy sx are each rounded to it once, in fp16 after a power of two has
+ * been taken out of the scales, so that small ones do not leave its range),
  * summed in fp32 and rounded once.  sx and xq are read for dW alone and may be
  * NULL without it.
  */
