@@ -73,6 +73,47 @@ template <int DT> struct Half16;
 template <> struct Half16<XF16> { typedef _Float16 type; };
 template <> struct Half16<XBF16> { typedef __bf16 type; };
 
+// ---- powers of two of fp16 operands -----------------------------------------
+// Values that become fp16 operands are first multiplied by a power of two that their
+// own block shares.  A block's level e is the exponent field of its largest magnitude
+// (of an infinity 255, a NaN counts for nothing), rounded up to 7 mod 8, at least 31:
+// the power 2^(141 - e) brings the largest value to [2^7, 2^15), where 21 binary digits
+// below it are still normal numbers.  Steps of 8 because blocks of one row whose levels
+// agree need not be touched again (w8a8_backward.hip).
+__device__ __forceinline__ uint32_t level_of(float top) {
+  const uint32_t e = (__builtin_bit_cast(uint32_t, top) >> 23) | 7u;
+  return e < 31u ? 31u : e;
+}
+__device__ __forceinline__ float level_power(uint32_t e) {
+  return __builtin_bit_cast(float, (268u - e) << 23);
+}
+__device__ __forceinline__ float level_inverse(uint32_t e) {
+  return __builtin_bit_cast(float, (e - 14u) << 23);
+}
+
+// Largest of the values of 8 (16) consecutive lanes, in each of them.
+template <int CTRL> __device__ __forceinline__ float dpp_max(float v) {
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false);
+  return fmaxf(v, __builtin_bit_cast(float, o));
+}
+template <int LANES> __device__ __forceinline__ float lanes_max(float v) {
+  static_assert(LANES == 8 || LANES == 16, "lanes of a DPP row");
+  v = dpp_max<0xB1>(v);                     // quad_perm [1,0,3,2]
+  v = dpp_max<0x4E>(v);                     // quad_perm [2,3,0,1]
+  v = dpp_max<0x141>(v);                    // row_half_mirror
+  if (LANES == 16) v = dpp_max<0x128>(v);   // row_ror:8
+  return v;
+}
+// Largest over the wave's 4 rows of 16 lanes at each lane position, by two lane
+// swaps (as rows4_sum).
+__device__ __forceinline__ float rows4_max(float v) {
+  float a0 = v, a1 = v;
+  asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(a0), "+v"(a1));
+  float c0 = fmaxf(a0, a1), c1 = c0;
+  asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(c0), "+v"(c1));
+  return fmaxf(c0, c1);
+}
+
 // 4 consecutive values stored as the output type: one store where `vec`
 // says that the address is aligned and all 4 exist, else one by one up to n.
 template <class T>

@@ -19,6 +19,8 @@ __host__ __device__ constexpr int64_t round_up(int64_t v, int64_t to) {
 // Bytes of contraction per stage of the tile kernels: operands that the library
 // lays out itself are zero-padded to whole stages.
 constexpr int kStageBytes = 128;
+// Columns of the gradients' operands that share a level (fp16): of d and of dt.
+constexpr int kLevelD = 32, kLevelT = 16;
 
 // ---- per-token quantizer (w8a8_quantize.hip) -------------------------------
 hipError_t launch_quantize_tokens(const void* x, int x_dtype, int64_t ldx, int8_t* xq,
@@ -48,10 +50,13 @@ hipError_t launch_rows(const W8A8Args& a, const void* x, int x_dtype, int64_t ld
 
 // ---- gradients -------------------------------------------------------------
 // What a backward pass keeps in its workspace; offsets in bytes.
-//   scal   4 floats: c1, 1 / c1, c2, 1 / c2 (powers of two, fp16 alone, see
+//   d      (M, Jp) dy sw (gated: dg sg | du su), Jp = parts * Np
+//   dt     (parts * Nr, Mp) dy sx transposed (rows N .. Nr of a part unused)
+//   de, dte  fp16: the level of each kLevelD columns of d (one for all parts: (M, Np /
+//          kLevelD) bytes) and of each kLevelT columns of dt ((parts * Nr, Mp / kLevelT))
+//   inv, invt  fp16: what the products' rows are multiplied by, (M) and (parts * Nr)
+//   scal   gated, fp16: 4 floats, c1, 1 / c1, c2, 1 / c2 (powers of two, see
 //          w8a8_backward.hip)
-//   d      (M, Jp) dy sw c1 (gated: dg sg c1 | du su c1), Jp = parts * Np
-//   dt     (parts * Nr, Mp) dy sx c2 transposed (rows N .. Nr of a part unused)
 //   part   fp32 shares of dx's product or dW's, where K is split
 // with the contracted axes zero-padded to whole stages.
 // How launch_tile_plain makes a product: tiles of 32 w (8 or 4), the contraction in
@@ -64,7 +69,7 @@ PlainPlan plain_plan(int64_t M, int64_t N, int64_t kb);
 struct BackwardPlan {
   int parts;
   int64_t Np, Jp, Nr, Mp;
-  size_t scal, d, dt, part, bytes;
+  size_t scal, d, dt, de, dte, inv, invt, part, bytes;
   PlainPlan dx, dw;
 };
 BackwardPlan plan_backward(int M, int N, int K, bool gated, bool weight_grad);
@@ -104,9 +109,9 @@ struct TileArgs {
   int64_t ldb;         // contracted axis their rows, each padded to bpad of it
   int brows, bpad;
   int M, N, kb;
-  const float* sa;     // scale of each row of A (int8)
+  const float* sa;     // scale of each row of A (int8), factor of each row of C (plain, fp16)
   const float* sb[2];  // scale of each row of B (int8)
-  const float* scal;   // plain: C is multiplied by *scal (fp16)
+  const float* scal;   // plain, fp16, where sa is NULL: factor of C
   void* y;
   int y_dtype;
   int64_t ldy;

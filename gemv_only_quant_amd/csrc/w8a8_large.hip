@@ -7,7 +7,7 @@
 //   GATED    h = act(g) u for two products g, u of the same left operand
 //   GRAD     dg = dh u act'(g), du = dh act(g), left as 16-bit operands of the
 //            gradients' products, once row-major and once transposed
-//   PLAIN    y = C * (a power of two), 16-bit
+//   PLAIN    y = C (fp16: times a power of two for each row), 16-bit
 //   PARTIAL  fp32 sums of a share of the contraction, added by a second launch
 //
 // Tiles of 256 x 256 (W = 8), bound by the matrix cores (2.7e15 operations/s of int8
@@ -256,7 +256,7 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   };
 
   float* sa = reinterpret_cast<float*>(lds + L::SCALES);
-  row_scales<EPI>(g, sa, m0, TILE);
+  row_scales<EPI, DT>(g, sa, m0, TILE);
 
   typedef typename Acc<KIND>::type acc_t;
   acc_t acc[MT][NT];
@@ -450,7 +450,8 @@ hipError_t launch_tile_grad(const TileArgs& t, int dtype, hipStream_t s) {
   return dtype == XF16 ? launch<kTypeI8, EPI_GRAD, XF16>(t, s) : launch<kTypeI8, EPI_GRAD, XBF16>(t, s);
 }
 
-// y = (sum of the partial products) *scal (fp16), rounded once; 4 columns per thread.
+// y = the sum of the partial products (fp16: times the row's factor), rounded once; 4
+// columns per thread.
 template <int DT>
 __global__ __launch_bounds__(256) void sum_partials_kernel(TileArgs t, int blocks_per_row) {
   typedef typename Half16<DT>::type T;
@@ -463,7 +464,7 @@ __global__ __launch_bounds__(256) void sum_partials_kernel(TileArgs t, int block
   f32x4_t v = {0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < t.plan.splits; ++s)
     v += *reinterpret_cast<const f32x4_t*>(t.part + s * (int64_t)t.M * ld + at);
-  const float k = DT == XF16 ? *t.scal : 1.f;
+  const float k = DT != XF16 ? 1.f : t.sa != nullptr ? t.sa[m] : *t.scal;
   T* y = static_cast<T*>(second ? t.y2 : t.y) + (int64_t)mo * t.ldy + n;
   const float o[4] = {v[0] * k, v[1] * k, v[2] * k, v[3] * k};
   store4(y, o, min(4, t.N - n), vec4_ok(second ? t.y2 : t.y, t.ldy, 2));

@@ -65,16 +65,14 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
 
   int lane, col, n0, n, nn;  // nn: columns of this lane that exist (may be <= 0)
   float s0[4], s1[4];        // column scales; of the up projection
-  float k1, k2;              // PLAIN: the factor; GRAD: c1, c2
+  float k1, k2;              // GRAD: c1, c2
   bool vec;
   uint16_t dh[EPI == EPI_GRAD ? PASSES : 1][4];  // the next tile's incoming gradient
 
   __device__ __forceinline__ void init(const TileArgs& g, int n0_, int lane_) {
     lane = lane_, n0 = n0_;
     col = 4 * (lane % LPR), n = n0 + col, nn = min(4, g.N - n);
-    if constexpr (EPI == EPI_PLAIN) {
-      k1 = DT == XF16 ? *g.scal : 1.f;
-    } else if constexpr (EPI != EPI_PARTIAL) {
+    if constexpr (EPI != EPI_PLAIN && EPI != EPI_PARTIAL) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         s0[j] = j < nn ? g.sb[0][n + j] : 0.f;
@@ -129,8 +127,9 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
         const int row = RPP * p + lane / LPR;
         const acc_t c = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, col));
         if constexpr (EPI == EPI_PLAIN) {
+          const float k = DT == XF16 ? sa[row] : 1.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[p][j] = c[j] * k1;
+          for (int j = 0; j < 4; ++j) v[p][j] = c[j] * k;
         } else if constexpr (EPI == EPI_SCALE) {
           const float a = sa[row];
 #pragma unroll
@@ -240,11 +239,15 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
   }
 };
 
-// The workgroup's row scales to LDS (0 for rows past M).
-template <int EPI>
+// The workgroup's row scales (plain, fp16: row factors) to LDS (0 for rows past M).
+template <int EPI, int DT>
 __device__ __forceinline__ void row_scales(const TileArgs& g, float* sa, int m0, int rows) {
-  if constexpr (EPI != EPI_PLAIN && EPI != EPI_PARTIAL)
-    for (int i = threadIdx.x; i < rows; i += 256) sa[i] = m0 + i < g.M ? g.sa[m0 + i] : 0.f;
+  if constexpr (EPI == EPI_PARTIAL || (EPI == EPI_PLAIN && DT != XF16)) return;
+  if (EPI == EPI_PLAIN && g.sa == nullptr) {
+    for (int i = threadIdx.x; i < rows; i += 256) sa[i] = *g.scal;
+    return;
+  }
+  for (int i = threadIdx.x; i < rows; i += 256) sa[i] = m0 + i < g.M ? g.sa[m0 + i] : 0.f;
 }
 
 // Tile of work item b of n_tiles x m_tiles: consecutive items on one XCD (the

@@ -109,10 +109,11 @@ QMM_API size_t qmm_w8a8_backward_workspace_bytes(int M, int N, int K, int gated,
  * both of dy's type (QMM_F16 or QMM_BF16).  dx[m][k] = sum_n dy[m][n] sw[n]
  * W[n][k]; dW[n][k] = sum_m dy[m][n] sx[m] xq[m][k].  Products are formed on
  * the matrix cores from operands of dy's type (the codes are exact in it;
- * dy sw and dy sx are each rounded to it once, in fp16 after a power of two has
- * been taken out of the scales, so that small ones do not leave its range),
- * summed in fp32 and rounded once.  sx and xq are read for dW alone and may be
- * NULL without it.
+ * dy sw and dy sx are each rounded to it once), summed in fp32 and rounded once.
+ * In fp16 each token's dy sw, and each channel's dy sx, has a power of two of its
+ * own, taken out of its sums again: none leaves the range, and next to a row's
+ * largest value the others lose less than 2^-30 of it beside their rounding.  sx
+ * and xq are read for dW alone and may be NULL without it.
  */
 QMM_API qmm_status qmm_w8a8_gemm_backward(const void* dy, int dtype, int64_t lddy,
                                           const int8_t* xq, int64_t ldx, const float* sx,
@@ -126,7 +127,8 @@ QMM_API qmm_status qmm_w8a8_gemm_backward(const void* dy, int dtype, int64_t ldd
  * (both or neither), dWg and dWu (N, K), all of dh's type.  g and u are made
  * again from the codes (exact sums, fp32), so the forward pass keeps nothing
  * of size M x N.  dg and du are formed in fp32; dg sg, du su, dg sx and du sx
- * are rounded to dh's type as above.
+ * are rounded to dh's type once, in fp16 after a power of two has been taken out of
+ * the scales.
  */
 QMM_API qmm_status qmm_w8a8_gated_backward(const void* dh, int dtype, int64_t lddh,
                                            const int8_t* xq, int64_t ldx, const float* sx,
