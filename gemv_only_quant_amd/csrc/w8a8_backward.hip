@@ -16,11 +16,10 @@
 // by its largest value, which leaves again, exactly, as the fp32 sums are stored.  The
 // kernels that make the operands know no more of a row than a block; they take the
 // block's power and note it as a level, and a second launch brings a row's blocks to one
-// level (what this costs beside one power for all rows, found from the scales alone: dx
-// 512 x 11008 x 4096 73.4 -> 74.3 us, both gradients 4096 x 11008 x 4096 689 -> 698).
-//
-// The gated block still takes powers from its scales alone: c1 (c2) brings the largest
-// weight (token) scale to [1/2, 1).
+// level.  What this costs beside one power for all rows, found from the scales alone (which
+// loses such rows, and dg beyond 65504): dx 512 x 11008 x 4096 73.4 -> 74.3 us, both gradients
+// 4096 x 11008 x 4096 689 -> 698; gated, dx 509 x 4096 x 11008 185 -> 185, all three at 64
+// tokens 115 -> 122, at 4096 1720 -> 1780.
 //
 // Steps: D and Dt -- from dy by scaling, or for the gated block by the gradient epilogue
 // of the int8 product, which makes g and u again; their levels (fp16); then the two
@@ -30,56 +29,6 @@
 #include "w8a8_device.h"
 
 namespace qmm {
-
-// out[0..3] = c1, 1 / c1, c2, 1 / c2 with c a power of two, c max |scale| in
-// [1/2, 1).  1 where the scales are all zero or not finite.
-__global__ __launch_bounds__(1024) void scale_powers_kernel(const float* __restrict__ s0,
-                                                            const float* __restrict__ s1,
-                                                            const float* __restrict__ sx, int N,
-                                                            int M, float* __restrict__ out) {
-  __shared__ uint32_t part[2][16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t top[2] = {0u, 0u};
-  auto take = [&](const float* p, int n, uint32_t& t) {
-    if (p == nullptr) return;
-    // 8 loads in flight per thread, the last value again past the end (one at a
-    // time 26112 scales take 13.9 us, so 6.8)
-    for (int i0 = threadIdx.x; i0 < n; i0 += 8 * 1024) {
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = p[min(i0 + 1024 * j, n - 1)];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t b = __builtin_bit_cast(uint32_t, v[j]) & 0x7FFFFFFFu;
-        if (b < 0x7F800000u && b > t) t = b;
-      }
-    }
-  };
-  take(s0, N, top[0]);
-  take(s1, N, top[0]);
-  take(sx, M, top[1]);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-      const uint32_t o = (uint32_t)__shfl_xor((int)top[i], d);
-      top[i] = o > top[i] ? o : top[i];
-    }
-    if (lane == 0) part[i][wave] = top[i];
-  }
-  __syncthreads();
-  if (threadIdx.x < 2) {
-    const int i = threadIdx.x;
-    uint32_t t = 0;
-    for (int w = 0; w < 16; ++w) t = part[i][w] > t ? part[i][w] : t;
-    // the exponent field e means [2^(e - 127), 2^(e - 126)); kept where both
-    // powers are normal numbers
-    int e = t == 0 ? 126 : (int)(t >> 23);
-    e = e < 26 ? 26 : (e > 226 ? 226 : e);
-    out[2 * i] = __builtin_bit_cast(float, (uint32_t)(253 - e) << 23);
-    out[2 * i + 1] = __builtin_bit_cast(float, (uint32_t)(e + 1) << 23);
-  }
-}
 
 // dy (M, N) -> d (M, Np) = dy sw and, where dt is not NULL, dt (N, Mp) = (dy sx)^t,
 // both with zeros where they only pad; in fp16 each block times its power of two, whose
@@ -271,7 +220,7 @@ BackwardPlan plan_backward(int M, int N, int K, bool gated, bool weight_grad) {
   p.Jp = p.parts * p.Np;
   p.Nr = round_up(N, 256);
   p.Mp = round_up(M, pad);
-  size_t at = 256;  // scal at 0
+  size_t at = 0;
   auto put = [&](int64_t elements) {
     const size_t here = at;
     at += (size_t)round_up(elements * 2, 256);
@@ -321,14 +270,10 @@ static hipError_t level_operands(const BackwardArgs& a, const BackwardPlan& p, c
 template <int DT>
 static hipError_t backward(const BackwardArgs& a, const BackwardPlan& p) {
   char* ws = static_cast<char*>(a.ws);
-  float* scal = reinterpret_cast<float*>(ws + p.scal);
   const bool wgrad = a.dw[0] != nullptr;
-  hipError_t e = hipSuccess;
-  const bool levels = DT == XF16 && !a.gated;
-  if (DT == XF16 && a.gated)
-    e = launch_kernel(scale_powers_kernel, dim3(1), dim3(1024), a.stream, a.sw[0],
-                      a.gated ? a.sw[1] : nullptr, wgrad ? a.sx : nullptr, a.N, a.M, scal);
-  if (e != hipSuccess) return e;
+  uint8_t* de = reinterpret_cast<uint8_t*>(ws + p.de);
+  uint8_t* dte = wgrad ? reinterpret_cast<uint8_t*>(ws + p.dte) : nullptr;
+  hipError_t e;
   if (a.gated) {
     TileArgs t{};
     t.a = a.x;
@@ -338,12 +283,12 @@ static hipError_t backward(const BackwardArgs& a, const BackwardPlan& p) {
     t.M = a.M, t.N = a.N, t.kb = a.K;
     t.sa = a.sx;
     t.sb[0] = a.sw[0], t.sb[1] = a.sw[1];
-    t.scal = scal;
     t.act = a.act;
     t.dh = a.dy;
     t.lddh = a.lddy;
     t.d = ws + p.d;
     t.dt = wgrad ? ws + p.dt : nullptr;
+    t.de = de, t.dte = dte;
     t.Np = p.Np, t.Nr = p.Nr, t.Mp = p.Mp;
     e = launch_tile_grad(t, DT, a.stream);
   } else {
@@ -352,11 +297,10 @@ static hipError_t backward(const BackwardArgs& a, const BackwardPlan& p) {
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     e = launch_kernel(scale_grad_kernel<DT>, dim3((unsigned)blocks), dim3(256), a.stream, a.dy,
                       a.lddy, a.sw[0], a.sx, ws + p.d, p.Np, wgrad ? ws + p.dt : nullptr, p.Mp,
-                      reinterpret_cast<uint8_t*>(ws + p.de), reinterpret_cast<uint8_t*>(ws + p.dte), a.M, a.N,
-                      n_tiles);
+                      de, dte, a.M, a.N, n_tiles);
   }
   if (e != hipSuccess) return e;
-  if (levels) e = level_operands(a, p, ws);
+  if (DT == XF16) e = level_operands(a, p, ws);
   if (e != hipSuccess) return e;
 
   TileArgs t{};  // dx
@@ -368,8 +312,7 @@ static hipError_t backward(const BackwardArgs& a, const BackwardPlan& p) {
   t.M = t.M2 = t.Mv = a.M;
   t.N = a.K;
   t.kb = (int)(2 * p.Jp);
-  t.scal = scal + 1;
-  t.sa = levels ? reinterpret_cast<const float*>(ws + p.inv) : nullptr;
+  t.sa = reinterpret_cast<const float*>(ws + p.inv);
   t.part = reinterpret_cast<float*>(ws + p.part);
   t.plan = p.dx;
   t.y = a.dx;
@@ -387,8 +330,7 @@ static hipError_t backward(const BackwardArgs& a, const BackwardPlan& p) {
   t.M2 = (int)p.Nr;
   t.Mv = a.N;
   t.kb = (int)(2 * p.Mp);
-  t.scal = scal + 3;
-  t.sa = levels ? reinterpret_cast<const float*>(ws + p.invt) : nullptr;
+  t.sa = reinterpret_cast<const float*>(ws + p.invt);
   t.plan = p.dw;
   t.y = a.dw[0];
   t.y2 = a.dw[1];

@@ -55,8 +55,6 @@ hipError_t launch_rows(const W8A8Args& a, const void* x, int x_dtype, int64_t ld
 //   de, dte  fp16: the level of each kLevelD columns of d (one for all parts: (M, Np /
 //          kLevelD) bytes) and of each kLevelT columns of dt ((parts * Nr, Mp / kLevelT))
 //   inv, invt  fp16: what the products' rows are multiplied by, (M) and (parts * Nr)
-//   scal   gated, fp16: 4 floats, c1, 1 / c1, c2, 1 / c2 (powers of two, see
-//          w8a8_backward.hip)
 //   part   fp32 shares of dx's product or dW's, where K is split
 // with the contracted axes zero-padded to whole stages.
 // How launch_tile_plain makes a product: tiles of 32 w (8 or 4), the contraction in
@@ -69,7 +67,7 @@ PlainPlan plain_plan(int64_t M, int64_t N, int64_t kb);
 struct BackwardPlan {
   int parts;
   int64_t Np, Jp, Nr, Mp;
-  size_t scal, d, dt, de, dte, inv, invt, part, bytes;
+  size_t d, dt, de, dte, inv, invt, part, bytes;
   PlainPlan dx, dw;
 };
 BackwardPlan plan_backward(int M, int N, int K, bool gated, bool weight_grad);
@@ -111,7 +109,6 @@ struct TileArgs {
   int M, N, kb;
   const float* sa;     // scale of each row of A (int8), factor of each row of C (plain, fp16)
   const float* sb[2];  // scale of each row of B (int8)
-  const float* scal;   // plain, fp16, where sa is NULL: factor of C
   void* y;
   int y_dtype;
   int64_t ldy;
@@ -123,6 +120,7 @@ struct TileArgs {
   int64_t lddh;
   void* d;             // (M, 2 Np)
   void* dt;            // (2 Nr, Mp) or NULL
+  uint8_t *de, *dte;   // their levels (fp16)
   int64_t Np, Nr, Mp;
   // plain: the shares' fp32 sums, where K is split, lie in part (splits, M, N rounded
   // up to 4) and are added in a fixed order by a second launch

@@ -367,18 +367,26 @@ __device__ __forceinline__ void large_body(const TileArgs& g, int n_tiles, int m
   epi.init(ge, nw + wn * CPW, lane);
   epi.fetch(ge, mw);
   constexpr int G = L::G;
+  // the activation is a constant of the loop over tiles, and not of its body alone: with
+  // three of them inside, the fp16 gradient's loop is beyond what the compiler unrolls,
+  // and the accumulators go to memory
+  auto tiles = [&](auto act) {
 #pragma unroll
-  for (int h = 0; h < MT / G; ++h) {
+    for (int h = 0; h < MT / G; ++h) {
 #pragma unroll
-    for (int i = 0; i < G; ++i) put_tile<KIND, NT>(acc[h * G + i], t0 + i * epi_words(NT), lane);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      for (int i = 0; i < G; ++i) put_tile<KIND, NT>(acc[h * G + i], t0 + i * epi_words(NT), lane);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll 1
-    for (int i = 0; i < G; ++i) {
-      const int r = 16 * (h * G + i);
-      epi.tile(ge, t0 + i * epi_words(NT), sa + rw + r, t0 + G * epi_words(NT), mw + r, mw + r + 16);
+      for (int i = 0; i < G; ++i) {
+        const int r = 16 * (h * G + i);
+        epi.template tile<decltype(act)::value>(ge, t0 + i * epi_words(NT), sa + rw + r, t0 + G * epi_words(NT),
+                                                mw + r, mw + r + 16);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  }
+  };
+  if constexpr (EPI == EPI_GRAD) with_act(g.act, tiles);
+  else tiles(std::integral_constant<int, ACT_SILU>{});
 }
 
 template <int KIND, int EPI, int W, int NB, int DT>
@@ -464,7 +472,7 @@ __global__ __launch_bounds__(256) void sum_partials_kernel(TileArgs t, int block
   f32x4_t v = {0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < t.plan.splits; ++s)
     v += *reinterpret_cast<const f32x4_t*>(t.part + s * (int64_t)t.M * ld + at);
-  const float k = DT != XF16 ? 1.f : t.sa != nullptr ? t.sa[m] : *t.scal;
+  const float k = DT == XF16 ? t.sa[m] : 1.f;
   T* y = static_cast<T*>(second ? t.y2 : t.y) + (int64_t)mo * t.ldy + n;
   const float o[4] = {v[0] * k, v[1] * k, v[2] * k, v[3] * k};
   store4(y, o, min(4, t.N - n), vec4_ok(second ? t.y2 : t.y, t.ldy, 2));

@@ -65,9 +65,9 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
 
   int lane, col, n0, n, nn;  // nn: columns of this lane that exist (may be <= 0)
   float s0[4], s1[4];        // column scales; of the up projection
-  float k1, k2;              // GRAD: c1, c2
   bool vec;
   uint16_t dh[EPI == EPI_GRAD ? PASSES : 1][4];  // the next tile's incoming gradient
+  uint32_t levels[2][4];     // GRAD, fp16: of dg's and du's columns, a byte for each of 4 tiles
 
   __device__ __forceinline__ void init(const TileArgs& g, int n0_, int lane_) {
     lane = lane_, n0 = n0_;
@@ -80,11 +80,23 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
       }
     }
     if constexpr (EPI == EPI_GRAD) {
-      k1 = DT == XF16 ? g.scal[0] : 1.f, k2 = DT == XF16 ? g.scal[2] : 1.f;
       vec = vec4_ok(g.dh, g.lddh, 2);
     } else {
       vec = vec4_ok(g.y, g.ldy, g.y_dtype == YF32 ? 4 : 2) && (EPI != EPI_PLAIN || vec4_ok(g.y2, 0, 2));
     }
+  }
+
+  // The power of two of column j's 16 rows in this tile, whose level joins the others'
+  // (fp16; else 1).
+  __device__ __forceinline__ float block_power(const float (&v)[PASSES][4], int j, uint32_t& l, int part) {
+    if constexpr (DT != XF16) return 1.f;
+    float top = 0.f;
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) top = fmaxf(top, fabsf(v[p][j]));
+    if (LPR == 8) top = dpp_max<0x128>(top);  // row_ror:8
+    const uint32_t level = level_of(rows4_max(top));
+    l = part == 0 ? level : l | (level << (8 * part));
+    return level_power(level);
   }
 
   // Requests what the tile at row m0 will need from memory.
@@ -109,7 +121,9 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
 
   // The tile that put_tile wrote to t0, whose first row is m0; sa: its rows'
   // scales; tt: the wave's transposed rows (GRAD), which leave with every fourth
-  // tile (m0 from a multiple of 64 on); m1: the next tile's first row.
+  // tile (m0 from a multiple of 64 on); m1: the next tile's first row; ACT: the
+  // activation (GRAD).
+  template <int ACT>
   __device__ __forceinline__ void tile(const TileArgs& g, const uint32_t* t0, const float* sa,
                                        uint32_t* ttw, int m0, int m1) {
     if constexpr (EPI == EPI_PARTIAL) {
@@ -164,64 +178,94 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
         }
       });
     } else {
-      // dg and du in fp32, then d = (dg sg c1 | du su c1) row-major and
-      // dt = (dg sx c2 | du sx c2) transposed through LDS, zeros where a row
-      // or column only pads
+      // dg and du in fp32, then d = (dg sg | du su) row-major and dt = (dg sx | du sx)
+      // transposed through LDS, zeros where a row or column only pads; in fp16 each
+      // block of both times its power of two
       T* dd = static_cast<T*>(g.d);
-      float e[PASSES][4];
+      float dg[PASSES][4], du[PASSES][4];
 #pragma unroll
       for (int p = 0; p < PASSES; ++p)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) e[p][j] = (float)__builtin_bit_cast(T, (uint16_t)dh[p][j]);
+        for (int j = 0; j < 4; ++j) dg[p][j] = (float)__builtin_bit_cast(T, (uint16_t)dh[p][j]);
       fetch(g, m1);
       const int part = (m0 / 16) % 4;  // of the 64 transposed rows
-      with_act(g.act, [&](auto act) {
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int row = row_of(p), m = m0 + row;
+        const acc_t cg = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, col));
+        const acc_t cu = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, COLS + col));
+        const float a = sa[row];  // 0 for rows past M
+        float vg[4], vu[4], top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float gv = (float)cg[j] * (a * s0[j]), uv = (float)cu[j] * (a * s1[j]);
+          float da;
+          const float r = act_parts<ACT>(gv, &da);
+          // rows past M and columns past N only pad: zeros, whatever the
+          // scales are
+          const bool ok = j < nn && m < g.M;
+          const float e = dg[p][j];
+          dg[p][j] = ok ? e * uv * da : 0.f;
+          du[p][j] = ok ? e * r : 0.f;
+          vg[j] = ok ? dg[p][j] * s0[j] : 0.f;
+          vu[j] = ok ? du[p][j] * s1[j] : 0.f;
+          if constexpr (DT == XF16) top = fmaxf(fmaxf(top, fabsf(vg[j])), fabsf(vu[j]));
+        }
+        const bool own = m < g.M && n < g.Np;  // n is a multiple of 4 and Np of 64
+        float k = 1.f;
+        if constexpr (DT == XF16) {
+          const uint32_t level = level_of(lanes_max<kLevelD / 4>(top));
+          k = level_power(level);
+          if (own && col % kLevelD == 0)
+            g.de[(int64_t)m * (g.Np / kLevelD) + n / kLevelD] = (uint8_t)level;
+        }
+        T4 dgv, duv;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dgv[j] = (T)(vg[j] * k), duv[j] = (T)(vu[j] * k);
+        if (own) {
+          T* o = dd + (int64_t)m * (2 * g.Np) + n;
+          *reinterpret_cast<T4*>(o) = dgv;
+          *reinterpret_cast<T4*>(o + g.Np) = duv;
+        }
+      }
+      if (g.dt == nullptr) return;
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const float a = sa[row_of(p)];
+        const bool ok = m0 + row_of(p) < g.M;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          dg[p][j] = ok && j < nn ? dg[p][j] * a : 0.f;
+          du[p][j] = ok && j < nn ? du[p][j] * a : 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float kg = block_power(dg, j, levels[0][j], part), ku = block_power(du, j, levels[1][j], part);
 #pragma unroll
         for (int p = 0; p < PASSES; p += 2) {
-          // two neighbouring rows at once: their transposed values go to LDS
-          // in pairs
-          T tg[2][4], tu[2][4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int row = row_of(p + h), m = m0 + row;
-            const acc_t cg = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, col));
-            const acc_t cu = *reinterpret_cast<const acc_t*>(t0 + epi_word<NT>(row, COLS + col));
-            const float a = sa[row];  // 0 for rows past M
-            const float ak = a * k2;
-            T4 dgv, duv;
+          // two neighbouring rows at once: they go to LDS in pairs
+          typedef T T2 __attribute__((ext_vector_type(2)));
+          const int r = 16 * part + row_of(p);  // even
+          const int c0 = col + j, c1 = COLS + col + j;
+          ttw[c0 * 32 + 4 * ((r >> 3) ^ ((c0 >> 2) & 7)) + ((r & 7) >> 1)] =
+              __builtin_bit_cast(uint32_t, (T2{(T)(dg[p][j] * kg), (T)(dg[p + 1][j] * kg)}));
+          ttw[c1 * 32 + 4 * ((r >> 3) ^ ((c1 >> 2) & 7)) + ((r & 7) >> 1)] =
+              __builtin_bit_cast(uint32_t, (T2{(T)(du[p][j] * ku), (T)(du[p + 1][j] * ku)}));
+        }
+      }
+      if (part == 3 && m0 < g.Mp) {
+        if constexpr (DT == XF16) {
+          if (lane < LPR) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float gv = (float)cg[j] * (a * s0[j]), uv = (float)cu[j] * (a * s1[j]);
-              float da;
-              const float r = act_parts<decltype(act)::value>(gv, &da);
-              const float dg = e[p + h][j] * uv * da, du = e[p + h][j] * r;
-              // rows past M and columns past N only pad: zeros, whatever the
-              // scales are
-              const bool ok = j < nn && m < g.M;
-              dgv[j] = (T)(ok ? dg * (s0[j] * k1) : 0.f);
-              duv[j] = (T)(ok ? du * (s1[j] * k1) : 0.f);
-              tg[h][j] = (T)(ok ? dg * ak : 0.f);
-              tu[h][j] = (T)(ok ? du * ak : 0.f);
+              if (j >= nn) continue;
+              uint32_t* o = reinterpret_cast<uint32_t*>(g.dte + (int64_t)(n + j) * (g.Mp / kLevelT) + (m0 - 48) / kLevelT);
+              o[0] = levels[0][j];
+              o[g.Nr * (g.Mp / kLevelT) / 4] = levels[1][j];
             }
-            if (m < g.M && n < g.Np) {  // n is a multiple of 4 and Np of 64
-              T* o = dd + (int64_t)m * (2 * g.Np) + n;
-              *reinterpret_cast<T4*>(o) = dgv;
-              *reinterpret_cast<T4*>(o + g.Np) = duv;
-            }
-          }
-          const int r = 16 * part + row_of(p);  // even
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            typedef T T2 __attribute__((ext_vector_type(2)));
-            const int c0 = col + j, c1 = COLS + col + j;
-            ttw[c0 * 32 + 4 * ((r >> 3) ^ ((c0 >> 2) & 7)) + ((r & 7) >> 1)] =
-                __builtin_bit_cast(uint32_t, (T2{tg[0][j], tg[1][j]}));
-            ttw[c1 * 32 + 4 * ((r >> 3) ^ ((c1 >> 2) & 7)) + ((r & 7) >> 1)] =
-                __builtin_bit_cast(uint32_t, (T2{tu[0][j], tu[1][j]}));
           }
         }
-      });
-      if (part == 3 && g.dt != nullptr && m0 < g.Mp) {
         // whole 128-byte lines: 8 lanes on a column's 64 rows
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         T* dt = static_cast<T*>(g.dt);
@@ -243,10 +287,6 @@ template <int KIND, int EPI, int NT, int DT> struct Epilogue {
 template <int EPI, int DT>
 __device__ __forceinline__ void row_scales(const TileArgs& g, float* sa, int m0, int rows) {
   if constexpr (EPI == EPI_PARTIAL || (EPI == EPI_PLAIN && DT != XF16)) return;
-  if (EPI == EPI_PLAIN && g.sa == nullptr) {
-    for (int i = threadIdx.x; i < rows; i += 256) sa[i] = *g.scal;
-    return;
-  }
   for (int i = threadIdx.x; i < rows; i += 256) sa[i] = m0 + i < g.M ? g.sa[m0 + i] : 0.f;
 }
 

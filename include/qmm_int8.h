@@ -127,8 +127,8 @@ QMM_API qmm_status qmm_w8a8_gemm_backward(const void* dy, int dtype, int64_t ldd
  * (both or neither), dWg and dWu (N, K), all of dh's type.  g and u are made
  * again from the codes (exact sums, fp32), so the forward pass keeps nothing
  * of size M x N.  dg and du are formed in fp32; dg sg, du su, dg sx and du sx
- * are rounded to dh's type once, in fp16 after a power of two has been taken out of
- * the scales.
+ * are rounded to dh's type as above (dg sg and du su of a token share its power of
+ * two), so dg and du themselves may lie beyond fp16's range.
  */
 QMM_API qmm_status qmm_w8a8_gated_backward(const void* dh, int dtype, int64_t lddh,
                                            const int8_t* xq, int64_t ldx, const float* sx,
