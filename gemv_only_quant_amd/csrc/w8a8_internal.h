@@ -46,6 +46,12 @@ hipError_t launch_w8a8(const W8A8Args& a);
 // A few tokens (w8a8_rows.hip): x of any type, quantized within the launch
 // where it is not codes (a.x and a.sx then count for nothing).
 bool rows_fits(int M, int K);
+// The tokens' codes lie in LDS in rows of ldk bytes, and step u of a wave's batch starts
+// at byte k of them.  Whether the row has it: a batch's later steps may lie past its end,
+// and of SHARED waves on a column those without a batch have no step at all.
+template <int SHARED> __host__ __device__ constexpr bool rows_step_exists(int k, int u, int ldk) {
+  return (SHARED == 1 && u == 0) || k < ldk;
+}
 hipError_t launch_rows(const W8A8Args& a, const void* x, int x_dtype, int64_t ldx);
 
 // ---- gradients -------------------------------------------------------------

@@ -197,7 +197,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = (it.bt * U + u) * 1024;
-      if (u > 0 && k >= LDK) break;
+      if (!rows_step_exists<S>(k, u, LDK)) break;
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
         const u32x4_t c = *reinterpret_cast<const u32x4_t*>(lds + m * LDK + k + 16 * lane);
