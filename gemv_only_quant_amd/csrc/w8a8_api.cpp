@@ -228,7 +228,15 @@ hipError_t launch_w8a8(const W8A8Args& a) {
   t.y = a.y, t.y_dtype = a.y_dtype, t.ldy = a.ldy;
   t.act = a.act;
   if (skinny_fits(a.M)) return launch_skinny(t, a.gated, a.stream);
-  return a.gated ? launch_tile_gated(t, a.stream) : launch_tile_scale(t, a.stream);
+  hipError_t e = hipSuccess;
+  for (int64_t m = 0; m < a.M && e == hipSuccess; m += kMaxLaunchRows) {
+    t.a = a.x + m * a.ldx;
+    t.sa = a.sx + m;
+    t.y = static_cast<char*>(a.y) + m * a.ldy * type_size(a.y_dtype);
+    t.M = (int)(a.M - m < kMaxLaunchRows ? a.M - m : kMaxLaunchRows);
+    e = a.gated ? launch_tile_gated(t, a.stream) : launch_tile_scale(t, a.stream);
+  }
+  return e;
 }
 
 }  // namespace qmm

@@ -38,13 +38,14 @@ template <int DT>
 __global__ __launch_bounds__(256) void scale_grad_kernel(
     const void* __restrict__ dy, int64_t lddy, const float* __restrict__ sw,
     const float* __restrict__ sx, void* __restrict__ d, int64_t Np, void* __restrict__ dt,
-    int64_t Mp, uint8_t* __restrict__ de, uint8_t* __restrict__ dte, int M, int N, int n_tiles) {
+    int64_t Mp, uint8_t* __restrict__ de, uint8_t* __restrict__ dte, int M, int N, int n_tiles,
+    int m_first) {
   typedef typename Half16<DT>::type T;
   typedef T T4 __attribute__((ext_vector_type(4)));
   typedef T T8 __attribute__((ext_vector_type(8)));
   __shared__ __align__(16) T t[64][72];
   const int n0 = (int)(blockIdx.x % (unsigned)n_tiles) * 64;
-  const int m0 = (int)(blockIdx.x / (unsigned)n_tiles) * 64;
+  const int m0 = m_first + (int)(blockIdx.x / (unsigned)n_tiles) * 64;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const T* src = static_cast<const T*>(dy);
   const bool vec = vec4_ok(dy, lddy, 2);
@@ -190,14 +191,15 @@ __global__ __launch_bounds__(256) void level_rows_kernel(LevelRows a, LevelRows 
   }
 }
 
-// Zeros rows of `len` elements of 2 or 4 bytes (a kernel, not a memset, so
-// that the call can be captured in a HIP graph).
+// Zeros rows of `len` elements of 2 or 4 bytes, 256 of one row at a time (a kernel, not a
+// memset, so that the call can be captured in a HIP graph).
 template <class T>
 __global__ __launch_bounds__(256) void fill_zero_kernel(T* __restrict__ y, int64_t ld, int len,
-                                                        int blocks_per_row) {
-  const int64_t row = blockIdx.x / (unsigned)blocks_per_row;
-  const int i = (int)(blockIdx.x % (unsigned)blocks_per_row) * 256 + (int)threadIdx.x;
-  if (i < len) y[row * ld + i] = 0;
+                                                        int blocks_per_row, int64_t blocks) {
+  for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+    const int i = (int)(b % blocks_per_row) * 256 + (int)threadIdx.x;
+    if (i < len) y[b / blocks_per_row * ld + i] = 0;
+  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -205,11 +207,11 @@ hipError_t launch_fill_zero(void* y, int size, int64_t ld, int rows, int cols, h
   const int bpr = (cols + 255) / 256;
   const int64_t blocks = (int64_t)rows * bpr;
   if (blocks == 0) return hipSuccess;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  return size == 4 ? launch_kernel(fill_zero_kernel<uint32_t>, dim3((unsigned)blocks), dim3(256), s,
-                                   static_cast<uint32_t*>(y), ld, cols, bpr)
-                   : launch_kernel(fill_zero_kernel<uint16_t>, dim3((unsigned)blocks), dim3(256), s,
-                                   static_cast<uint16_t*>(y), ld, cols, bpr);
+  const dim3 grid((unsigned)(blocks < kMaxGroups ? blocks : kMaxGroups));
+  return size == 4 ? launch_kernel(fill_zero_kernel<uint32_t>, grid, dim3(256), s,
+                                   static_cast<uint32_t*>(y), ld, cols, bpr, blocks)
+                   : launch_kernel(fill_zero_kernel<uint16_t>, grid, dim3(256), s,
+                                   static_cast<uint16_t*>(y), ld, cols, bpr, blocks);
 }
 
 BackwardPlan plan_backward(int M, int N, int K, bool gated, bool weight_grad) {
@@ -292,12 +294,15 @@ static hipError_t backward(const BackwardArgs& a, const BackwardPlan& p) {
     t.Np = p.Np, t.Nr = p.Nr, t.Mp = p.Mp;
     e = launch_tile_grad(t, DT, a.stream);
   } else {
-    const int n_tiles = (int)((p.Np + 63) / 64);
-    const int64_t blocks = n_tiles * (((wgrad ? p.Mp : a.M) + 63) / 64);
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    e = launch_kernel(scale_grad_kernel<DT>, dim3((unsigned)blocks), dim3(256), a.stream, a.dy,
-                      a.lddy, a.sw[0], a.sx, ws + p.d, p.Np, wgrad ? ws + p.dt : nullptr, p.Mp,
-                      de, dte, a.M, a.N, n_tiles);
+    const int n_tiles = (int)(p.Np / 64);
+    const int64_t m_tiles = ((wgrad ? p.Mp : a.M) + 63) / 64, most = kMaxGroups / n_tiles;
+    e = hipSuccess;
+    for (int64_t m = 0; m < m_tiles && e == hipSuccess; m += most) {
+      const int64_t blocks = n_tiles * (m_tiles - m < most ? m_tiles - m : most);
+      e = launch_kernel(scale_grad_kernel<DT>, dim3((unsigned)blocks), dim3(256), a.stream, a.dy, a.lddy,
+                        a.sw[0], a.sx, ws + p.d, p.Np, wgrad ? ws + p.dt : nullptr, p.Mp, de, dte, a.M,
+                        a.N, n_tiles, (int)(64 * m));
+    }
   }
   if (e != hipSuccess) return e;
   if (DT == XF16) e = level_operands(a, p, ws);

@@ -22,6 +22,11 @@ constexpr int kStageBytes = 128;
 // Columns of the gradients' operands that share a level (fp16): of d and of dt.
 constexpr int kLevelD = 32, kLevelT = 16;
 
+// A launch has at most 2^32 - 1 threads (of a larger grid the rest is dropped without an
+// error): workgroups of 256 threads of one launch, and rows that a launch is given.
+constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;
+constexpr int kMaxLaunchRows = 1 << 22;
+
 // ---- per-token quantizer (w8a8_quantize.hip) -------------------------------
 hipError_t launch_quantize_tokens(const void* x, int x_dtype, int64_t ldx, int8_t* xq,
                                   int64_t ldxq, float* sx, int M, int K, hipStream_t s);

@@ -432,7 +432,7 @@ static hipError_t launch_w(const TileArgs& t, int64_t m, int64_t n, hipStream_t 
     per = (t.kb / kStageBytes + t.plan.splits - 1) / t.plan.splits;
     n_tiles *= t.plan.splits;
   }
-  if (n_tiles * m_tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (n_tiles * m_tiles > kMaxGroups) return hipErrorInvalidValue;
   return launch_kernel(large_kernel<KIND, EPI, W, NB, DT>, dim3((unsigned)(n_tiles * m_tiles)), dim3(256),
                        s, t, (int)n_tiles, (int)m_tiles, per);
 }

@@ -106,9 +106,16 @@ static hipError_t launch_q_type(const void* x, int64_t ldx, int8_t* xq, int64_t 
 
 hipError_t launch_quantize_tokens(const void* x, int x_dtype, int64_t ldx, int8_t* xq,
                                   int64_t ldxq, float* sx, int M, int K, hipStream_t s) {
-  if (x_dtype == YF32) return launch_q_type<YF32>(x, ldx, xq, ldxq, sx, M, K, s);
-  if (x_dtype == XF16) return launch_q_type<XF16>(x, ldx, xq, ldxq, sx, M, K, s);
-  return launch_q_type<XBF16>(x, ldx, xq, ldxq, sx, M, K, s);
+  hipError_t e = hipSuccess;
+  for (int64_t m = 0; m < M && e == hipSuccess; m += kMaxLaunchRows) {
+    const int rows = (int)(M - m < kMaxLaunchRows ? M - m : kMaxLaunchRows);
+    const void* xm = static_cast<const char*>(x) + m * ldx * (x_dtype == YF32 ? 4 : 2);
+    int8_t* qm = xq + m * ldxq;
+    if (x_dtype == YF32) e = launch_q_type<YF32>(xm, ldx, qm, ldxq, sx + m, rows, K, s);
+    else if (x_dtype == XF16) e = launch_q_type<XF16>(xm, ldx, qm, ldxq, sx + m, rows, K, s);
+    else e = launch_q_type<XBF16>(xm, ldx, qm, ldxq, sx + m, rows, K, s);
+  }
+  return e;
 }
 
 }  // namespace qmm
