@@ -46,6 +46,7 @@ EXPORTS_INT8 = ("qmm_quantize_tokens", "qmm_w8a8_workspace_bytes", "qmm_w8a8_gem
                 "qmm_w8a8_gated", "qmm_w8a8_backward_workspace_bytes", "qmm_w8a8_gemm_backward",
                 "qmm_w8a8_gated_backward")
 
+_INT_MAX = (1 << 31) - 1
 _CODES = {torch.float32: QMM_F32, torch.float16: QMM_F16, torch.bfloat16: QMM_BF16}
 
 
@@ -58,6 +59,8 @@ def _matrix(fn, name, t, shape=None):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         _refuse(fn, f"{name} must be a 2-D tensor")
     rows, cols = t.shape
+    if rows > _INT_MAX or cols > _INT_MAX:  # ctypes would pass on the low 32 bits
+        _refuse(fn, f"{name} is too large ({rows} x {cols})", QMM_ERR_UNSUPPORTED)
     if shape is not None and (rows, cols) != shape:
         _refuse(fn, f"{name} must be {tuple(shape)}, got {(rows, cols)}")
     ld, unit = t.stride()
