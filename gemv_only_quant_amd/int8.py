@@ -15,9 +15,11 @@ and start on 16 bytes.  All of a call's tensors sit on one GPU; the work goes
 to that GPU's current stream and the scratch comes from torch's allocator on
 that stream, so tensors in use on another stream need the usual wait_stream
 or record_stream.  Nothing here is an autograd function: the backward calls
-are what one's backward would call.
+are what one's backward would call.  A call whose operands require gradients warns
+that it passes none on, unless gradients are off.
 """
 import ctypes
+import warnings
 
 import torch
 
@@ -99,18 +101,21 @@ def _scale(fn, name, t, n):
 
 
 def _one_gpu(fn, *tensors):
-    """Index of the GPU that holds all of them."""
+    """Index of the GPU that holds all of them; warns where gradients end here."""
     index = None
     for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
-            _refuse(fn, f"operands must be GPU tensors (got one on {t.device})")
         i = t.get_device()
-        if index is None:
+        if i != index:
+            if not t.is_cuda:
+                _refuse(fn, f"operands must be GPU tensors (got one on {t.device})")
+            if index is not None:
+                _refuse(fn, f"operands on different GPUs ({index} and {i})")
             index = i
-        elif i != index:
-            _refuse(fn, f"operands on different GPUs ({index} and {i})")
+        if t.requires_grad and torch.is_grad_enabled():
+            warnings.warn(f"{fn}: an operand requires gradients, and this call passes none on; call it and its "
+                          f"backward call from a torch.autograd.Function, or under torch.no_grad()", stacklevel=3)
     return index
 
 
