@@ -43,8 +43,6 @@
 
 namespace qmm {
 
-// W: 16 x 16 tiles of a wave in each direction; a workgroup's tile is 32 W rows
-// and columns of B
 // s_waitcnt vmcnt(n) lgkmcnt(0)
 static constexpr int wait_mem(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0070; }
 
@@ -131,6 +129,8 @@ template <int KIND, int EPI, int W, int NB> struct LargeLds {
   static constexpr int WORDS16 = SCALES + 32 * W / 4;
 };
 
+// W: a workgroup's tile is 32 W rows and columns of B, a wave's W x W tiles of 16 x 16
+// (codes: 2 W x W / 2); NB stages are in flight.
 // (a device function beside its kernel: the host pass drops a kernel whose own
 // body has matrix-core registers in inline asm)
 template <int KIND, int EPI, int W, int NB, int DT>
