@@ -434,3 +434,7 @@ def quantize(W, w_bit, group_size, symmetric=False):
 from .int8 import (ACTIVATIONS, EXPORTS_INT8, QMM_GELU, QMM_GELU_TANH, QMM_I8, QMM_SILU,  # noqa: E402,F401
                    quantize_tokens, w8a8_gated, w8a8_gated_backward, w8a8_gemm,
                    w8a8_gemm_backward)
+
+# ------------------------------------------------ microscaled 4-bit (include/qmm_mx4.h)
+from .mx4 import (EXPORTS_MX4, QMM_MX4, QMM_MX4_MAX_EXPERTS, QMM_MX4_MAX_TOKENS, QMM_MX4_MAX_TOP_K,  # noqa: E402,F401
+                  mx4_dequantize, mx4_gemm, mx4_moe, mx4_pack, mx4_packed_bytes, mx4_quantize)

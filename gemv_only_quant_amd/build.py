@@ -29,7 +29,8 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 SOURCES = ["qmm_api.cpp", "gemv_lowbit.hip", "gemv_tile.hip", "gemv_int8.hip", "repack.hip",
            "gemm_mfma.hip", "gemm_large.hip", "gemm_medium.hip", "ternary.hip", "ternary_large.hip",
            "quantize.hip", "w8a8_api.cpp", "w8a8_quantize.hip", "w8a8_rows.hip", "w8a8_skinny.hip",
-           "w8a8_large.hip", "w8a8_backward.hip"]
+           "w8a8_large.hip", "w8a8_backward.hip", "mx4_api.cpp", "mx4_quantize.hip", "mx4_skinny.hip",
+           "mx4_moe.hip"]
 
 
 def _stale(src, obj):
@@ -37,7 +38,7 @@ def _stale(src, obj):
         return True
     deps = [os.path.join(CSRC, src)] + [os.path.join(CSRC, h) for h in os.listdir(CSRC)
                                         if h.endswith(".h")]
-    deps += [os.path.join(ROOT, "include", h) for h in ("qmm.h", "qmm_int8.h")]
+    deps += [os.path.join(ROOT, "include", h) for h in ("qmm.h", "qmm_int8.h", "qmm_mx4.h")]
     return max(os.path.getmtime(d) for d in deps) > os.path.getmtime(obj)
 
 

@@ -1,0 +1,58 @@
+// mx4_device.h -- device helpers of the microscaled 4-bit kernels (gfx950).
+#pragma once
+#include "mx4_internal.h"
+#include "w8a8_device.h"
+
+namespace qmm {
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+// 2^(e - 127) of a scale byte: 0 is the subnormal 2^-127, 255 NaN.
+__device__ __forceinline__ float scale_f32(uint32_t e) {
+  const uint32_t b = e << 23;
+  return __builtin_bit_cast(float, e == 0 ? 0x00400000u : e == 255 ? 0x7FC00000u : b);
+}
+
+// c += A B^t over 128 values of 16 rows each, both operands mx4: lane L holds
+// block L / 16 (32 codes, 16 bytes) of row L % 16, and in the low byte of its
+// scale word that block's scale; the matrix cores apply the scales (255 gives
+// NaN, 0 is 2^-127).  Products within a block are summed exactly; block sums and
+// accumulator are aligned to the largest of them, and what falls below its last
+// bits is dropped.
+__device__ __forceinline__ f32x4_t mfma_mx4(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c,
+                                            uint32_t sa, uint32_t sb) {
+  const i32x8_t x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8_t y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, (int)sa, 0, (int)sb);
+}
+
+// 8 codes times their scale as bf16, pairs in order: exact wherever bf16 has
+// the value (code times power of two: all but the ends of its range).
+__device__ __forceinline__ u32x4_t bf16_of_codes(uint32_t c, float scale) {
+  u32x4_t o;
+  o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0));
+  o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1));
+  o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2));
+  o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3));
+  return o;
+}
+
+// 8 values to 8 codes with a block's scale byte (255: codes 0): the hardware
+// divides by the power of two, rounds to nearest even and holds to +-6.
+__device__ __forceinline__ uint32_t codes_of8(const float (&v)[8], uint32_t e) {
+  const float s = scale_f32(e == 255 ? 127 : e);
+  uint32_t c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], s, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], s, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], s, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], s, 3);
+  return e == 255 ? 0u : c;
+}
+
+// The scale byte of a block from the bit pattern of its largest magnitude.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+  const uint32_t e = top >> 23;
+  return e == 255 ? 255u : (e < 2 ? 0u : e - 2);
+}
+
+}  // namespace qmm

@@ -1,0 +1,82 @@
+// mx4_internal.h -- launchers of the microscaled 4-bit operators (not public).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "w8a8_internal.h"
+
+namespace qmm {
+
+// Data types as in qmm.h / qmm_int8.h / qmm_mx4.h: 0 fp16, 1 bf16, 2 fp32, 4 mx4.
+constexpr int kTypeMx4 = 4;
+
+// ---- layouts ---------------------------------------------------------------
+constexpr int kBlock = 32;  // values that share a scale
+__host__ __device__ constexpr int mx4_blocks(int K) { return (K + kBlock - 1) / kBlock; }
+// packed weights: steps of 128 values, strips of 16 columns
+__host__ __device__ constexpr int mx4_steps(int K) { return (K + 127) / 128; }
+__host__ __device__ constexpr int64_t mx4_strip_bytes(int K) {
+  return (int64_t)1024 * mx4_steps(K) + 256 * ((mx4_steps(K) + 3) / 4);
+}
+__host__ __device__ constexpr int64_t mx4_weight_bytes(int N, int K) {
+  return (int64_t)((N + 15) / 16) * mx4_strip_bytes(K);
+}
+
+// ---- quantizer, its inverse, packing (mx4_quantize.hip) ---------------------
+hipError_t launch_mx4_quantize(const void* x, int x_dtype, int64_t ldx, uint8_t* codes, int64_t ldc,
+                               uint8_t* scales, int64_t lds, int M, int K, hipStream_t s);
+hipError_t launch_mx4_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scales,
+                                 int64_t lds, void* y, int y_dtype, int64_t ldy, int M, int K,
+                                 hipStream_t s);
+hipError_t launch_mx4_pack(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds,
+                           void* W, int batch, int N, int K, hipStream_t s);
+
+// ---- product ---------------------------------------------------------------
+struct Mx4Args {
+  const uint8_t* a;  // codes (M, 16 blocks bytes), scales (M, blocks)
+  int64_t lda;
+  const uint8_t* sa;
+  int64_t ldsa;
+  const uint8_t* w;  // packed (N, K)
+  void* y;
+  int y_dtype;
+  int64_t ldy;
+  int M, N, K;
+};
+hipError_t launch_mx4_skinny(const Mx4Args& a, hipStream_t s);
+
+// ---- mixture of experts (mx4_moe.hip) ---------------------------------------
+constexpr int kMoeTokens = 64, kMoeTopK = 32, kMoeExperts = 1024;
+struct MoeArgs {
+  const void* x;
+  int x_dtype;
+  int64_t ldx;
+  const uint8_t *wg, *wu, *wd;
+  void* y;
+  int y_dtype;
+  int64_t ldy;
+  int T, D, I, E, top_k, act;
+  const void* logits;  // or NULL
+  int logits_dtype;
+  int64_t ldl;
+  int renormalize;
+  const void* ids;
+  int ids_size;
+  const void* weights;
+  int weights_dtype;
+  void* ws;
+};
+// What a call keeps in its workspace, offsets in bytes:
+//   ids, w  (T, top_k) int32 and fp32: experts (-1: none) and weights
+//   x       (parts of x, T, Dp) bf16: x as a sum of parts
+//   h       (parts of h, T top_k, Ip) bf16: w act(g) u as a sum of parts
+struct MoePlan {
+  int xparts, hparts;
+  int Dp, Ip;
+  size_t ids, w, x, h, bytes;
+};
+MoePlan plan_moe(int T, int D, int I, int top_k, int x_dtype, int y_dtype);
+hipError_t launch_mx4_moe(const MoeArgs& a, const MoePlan& p, hipStream_t s);
+
+}  // namespace qmm

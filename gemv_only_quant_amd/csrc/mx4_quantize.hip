@@ -1,0 +1,208 @@
+// mx4_quantize.hip -- values to microscaled 4-bit codes and back, and the
+// layout of weights that the products read.  All three are bound by memory.
+#include "mx4_device.h"
+
+namespace qmm {
+
+// 8 consecutive values of a row (zeros from `n` on), fp32.
+template <int XDT, bool VEC>
+__device__ __forceinline__ Raw8<XDT> take8(const typename Elem<XDT>::type* p, int n) {
+  Raw8<XDT> r = {};
+  if constexpr (VEC) {
+    if (n > 0) {
+      const u32x4_t* v = reinterpret_cast<const u32x4_t*>(p);
+      r.w[0] = v[0];
+      if constexpr (XDT == YF32) r.w[1] = v[1];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j >= n) break;
+      if constexpr (XDT == YF32) r.w[j / 4][j % 4] = __builtin_bit_cast(uint32_t, p[j]);
+      else r.w[0][j / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[j]) << (16 * (j % 2));
+    }
+  }
+  return r;
+}
+
+// Largest over the 4 lanes of a quad, in each of them.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false);
+  v = o > v ? o : v;
+  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false);
+  return o > v ? o : v;
+}
+
+// 4 lanes on a block, 8 values each: a wave reads 512 consecutive values and
+// writes 256 consecutive bytes of codes.  `units` 8-value units a row.
+template <int XDT, bool VEC>
+__global__ __launch_bounds__(256) void mx4_quantize_kernel(
+    const typename Elem<XDT>::type* __restrict__ x, int64_t ldx, uint8_t* __restrict__ codes,
+    int64_t ldc, uint8_t* __restrict__ scales, int64_t lds, uint32_t total, int units, int K) {
+  const uint32_t u = blockIdx.x * 256u + threadIdx.x;
+  if (u >= total) return;  // whole quads: units are multiples of 4
+  const uint32_t m = u / (uint32_t)units;
+  const int i = (int)(u - m * (uint32_t)units);
+  const Raw8<XDT> raw = take8<XDT, VEC>(x + (int64_t)m * ldx + 8 * i, K - 8 * i);
+  const uint32_t e = scale_byte(quad_max(top_f32<XDT>(top8<XDT>(raw, 0u))));
+  float v[8];
+  floats8<XDT>(raw, v);
+  *reinterpret_cast<uint32_t*>(codes + (int64_t)m * ldc + 4 * i) = codes_of8(v, e);
+  uint8_t* s = scales + (int64_t)m * lds;
+  const int b = i / 4;
+  if (i % 4 == 0) s[b] = (uint8_t)e;
+  // padding of the row of scales, by the last block's other lanes
+  if (b == units / 4 - 1 && i % 4 != 0) {
+    const int at = b + i % 4;
+    if (at < (units / 4 + 3) / 4 * 4 && at < lds) s[at] = 0;
+  }
+}
+
+// 8 values per thread.
+template <class Y, bool VEC>
+__global__ __launch_bounds__(256) void mx4_dequantize_kernel(
+    const uint8_t* __restrict__ codes, int64_t ldc, const uint8_t* __restrict__ scales, int64_t lds,
+    Y* __restrict__ y, int64_t ldy, uint32_t total, int units, int K) {
+  const uint32_t u = blockIdx.x * 256u + threadIdx.x;
+  if (u >= total) return;
+  const uint32_t m = u / (uint32_t)units;
+  const int i = (int)(u - m * (uint32_t)units);
+  const uint8_t* p = codes + (int64_t)m * ldc + 4 * i;
+  uint32_t c;
+  if constexpr (VEC) c = *reinterpret_cast<const uint32_t*>(p);
+  else c = p[0] | (p[1] << 8) | (p[2] << 16) | ((uint32_t)p[3] << 24);
+  const float s = scale_f32(scales[(int64_t)m * lds + i / 4]);
+  float v[8];
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0);
+  const f32x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
+  const f32x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2);
+  const f32x2_t f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
+  v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1];
+  v[4] = d[0], v[5] = d[1], v[6] = f[0], v[7] = f[1];
+  Y* o = y + (int64_t)m * ldy + 8 * i;
+  const int n = K - 8 * i;
+  if (VEC && n >= 8) {
+    typedef Y Y8 __attribute__((ext_vector_type(8)));
+    Y8 q;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = (Y)v[j];
+    *reinterpret_cast<Y8*>(o) = q;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) o[j] = (Y)v[j];
+  }
+}
+
+// A thread writes 16 bytes of a packed strip: a block's codes, or 16 scales of a column.
+__global__ __launch_bounds__(256) void mx4_pack_kernel(const uint8_t* __restrict__ codes, int64_t ldc,
+                                                       const uint8_t* __restrict__ scales, int64_t lds,
+                                                       u32x4_t* __restrict__ w, int strips, int N,
+                                                       int K, int first) {
+  const int blocks = mx4_blocks(K), steps = mx4_steps(K);
+  const int pieces = (int)(mx4_strip_bytes(K) / 16);
+  const int64_t strip = (int64_t)first + blockIdx.x;  // of all matrices
+  const int64_t matrix = strip / strips;
+  const int n0 = (int)(strip - matrix * strips) * 16;
+  for (int i = (int)blockIdx.y * 256 + (int)threadIdx.x; i < pieces; i += (int)gridDim.y * 256) {
+    const int col = i % 16, n = n0 + col;
+    const int64_t row = matrix * N + n;
+    u32x4_t o = {0u, 0u, 0u, 0u};
+    if (i < 64 * steps) {
+      const int b = i / 16;
+      if (n < N && b < blocks) {
+        const uint8_t* p = codes + row * ldc + 16 * b;
+        if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+          o = *reinterpret_cast<const u32x4_t*>(p);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j / 4] |= (uint32_t)p[j] << (8 * (j % 4));
+        }
+      }
+    } else {
+      const int c = (i - 64 * steps) / 16;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int b = 16 * c + j;
+        const uint32_t e = n < N && b < blocks ? scales[row * lds + b] : 127u;
+        o[j / 4] |= e << (8 * (j % 4));
+      }
+    }
+    w[strip * pieces + i] = o;
+  }
+}
+
+// ---------------------------------------------------------------- host side
+// f(first row, rows) for launches of at most 2^31 units.
+template <class F> static hipError_t by_rows(int M, int units, F&& f) {
+  const int64_t rows = (int64_t(1) << 31) / units;
+  hipError_t e = hipSuccess;
+  for (int64_t m = 0; m < M && e == hipSuccess; m += rows)
+    e = f(m, (int)(M - m < rows ? M - m : rows));
+  return e;
+}
+static dim3 groups_of(uint32_t total) { return dim3((unsigned)(((int64_t)total + 255) / 256)); }
+
+template <int XDT>
+static hipError_t quantize_t(const void* x, int64_t ldx, uint8_t* codes, int64_t ldc, uint8_t* scales,
+                             int64_t lds, int M, int K, hipStream_t s) {
+  typedef typename Elem<XDT>::type T;
+  const int units = 4 * mx4_blocks(K);
+  const bool vec = vec8_ok(x, ldx, K, sizeof(T)) && K % 8 == 0;
+  return by_rows(M, units, [&](int64_t m, int rows) {
+    const uint32_t total = (uint32_t)rows * (uint32_t)units;
+    return launch_kernel(vec ? mx4_quantize_kernel<XDT, true> : mx4_quantize_kernel<XDT, false>,
+                         groups_of(total), dim3(256), s, static_cast<const T*>(x) + m * ldx, ldx,
+                         codes + m * ldc, ldc, scales + m * lds, lds, total, units, K);
+  });
+}
+
+hipError_t launch_mx4_quantize(const void* x, int x_dtype, int64_t ldx, uint8_t* codes, int64_t ldc,
+                               uint8_t* scales, int64_t lds, int M, int K, hipStream_t s) {
+  switch (x_dtype) {
+    case XF16: return quantize_t<XF16>(x, ldx, codes, ldc, scales, lds, M, K, s);
+    case XBF16: return quantize_t<XBF16>(x, ldx, codes, ldc, scales, lds, M, K, s);
+  }
+  return quantize_t<YF32>(x, ldx, codes, ldc, scales, lds, M, K, s);
+}
+
+template <class Y>
+static hipError_t dequantize_t(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds,
+                               void* y, int64_t ldy, int M, int K, hipStream_t s) {
+  const int units = (K + 7) / 8;
+  const bool vec = ((reinterpret_cast<uintptr_t>(codes) | (uintptr_t)ldc) & 3) == 0 &&
+                   ((reinterpret_cast<uintptr_t>(y) | (uintptr_t)(ldy * sizeof(Y))) & (8 * sizeof(Y) - 1)) == 0;
+  return by_rows(M, units, [&](int64_t m, int rows) {
+    const uint32_t total = (uint32_t)rows * (uint32_t)units;
+    return launch_kernel(vec ? mx4_dequantize_kernel<Y, true> : mx4_dequantize_kernel<Y, false>,
+                         groups_of(total), dim3(256), s, codes + m * ldc, ldc, scales + m * lds, lds,
+                         static_cast<Y*>(y) + m * ldy, ldy, total, units, K);
+  });
+}
+
+hipError_t launch_mx4_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scales,
+                                 int64_t lds, void* y, int y_dtype, int64_t ldy, int M, int K,
+                                 hipStream_t s) {
+  switch (y_dtype) {
+    case XF16: return dequantize_t<_Float16>(codes, ldc, scales, lds, y, ldy, M, K, s);
+    case XBF16: return dequantize_t<__bf16>(codes, ldc, scales, lds, y, ldy, M, K, s);
+  }
+  return dequantize_t<float>(codes, ldc, scales, lds, y, ldy, M, K, s);
+}
+
+hipError_t launch_mx4_pack(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds,
+                           void* W, int batch, int N, int K, hipStream_t s) {
+  const int strips = (N + 15) / 16;
+  const int64_t all = (int64_t)batch * strips;
+  const int64_t pieces = mx4_strip_bytes(K) / 16;
+  const unsigned parts = (unsigned)(pieces > 256 * 64 ? 64 : (pieces + 255) / 256);
+  const int64_t most = kMaxGroups / parts;
+  hipError_t e = hipSuccess;
+  for (int64_t f = 0; f < all && e == hipSuccess; f += most)
+    e = launch_kernel(mx4_pack_kernel, dim3((unsigned)(all - f < most ? all - f : most), parts), dim3(256), s,
+                      codes, ldc, scales, lds, static_cast<u32x4_t*>(W), strips, N, K, (int)f);
+  return e;
+}
+
+}  // namespace qmm
