@@ -30,7 +30,7 @@ SOURCES = ["qmm_api.cpp", "gemv_lowbit.hip", "gemv_tile.hip", "gemv_int8.hip", "
            "gemm_mfma.hip", "gemm_large.hip", "gemm_medium.hip", "ternary.hip", "ternary_large.hip",
            "quantize.hip", "w8a8_api.cpp", "w8a8_quantize.hip", "w8a8_rows.hip", "w8a8_skinny.hip",
            "w8a8_large.hip", "w8a8_backward.hip", "mx4_api.cpp", "mx4_quantize.hip", "mx4_skinny.hip",
-           "mx4_moe.hip"]
+           "mx4_large.hip", "mx4_moe.hip"]
 
 
 def _stale(src, obj):

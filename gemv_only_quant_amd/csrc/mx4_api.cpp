@@ -195,7 +195,7 @@ qmm_status qmm_mx4_gemm(const void* x, int x_dtype, int64_t ldx, const uint8_t* 
     a.a = codes;
     a.sa = scales;
   }
-  return device_status(fn, qmm::launch_mx4_skinny(a, s));
+  return device_status(fn, M <= 64 ? qmm::launch_mx4_skinny(a, s) : qmm::launch_mx4_large(a, s));
 }
 
 size_t qmm_mx4_moe_workspace_bytes(int T, int D, int I, int E, int top_k, int x_dtype, int y_dtype) {

@@ -45,6 +45,7 @@ struct Mx4Args {
   int M, N, K;
 };
 hipError_t launch_mx4_skinny(const Mx4Args& a, hipStream_t s);
+hipError_t launch_mx4_large(const Mx4Args& a, hipStream_t s);
 
 // ---- mixture of experts (mx4_moe.hip) ---------------------------------------
 constexpr int kMoeTokens = 64, kMoeTopK = 32, kMoeExperts = 1024;
