@@ -32,9 +32,13 @@ hipError_t launch_mx4_dequantize(const uint8_t* codes, int64_t ldc, const uint8_
 hipError_t launch_mx4_pack(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds,
                            void* W, int batch, int N, int K, hipStream_t s);
 
+// Values straight to the packed layout of a weight (M, K).  (Rows past M of the last strip: anything.)
+hipError_t launch_mx4_quantize_packed(const void* x, int x_dtype, int64_t ldx, uint8_t* w, int M, int K,
+                                      hipStream_t s);
+
 // ---- product ---------------------------------------------------------------
 struct Mx4Args {
-  const uint8_t* a;  // codes (M, 16 blocks bytes), scales (M, blocks)
+  const uint8_t* a;  // skinny: codes (M, 16 blocks bytes), scales (M, blocks); large: packed (M, K)
   int64_t lda;
   const uint8_t* sa;
   int64_t ldsa;
@@ -44,6 +48,7 @@ struct Mx4Args {
   int64_t ldy;
   int M, N, K;
 };
+bool mx4_skinny_fits(int M);
 hipError_t launch_mx4_skinny(const Mx4Args& a, hipStream_t s);
 hipError_t launch_mx4_large(const Mx4Args& a, hipStream_t s);
 

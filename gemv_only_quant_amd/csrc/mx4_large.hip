@@ -4,19 +4,18 @@
 //
 // Tiles of 256 x 256 (W = 8) or 128 x 128 (W = 4) by 4 waves as 2 x 2; a wave owns W x
 // W tiles of 16 x 16, whose accumulators are pinned to the matrix-core (AGPR) registers.
-//  * a stage is 256 values of K, two MFMA k steps: 128 bytes of a row of codes and 8
+//  * a stage is 256 values of K, two MFMA k steps: 2 KiB of a strip's codes and 128 bytes of
 //    scales.  Both operands' codes and scales go to LDS by loads straight to it, NB
 //    stages in flight;
-//  * A: 8 rows of 128 bytes per load, chunk c of row r at slot 8 r + (c ^ (r / 2 % 8)), so
-//    that operand reads are conflict-free.  B is packed: 1 KiB of a strip as it lies in
-//    memory, read from LDS as consecutive 256 bytes by 16 lanes;
+//  * both operands are packed: 1 KiB of a strip as it lies in memory, read from LDS as
+//    consecutive 256 bytes by 16 lanes;
 //  * a lane's block in k step k is 2 (lane / 16) + k of the stage's 8: the scales of both k
 //    steps are then neighbouring bytes, one 2-byte read for each operand and stage, of
 //    which the instruction picks the byte;
 //  * the operands of the next k step are read while the MFMAs of this one run.  When a
 //    stage's second k step begins all of its operands are in registers, and one barrier
 //    there does everything: the next stage has arrived, the one after may go out.
-// Rows past M, strips past N and steps past K read zeros.
+// Strips past M or N and steps past K read zeros.
 #include "mx4_device.h"
 #include <stdlib.h>
 #include "w8a8_tile.h"
@@ -61,75 +60,47 @@ __device__ __forceinline__ void mx4_large_body(const Mx4Args& g, int n_tiles, in
   tile_of((int)blockIdx.x, n_tiles, m_tiles, &mt, &nt);
   const int m0 = mt * TILE, n0 = nt * TILE;
   const int wm = wave >> 1, wn = wave & 1;
-  const int blocks = mx4_blocks(g.K), steps = mx4_steps(g.K);
-  const int nst = (steps + 1) / 2;
-  const int row_bytes = 16 * blocks;
-  const int lda = (int)g.lda, ldsa = (int)g.ldsa;
+  const int steps = mx4_steps(g.K), nst = (steps + 1) / 2;
   const int strip_bytes = (int)mx4_strip_bytes(g.K);
 
-  // Buffers: 16 rows of A that this wave moves (W / 2 of each), their scales, and the workgroup's strips of B.
-  buf_t ra[PIECES], sa;
-#pragma unroll
-  for (int i = 0; i < PIECES; ++i) {
-    const int first = m0 + 16 * (PIECES * wave + i), n = min(16, g.M - first);
-    ra[i] = make_buf(g.a + (int64_t)(n > 0 ? first : 0) * g.lda, n > 0 ? (uint32_t)((n - 1) * lda + row_bytes) : 0u);
-  }
-  const int mw = m0 + 16 * PIECES * wave;
-  {
-    const int n = min(16 * PIECES, g.M - mw);
-    sa = make_buf(g.sa + (int64_t)(n > 0 ? mw : 0) * g.ldsa,
-                  n > 0 ? (uint32_t)((n - 1) * ldsa + (int)round_up(blocks, 4)) : 0u);
-  }
-  const int strips = (g.N + 15) / 16, s0 = n0 / 16 + PIECES * wave;
-  const int ns = min(PIECES, strips - s0);
-  const buf_t rb = make_buf(g.w + (int64_t)(ns > 0 ? s0 : 0) * strip_bytes, ns > 0 ? (uint32_t)(ns * strip_bytes) : 0u);
+  // This wave's W / 2 strips of either operand, each a buffer that ends with the last.
+  auto strips_of = [&](const uint8_t* p, int first, int limit) {
+    const int n = min(PIECES, limit - first);
+    return make_buf(p + (int64_t)(n > 0 ? first : 0) * strip_bytes, n > 0 ? (uint32_t)(n * strip_bytes) : 0u);
+  };
+  const buf_t ra = strips_of(g.a, m0 / 16 + PIECES * wave, (g.M + 15) / 16);
+  const buf_t rb = strips_of(g.w, n0 / 16 + PIECES * wave, (g.N + 15) / 16);
 
-  // Lanes' offsets.  A: load unit u (1 KiB) is rows 8 u .. + 7: lane p's 16 bytes land at
-  // slot 64 u + p, so it fetches chunk (p % 8) ^ (r / 2 % 8) of row r = 8 u + p / 8.
-  int ao[2];
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-    ao[c] = (8 * c + (lane >> 3)) * lda + 16 * ((lane & 7) ^ ((4 * c + (lane >> 4)) & 7));
-  // scales, 4 bytes a lane: dword d of the wave's, row d / 2
+  // Lanes' offsets: 16 bytes of codes; scales 4 bytes a lane, dword d of the wave's, row d / 2
   constexpr int SL = W / 4;  // loads of one operand's scales (128 W / 4 bytes a wave)
-  int so[SL], to[SL];
+  int so[SL];
 #pragma unroll
   for (int i = 0; i < SL; ++i) {
     const int d = 64 * i + lane, r = d >> 1;
-    so[i] = r * ldsa + 4 * (d & 1);
-    to[i] = (r >> 4) * strip_bytes + 1024 * steps + 16 * (r & 15) + 4 * (d & 1);
+    so[i] = (r >> 4) * strip_bytes + 1024 * steps + 16 * (r & 15) + 4 * (d & 1);
   }
-  const int bo = 16 * lane;
   constexpr int LOADS = 2 * W + 2 * SL;
   auto lds_at = [&](int word) { return (__attribute__((address_space(3))) void*)(lds + word); };
   // load j of this wave's share of stage st (past the last stage: the last again, unused)
   auto load = [&](int j, int st) {
     const int base = st % NB * STAGE;
     const int q = min(st, nst - 1);
-    if (j < W) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra[j / 2], lds_at(base + (W * wave + j) * 64), 16, ao[j % 2] + 128 * q, 0, 0, 0);
-    } else if (j < 2 * W) {
-      // strip i's step 2 q + h; past K no bytes of the strip's scales
-      const int i = (j - W) / 2, h = (j - W) % 2, step = 2 * q + h;
+    if (j < 2 * W) {
+      // strip i's step 2 q + h; past K nothing
+      const int o = j / W, i = j % W / 2, h = j % 2, step = 2 * q + h;
       const int at = step < steps ? i * strip_bytes + 1024 * step : 0x7FFF0000;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, lds_at(base + L::CODES + (W * wave + j - W) * 64), 16, bo + at, 0, 0, 0);
-    } else if (j < 2 * W + SL) {
-      const int i = j - 2 * W;
-      // blocks from the row's last 4 on: outside the buffer, zeros (2^-127, not NaN)
-      const int off = 8 * q + 4 * (lane & 1) < blocks ? so[i] + 8 * q : 0x7FFF0000;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(sa, lds_at(base + 2 * L::CODES + (SL * wave + i) * 16), 4, off, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(o == 0 ? ra : rb, lds_at(base + o * L::CODES + (W * wave + j % W) * 64), 16,
+                                               16 * lane + at, 0, 0, 0);
     } else {
-      const int i = j - 2 * W - SL;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, lds_at(base + 2 * L::CODES + L::SCALES + (SL * wave + i) * 16), 4,
-                                               to[i] + 256 * (q >> 1) + 8 * (q & 1), 0, 0, 0);
+      const int o = (j - 2 * W) / SL, i = (j - 2 * W) % SL;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(o == 0 ? ra : rb, lds_at(base + 2 * L::CODES + o * L::SCALES + (SL * wave + i) * 16),
+                                               4, so[i] + 256 * (q >> 1) + 8 * (q & 1), 0, 0, 0);
     }
   };
   // operand i (W of A, then W of B) of k step k of stage st
-  const int swz = (l16 >> 1) & 7;
-  const int oa = (16 * W * wm + l16) * 8, ob = L::CODES + 128 * W * wn + l16;
+  const int oa = 128 * W * wm + l16, ob = L::CODES + 128 * W * wn + l16;
   auto frag = [&](int i, int k, int st) {
-    const int c = 2 * quad + k;
-    return i < W ? lds[st % NB * STAGE + oa + 128 * i + (c ^ swz)] : lds[st % NB * STAGE + ob + 128 * (i - W) + 16 * c];
+    return lds[st % NB * STAGE + (i < W ? oa + 128 * i : ob + 128 * (i - W)) + 16 * (2 * quad + k)];
   };
   // both k steps' scales of operand i
   const int os = 16 * W * wm + l16, ot = 16 * W * wn + l16;
@@ -144,17 +115,6 @@ __device__ __forceinline__ void mx4_large_body(const Mx4Args& g, int n_tiles, in
 #pragma unroll
     for (int s = 0; s < W; ++s) acc[i][s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  // A row's scales are read in fours: those past its last block may be NaN's byte, and
-  // are cleared in LDS by the workgroup, before that stage is read (B's codes there are zeros)
-  auto clear_last = [&](int st) {
-    if (blocks % 4 == 0) return;
-    if (threadIdx.x < TILE) {
-      uint32_t* p = reinterpret_cast<uint32_t*>(lds + st % NB * STAGE + 2 * L::CODES) + 2 * threadIdx.x + (blocks % 8) / 4;
-      *p &= (1u << (8 * (blocks % 4))) - 1u;
-    }
-    __syncthreads();
-  };
-
   u32x4_t f[2][2 * W];  // operands of the two k steps
   uint32_t sc[2 * W], sn[2 * W];
 #pragma unroll
@@ -163,7 +123,6 @@ __device__ __forceinline__ void mx4_large_body(const Mx4Args& g, int n_tiles, in
     for (int j = 0; j < LOADS; ++j) load(j, q);
   __builtin_amdgcn_s_waitcnt(wait_mem((NB - 1) * LOADS));
   __syncthreads();
-  if (nst == 1) clear_last(0);
 #pragma unroll
   for (int i = 0; i < 2 * W; ++i) f[0][i] = frag(i, 0, 0), sc[i] = scale(i, 0);
 
@@ -199,7 +158,6 @@ __device__ __forceinline__ void mx4_large_body(const Mx4Args& g, int n_tiles, in
       if (k == 0) {
         __builtin_amdgcn_s_waitcnt(wait_mem((NB - 2) * LOADS));
         __syncthreads();
-        if (st + 2 == nst) clear_last(st + 1);
         __builtin_amdgcn_sched_barrier(0);
       }
     }

@@ -58,6 +58,46 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(
   }
 }
 
+// Values to codes in the packed layout (as a weight (M, K)): a wave takes a step of 128
+// values of a strip's 16 rows, 16 lanes on a row, 4 rows at a time.
+template <int XDT, bool VEC>
+__global__ __launch_bounds__(256) void mx4_quantize_packed_kernel(
+    const typename Elem<XDT>::type* __restrict__ x, int64_t ldx, uint8_t* __restrict__ w, uint32_t total, int M, int K) {
+  const int lane = threadIdx.x & 63, l16 = lane & 15;
+  const uint32_t u = blockIdx.x * 4u + (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (u >= total) return;
+  const uint32_t steps = (uint32_t)mx4_steps(K);
+  const uint32_t strip = u / steps;
+  const int s = (int)(u - strip * steps);
+  uint8_t* o = w + (int64_t)strip * mx4_strip_bytes(K);
+  uint8_t* os = o + (int64_t)1024 * steps + 256 * (s / 4) + 4 * (s % 4);
+  Raw8<XDT> raw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m = 16 * (int)strip + 4 * i + lane / 16, k = 128 * s + 8 * l16;
+    raw[i] = take8<XDT, VEC>(x + (int64_t)(m < M ? m : 0) * ldx + k, m < M ? K - k : 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * i + lane / 16;
+    const uint32_t e = scale_byte(quad_max(top_f32<XDT>(top8<XDT>(raw[i], 0u))));
+    float v[8];
+    floats8<XDT>(raw[i], v);
+    *reinterpret_cast<uint32_t*>(o + 1024 * s + 256 * (l16 / 4) + 16 * r + 4 * (l16 % 4)) = codes_of8(v, e);
+    // the row's 4 scales meet in its first lane
+    uint32_t d = e;
+    d |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)e, 0x104, 0xF, 0xF, true) << 8;   // row_shl:4
+    d |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)e, 0x108, 0xF, 0xF, true) << 16;  // row_shl:8
+    d |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)e, 0x10C, 0xF, 0xF, true) << 24;  // row_shl:12
+    if (l16 == 0) {
+      *reinterpret_cast<uint32_t*>(os + 16 * r) = d;
+      // what is left of the last 512 values: scales that are not NaN
+      if (s + 1 == (int)steps)
+        for (int j = s % 4 + 1; j < 4; ++j) *reinterpret_cast<uint32_t*>(os + 16 * r + 4 * (j - s % 4)) = 0x7F7F7F7Fu;
+    }
+  }
+}
+
 // 8 values per thread.
 template <class Y, bool VEC>
 __global__ __launch_bounds__(256) void mx4_dequantize_kernel(
@@ -165,6 +205,32 @@ hipError_t launch_mx4_quantize(const void* x, int x_dtype, int64_t ldx, uint8_t*
     case XBF16: return quantize_t<XBF16>(x, ldx, codes, ldc, scales, lds, M, K, s);
   }
   return quantize_t<YF32>(x, ldx, codes, ldc, scales, lds, M, K, s);
+}
+
+template <int XDT>
+static hipError_t quantize_packed_t(const void* x, int64_t ldx, uint8_t* w, int M, int K, hipStream_t s) {
+  typedef typename Elem<XDT>::type T;
+  const bool vec = vec8_ok(x, ldx, K, sizeof(T)) && K % 8 == 0;
+  // strips of one launch: at most 2^31 steps
+  const int64_t strips = ((int64_t)M + 15) / 16, most = (int64_t(1) << 25) / mx4_steps(K);
+  hipError_t e = hipSuccess;
+  for (int64_t f = 0; f < strips && e == hipSuccess; f += most) {
+    const int64_t n = strips - f < most ? strips - f : most;
+    const uint32_t total = (uint32_t)(n * mx4_steps(K));
+    e = launch_kernel(vec ? mx4_quantize_packed_kernel<XDT, true> : mx4_quantize_packed_kernel<XDT, false>,
+                      dim3((total + 3) / 4), dim3(256), s, static_cast<const T*>(x) + 16 * f * ldx, ldx,
+                      w + f * mx4_strip_bytes(K), total, (int)(M - 16 * f < 16 * n ? M - 16 * f : 16 * n), K);
+  }
+  return e;
+}
+
+hipError_t launch_mx4_quantize_packed(const void* x, int x_dtype, int64_t ldx, uint8_t* w, int M, int K,
+                                      hipStream_t s) {
+  switch (x_dtype) {
+    case XF16: return quantize_packed_t<XF16>(x, ldx, w, M, K, s);
+    case XBF16: return quantize_packed_t<XBF16>(x, ldx, w, M, K, s);
+  }
+  return quantize_packed_t<YF32>(x, ldx, w, M, K, s);
 }
 
 template <class Y>

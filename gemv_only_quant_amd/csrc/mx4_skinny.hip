@@ -46,6 +46,8 @@ __global__ __launch_bounds__(256) void mx4_skinny_kernel(Mx4Args g, int strips) 
 }
 
 // ---------------------------------------------------------------- host side
+bool mx4_skinny_fits(int M) { return M <= 64; }
+
 hipError_t launch_mx4_skinny(const Mx4Args& a, hipStream_t s) {
   const int strips = (a.N + 15) / 16;
   const int64_t tiles = ((int64_t)a.M + 15) / 16;

@@ -151,7 +151,7 @@ def mx4_gemm(x, W, N, sx=None, out=None, out_dtype=torch.float32):
         if sx is None:
             _refuse(fn, "uint8 x needs its scales (sx)")
         px, ldx, ps, lds, B = _coded(fn, x, sx)
-        code, K, need = QMM_MX4, 32 * B, 0
+        code, K = QMM_MX4, 32 * B
         if x.shape[0] <= 1:
             lds = -(-lds // 4) * 4
         if B % 4 and x.shape[0]:
@@ -165,8 +165,8 @@ def mx4_gemm(x, W, N, sx=None, out=None, out_dtype=torch.float32):
             _refuse(fn, "sx goes with uint8 x")
         code = _float_type(fn, "x", x.dtype)
         K = x.shape[1]
-        need = _lib.qmm_mx4_workspace_bytes(x.shape[0], K, code)
     M = x.shape[0]
+    need = _lib.qmm_mx4_workspace_bytes(M, K, code)
     pw = _packed(fn, "W", W, mx4_packed_bytes(N, K))
     index = _one_gpu(fn, x, sx, W, out)
     y, ycode, py, ldy = _output(fn, "out", out, out_dtype, (M, N), x.device)

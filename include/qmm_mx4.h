@@ -85,9 +85,9 @@ QMM_API qmm_status qmm_mx4_pack(const uint8_t* codes, int64_t ldc, const uint8_t
                                 int64_t lds, void* W, int batch, int N, int K, void* stream);
 
 /* Scratch of qmm_mx4_gemm for activations that the call quantizes itself (x_dtype
- * other than QMM_MX4).  Device memory, 16-byte aligned, any contents; in use
- * until the call's work on the stream is done.  0 for QMM_MX4, for sizes that
- * need none and for invalid arguments. */
+ * other than QMM_MX4) or, where there are many, lays out.  Device memory, 16-byte
+ * aligned, any contents; in use until the call's work on the stream is done.  0
+ * where none is needed and for invalid arguments. */
 QMM_API size_t qmm_mx4_workspace_bytes(int M, int K, int x_dtype);
 
 /*
