@@ -14,11 +14,10 @@ constexpr int kTypeMx4 = 4;
 // ---- layouts ---------------------------------------------------------------
 constexpr int kBlock = 32;  // values that share a scale
 __host__ __device__ constexpr int mx4_blocks(int K) { return (K + kBlock - 1) / kBlock; }
-// packed weights: steps of 128 values, strips of 16 columns
-__host__ __device__ constexpr int mx4_steps(int K) { return (K + 127) / 128; }
-__host__ __device__ constexpr int64_t mx4_strip_bytes(int K) {
-  return (int64_t)1024 * mx4_steps(K) + 256 * ((mx4_steps(K) + 3) / 4);
-}
+// packed weights: chunks of 512 values of strips of 16 columns
+constexpr int kChunkBytes = 4096 + 256;
+__host__ __device__ constexpr int mx4_chunks(int K) { return (K + 511) / 512; }
+__host__ __device__ constexpr int64_t mx4_strip_bytes(int K) { return (int64_t)kChunkBytes * mx4_chunks(K); }
 __host__ __device__ constexpr int64_t mx4_weight_bytes(int N, int K) {
   return (int64_t)((N + 15) / 16) * mx4_strip_bytes(K);
 }

@@ -181,7 +181,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(MoeArgs g, MoeBuf
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
   const int strip = (int)blockIdx.x;
-  const int steps = mx4_steps(g.D);
+  const int steps = 4 * mx4_chunks(g.D);
   const int64_t at = (int64_t)e * mx4_weight_bytes(g.I, g.D) + (int64_t)strip * mx4_strip_bytes(g.D);
   float wt;
   const int place = place_of(r, lane, g.T, g.top_k, e, &wt);
@@ -194,9 +194,9 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(MoeArgs g, MoeBuf
     float sc[2];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      const uint8_t* w = (p == 0 ? g.wg : g.wu) + at;
-      c[p] = *reinterpret_cast<const u32x4_t*>(w + 1024 * s + 16 * lane);
-      sc[p] = scale_f32(w[1024 * (int64_t)steps + 256 * (s / 4) + 16 * l16 + 4 * (s % 4) + quad]);
+      const uint8_t* w = (p == 0 ? g.wg : g.wu) + at + (int64_t)kChunkBytes * (s / 4);
+      c[p] = *reinterpret_cast<const u32x4_t*>(w + 1024 * (s % 4) + 16 * lane);
+      sc[p] = scale_f32(w[4096 + 4 * lane + s % 4]);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(MoeArgs g, MoeBuf
         for (int q = 0; q < XP; ++q) {
           u32x4_t a = {0u, 0u, 0u, 0u};
           if ((members >> t) & 1)
-            a = *reinterpret_cast<const u32x4_t*>(o.x + ((int64_t)q * g.T + t) * Dp + 128 * s + 32 * quad + 8 * i);
+            a = *reinterpret_cast<const u32x4_t*>(o.x + ((int64_t)q * g.T + t) * Dp + 512 * (s / 4) + 32 * (4 * quad + s % 4) + 8 * i);
           const bf16x8_t av = __builtin_bit_cast(bf16x8_t, a);
           acc[m][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bg, acc[m][0], 0, 0, 0);
           acc[m][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bu, acc[m][1], 0, 0, 0);
@@ -265,7 +265,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeArgs g, Mo
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
   const int strip = (int)blockIdx.x;
-  const int steps = mx4_steps(g.I);
+  const int steps = 4 * mx4_chunks(g.I);
   f32x4_t acc[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -283,12 +283,13 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeArgs g, Mo
       members = __ballot(place >= 0);
       w = g.wd + (int64_t)e * mx4_weight_bytes(g.D, g.I) + (int64_t)strip * mx4_strip_bytes(g.I);
     }
-    const u32x4_t c = *reinterpret_cast<const u32x4_t*>(w + 1024 * s + 16 * lane);
-    const float sc = scale_f32(w[1024 * (int64_t)steps + 256 * (s / 4) + 16 * l16 + 4 * (s % 4) + quad]);
+    const uint8_t* wc = w + (int64_t)kChunkBytes * (s / 4);
+    const u32x4_t c = *reinterpret_cast<const u32x4_t*>(wc + 1024 * (s % 4) + 16 * lane);
+    const float sc = scale_f32(wc[4096 + 4 * lane + s % 4]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bf16x8_t b = __builtin_bit_cast(bf16x8_t, bf16_of_codes(c[i], sc));
-      const int kk = 128 * s + 32 * quad + 8 * i;
+      const int kk = 512 * (s / 4) + 32 * (4 * quad + s % 4) + 8 * i;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         if (((members >> (16 * m)) & 0xFFFF) == 0) continue;
@@ -328,7 +329,7 @@ MoePlan plan_moe(int T, int D, int I, int top_k, int x_dtype, int y_dtype) {
   MoePlan p{};
   p.xparts = x_dtype == YF32 ? 3 : x_dtype == XF16 ? 2 : 1;
   p.hparts = y_dtype == YF32 ? 3 : 2;
-  p.Dp = (int)round_up(D, 128);
+  p.Dp = (int)round_up(D, 512);
   p.Ip = (int)round_up(I, 16);
   size_t at = 0;
   auto take = [&](size_t bytes) {

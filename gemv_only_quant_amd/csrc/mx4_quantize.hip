@@ -58,43 +58,41 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(
   }
 }
 
-// Values to codes in the packed layout (as a weight (M, K)): a wave takes a step of 128
-// values of a strip's 16 rows, 16 lanes on a row, 4 rows at a time.
+// Values to codes in the packed layout (as a weight (M, K)): a wave takes a chunk of 512
+// values of 4 rows, 8 values a lane.  (Blocks of zeros past K have scale byte 0, which is as good
+// as 127; rows past M are never stored by who reads them.)
 template <int XDT, bool VEC>
 __global__ __launch_bounds__(256) void mx4_quantize_packed_kernel(
     const typename Elem<XDT>::type* __restrict__ x, int64_t ldx, uint8_t* __restrict__ w, uint32_t total, int M, int K) {
-  const int lane = threadIdx.x & 63, l16 = lane & 15;
+  const int lane = threadIdx.x & 63;
   const uint32_t u = blockIdx.x * 4u + (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (u >= total) return;
-  const uint32_t steps = (uint32_t)mx4_steps(K);
-  const uint32_t strip = u / steps;
-  const int s = (int)(u - strip * steps);
-  uint8_t* o = w + (int64_t)strip * mx4_strip_bytes(K);
-  uint8_t* os = o + (int64_t)1024 * steps + 256 * (s / 4) + 4 * (s % 4);
+  const uint32_t chunks = (uint32_t)mx4_chunks(K);
+  const uint32_t at = u / 4;  // chunk of the matrix; rows 4 (u % 4) .. + 3 of its strip
+  const uint32_t strip = at / chunks;
+  const int c = (int)(at - strip * chunks);
+  uint8_t* o = w + (int64_t)at * kChunkBytes;
   Raw8<XDT> raw[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int m = 16 * (int)strip + 4 * i + lane / 16, k = 128 * s + 8 * l16;
+    const int m = 16 * (int)strip + 4 * (int)(u % 4) + i, k = 512 * c + 8 * lane;
     raw[i] = take8<XDT, VEC>(x + (int64_t)(m < M ? m : 0) * ldx + k, m < M ? K - k : 0);
   }
+  // lane: quarter lane % 4 of block lane / 4 = 4 q + j
+  const int q = lane >> 4, j = (lane >> 2) & 3;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = 4 * i + lane / 16;
+    const int r = 4 * (int)(u % 4) + i;
     const uint32_t e = scale_byte(quad_max(top_f32<XDT>(top8<XDT>(raw[i], 0u))));
     float v[8];
     floats8<XDT>(raw[i], v);
-    *reinterpret_cast<uint32_t*>(o + 1024 * s + 256 * (l16 / 4) + 16 * r + 4 * (l16 % 4)) = codes_of8(v, e);
-    // the row's 4 scales meet in its first lane
+    *reinterpret_cast<uint32_t*>(o + 1024 * j + 256 * q + 16 * r + 4 * (lane & 3)) = codes_of8(v, e);
+    // the scales of 4 blocks meet in the first of their 16 lanes
     uint32_t d = e;
     d |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)e, 0x104, 0xF, 0xF, true) << 8;   // row_shl:4
     d |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)e, 0x108, 0xF, 0xF, true) << 16;  // row_shl:8
     d |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)e, 0x10C, 0xF, 0xF, true) << 24;  // row_shl:12
-    if (l16 == 0) {
-      *reinterpret_cast<uint32_t*>(os + 16 * r) = d;
-      // what is left of the last 512 values: scales that are not NaN
-      if (s + 1 == (int)steps)
-        for (int j = s % 4 + 1; j < 4; ++j) *reinterpret_cast<uint32_t*>(os + 16 * r + 4 * (j - s % 4)) = 0x7F7F7F7Fu;
-    }
+    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(o + 4096 + 64 * q + 4 * r) = d;
   }
 }
 
@@ -135,37 +133,36 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(
   }
 }
 
-// A thread writes 16 bytes of a packed strip: a block's codes, or 16 scales of a column.
+// A thread writes 16 bytes of a packed chunk: a block's codes, or 4 columns' 4 scales.
 __global__ __launch_bounds__(256) void mx4_pack_kernel(const uint8_t* __restrict__ codes, int64_t ldc,
                                                        const uint8_t* __restrict__ scales, int64_t lds,
                                                        u32x4_t* __restrict__ w, int strips, int N,
                                                        int K, int first) {
-  const int blocks = mx4_blocks(K), steps = mx4_steps(K);
-  const int pieces = (int)(mx4_strip_bytes(K) / 16);
+  const int blocks = mx4_blocks(K), chunks = mx4_chunks(K);
+  constexpr int PER = kChunkBytes / 16;  // 256 of codes, 16 of scales
+  const int pieces = PER * chunks;
   const int64_t strip = (int64_t)first + blockIdx.x;  // of all matrices
   const int64_t matrix = strip / strips;
   const int n0 = (int)(strip - matrix * strips) * 16;
   for (int i = (int)blockIdx.y * 256 + (int)threadIdx.x; i < pieces; i += (int)gridDim.y * 256) {
-    const int col = i % 16, n = n0 + col;
-    const int64_t row = matrix * N + n;
+    const int c = i / PER, p = i - PER * c;
     u32x4_t o = {0u, 0u, 0u, 0u};
-    if (i < 64 * steps) {
-      const int b = i / 16;
+    if (p < 256) {
+      const int n = n0 + p % 16, b = 16 * c + 4 * (p / 16 % 4) + p / 64;
       if (n < N && b < blocks) {
-        const uint8_t* p = codes + row * ldc + 16 * b;
-        if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-          o = *reinterpret_cast<const u32x4_t*>(p);
+        const uint8_t* src = codes + (matrix * N + n) * ldc + 16 * b;
+        if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+          o = *reinterpret_cast<const u32x4_t*>(src);
         } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j / 4] |= (uint32_t)p[j] << (8 * (j % 4));
+          for (int j = 0; j < 16; ++j) o[j / 4] |= (uint32_t)src[j] << (8 * (j % 4));
         }
       }
     } else {
-      const int c = (i - 64 * steps) / 16;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const int b = 16 * c + j;
-        const uint32_t e = n < N && b < blocks ? scales[row * lds + b] : 127u;
+        const int l = 4 * (p - 256) + j / 4, n = n0 + l % 16, b = 16 * c + 4 * (l / 16) + j % 4;
+        const uint32_t e = n < N && b < blocks ? scales[(matrix * N + n) * lds + b] : 127u;
         o[j / 4] |= e << (8 * (j % 4));
       }
     }
@@ -211,12 +208,12 @@ template <int XDT>
 static hipError_t quantize_packed_t(const void* x, int64_t ldx, uint8_t* w, int M, int K, hipStream_t s) {
   typedef typename Elem<XDT>::type T;
   const bool vec = vec8_ok(x, ldx, K, sizeof(T)) && K % 8 == 0;
-  // strips of one launch: at most 2^31 steps
-  const int64_t strips = ((int64_t)M + 15) / 16, most = (int64_t(1) << 25) / mx4_steps(K);
+  // strips of one launch: at most 2^25 waves
+  const int64_t strips = ((int64_t)M + 15) / 16, most = (int64_t(1) << 23) / mx4_chunks(K);
   hipError_t e = hipSuccess;
   for (int64_t f = 0; f < strips && e == hipSuccess; f += most) {
     const int64_t n = strips - f < most ? strips - f : most;
-    const uint32_t total = (uint32_t)(n * mx4_steps(K));
+    const uint32_t total = (uint32_t)(4 * n * mx4_chunks(K));
     e = launch_kernel(vec ? mx4_quantize_packed_kernel<XDT, true> : mx4_quantize_packed_kernel<XDT, false>,
                       dim3((total + 3) / 4), dim3(256), s, static_cast<const T*>(x) + 16 * f * ldx, ldx,
                       w + f * mx4_strip_bytes(K), total, (int)(M - 16 * f < 16 * n ? M - 16 * f : 16 * n), K);

@@ -1,7 +1,7 @@
 // mx4_skinny.hip -- products of microscaled 4-bit codes, y = x^ W^t.
 //
 // A workgroup owns 16 rows and one strip of 16 columns; its 4 waves take steps
-// of 128 values in turn and add their sums in LDS.  The packed strip is the
+// of 128 values (a quarter of a chunk) in turn and add their sums in LDS.  The packed strip is the
 // matrix cores' operand: 1 KiB of consecutive bytes per step.
 #include "mx4_device.h"
 
@@ -13,17 +13,17 @@ __global__ __launch_bounds__(256) void mx4_skinny_kernel(Mx4Args g, int strips) 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
   const int strip = (int)(blockIdx.x % (unsigned)strips), m0 = 16 * (int)(blockIdx.x / (unsigned)strips);
-  const int steps = mx4_steps(g.K), blocks = mx4_blocks(g.K);
+  const int steps = 4 * mx4_chunks(g.K), blocks = mx4_blocks(g.K);
   const uint8_t* w = g.w + (int64_t)strip * mx4_strip_bytes(g.K);
-  const uint8_t* ws = w + (int64_t)1024 * steps;
   const int m = m0 + l16;
   const uint8_t* a = g.a + (int64_t)(m < g.M ? m : 0) * g.lda;
   const uint8_t* sa = g.sa + (int64_t)(m < g.M ? m : 0) * g.ldsa;
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
   for (int s = wave; s < steps; s += 4) {
-    const int b = 4 * s + quad;
-    const u32x4_t cb = *reinterpret_cast<const u32x4_t*>(w + 1024 * s + 16 * lane);
-    const uint32_t eb = ws[256 * (s / 4) + 16 * l16 + 4 * (s % 4) + quad];
+    const int b = 16 * (s / 4) + 4 * quad + s % 4;
+    const uint8_t* c = w + (int64_t)kChunkBytes * (s / 4);
+    const u32x4_t cb = *reinterpret_cast<const u32x4_t*>(c + 1024 * (s % 4) + 16 * lane);
+    const uint32_t eb = c[4096 + 4 * lane + s % 4];
     u32x4_t ca = {0u, 0u, 0u, 0u};
     uint32_t ea = 127;
     if (b < blocks && m < g.M) {

@@ -74,11 +74,11 @@ QMM_API size_t qmm_mx4_packed_bytes(int N, int K);
  * qmm_mx4_pack: `batch` weights (N, K), codes (batch N, 16 B) and scales (batch N,
  * B) as above (any alignment and ld), to `batch` packed weights one after the other (offline).
  * W starts on 16 bytes.  A packed weight is the matrix cores' operand:
- *   columns (rows n of the weight) in strips of 16, K in steps of 128, S = ceil(K
- *   / 128).  A strip is 1024 S bytes of codes and 256 ceil(S / 4) of scales.
- *   Codes: bytes 1024 s + 16 L .. + 15 hold block 4 s + L / 16 of column 16 strip + L % 16.
- *   Scales: byte 256 c + 16 l + b is the scale of block 16 c + b of column 16
- *   strip + l.
+ *   columns (rows n of the weight) in strips of 16, K in chunks of 512 values (16
+ *   blocks); a chunk of a strip is 4352 bytes, a strip's chunks follow each other.
+ *   Codes: its bytes 1024 j + 16 L .. + 15, j < 4, L < 64, hold block 4 (L / 16) + j of
+ *   column 16 strip + L % 16.
+ *   Scales: its byte 4096 + 4 L + j is that block's scale.
  *   Blocks and columns that do not exist have codes 0 and scale byte 127.
  */
 QMM_API qmm_status qmm_mx4_pack(const uint8_t* codes, int64_t ldc, const uint8_t* scales,

@@ -114,16 +114,16 @@ def test_pack_by_the_header(e, n, k):
     q, s = m4.coded(e * n, k, seed=n + k, lo=0, hi=255)
     B = m4.blocks(k)
     W = qmm.mx4_pack(q.view(e, n, -1).cuda(), s.view(e, n, -1).cuda())
-    strips, S = -(-n // 16), -(-k // 128)
-    W = W.cpu().view(e, strips, 1024 * S + 256 * (-(-S // 4)))
-    codes = torch.zeros((e, strips, 16, 4 * S, 16), dtype=torch.uint8)
-    scales = torch.full((e, strips, 16, 16 * -(-S // 4)), 127, dtype=torch.uint8)
+    strips, C = -(-n // 16), -(-k // 512)
+    W = W.cpu().view(e, strips, C, 4352)
+    codes = torch.zeros((e, strips, 16, C, 4, 4, 16), dtype=torch.uint8)  # column, chunk, block / 4, block % 4, byte
+    scales = torch.full((e, strips, 16, C, 4, 4), 127, dtype=torch.uint8)
     for i in range(e):
         for j in range(n):
-            codes[i, j // 16, j % 16, :B] = q[i * n + j].view(B, 16)
-            scales[i, j // 16, j % 16, :B] = s[i * n + j]
-    assert torch.equal(W[:, :, :1024 * S].reshape(e, strips, S, 4, 16, 16), codes.view(e, strips, 16, S, 4, 16).permute(0, 1, 3, 4, 2, 5))
-    assert torch.equal(W[:, :, 1024 * S:].reshape(e, strips, -1, 16, 16), scales.view(e, strips, 16, -1, 16).permute(0, 1, 3, 2, 4))
+            codes[i, j // 16, j % 16].view(16 * C, 16)[:B] = q[i * n + j].view(B, 16)
+            scales[i, j // 16, j % 16].view(16 * C)[:B] = s[i * n + j]
+    assert torch.equal(W[..., :4096].reshape(e, strips, C, 4, 4, 16, 16), codes.permute(0, 1, 3, 5, 4, 2, 6))
+    assert torch.equal(W[..., 4096:].reshape(e, strips, C, 4, 16, 4), scales.permute(0, 1, 3, 4, 2, 5))
     two = qmm.mx4_pack(q[:n].cuda(), s[:n].cuda())
     assert torch.equal(two.cpu(), W[0].flatten())
 

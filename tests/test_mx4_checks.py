@@ -96,9 +96,9 @@ def test_nothing_to_do(fn, over):
 
 
 def test_sizes():
-    # strips of 16 columns: 1024 bytes of codes for each 128 values, 256 of scales for each 512
-    assert L.qmm_mx4_packed_bytes(16, 128) == 1280 and L.qmm_mx4_packed_bytes(1, 1) == 1280
-    assert L.qmm_mx4_packed_bytes(17, 512) == 2 * (4096 + 256) and L.qmm_mx4_packed_bytes(16, 513) == 5 * 1024 + 512
+    # strips of 16 columns, chunks of 512 values: 4096 bytes of codes and 256 of scales
+    assert L.qmm_mx4_packed_bytes(16, 512) == L.qmm_mx4_packed_bytes(1, 1) == 4352
+    assert L.qmm_mx4_packed_bytes(17, 512) == 2 * 4352 and L.qmm_mx4_packed_bytes(16, 513) == 2 * 4352
     assert L.qmm_mx4_packed_bytes(0, 128) == L.qmm_mx4_packed_bytes(16, 0) == L.qmm_mx4_packed_bytes(16, 1 << 20) == 0
     assert L.qmm_mx4_workspace_bytes(100, 4096, 4) == 0 and L.qmm_mx4_workspace_bytes(0, 64, 1) == 0
     assert L.qmm_mx4_workspace_bytes(100, 1 << 20, 1) == 0 and L.qmm_mx4_workspace_bytes(2 ** 31 - 1, 64, 1) == 0
