@@ -72,16 +72,14 @@ struct MoeArgs {
   int weights_dtype;
   void* ws;
 };
-// What a call keeps in its workspace, offsets in bytes:
-//   ids, w  (T, top_k) int32 and fp32: experts (-1: none) and weights
-//   x       (parts of x, T, Dp) bf16: x as a sum of parts
-//   h       (parts of h, T top_k, Ip) bf16: w act(g) u as a sum of parts
+// What a call keeps in its workspace (offsets in bytes; MoeBufs in mx4_moe.hip): tables of the choices for
+// `slots` experts, x and h as sums of bf16 parts, rows padded to whole blocks.
 struct MoePlan {
   int xparts, hparts;
-  int Dp, Ip;
-  size_t ids, w, x, h, bytes;
+  int Dp, Ip, slots;
+  size_t list, who, place, x, h, bytes;
 };
-MoePlan plan_moe(int T, int D, int I, int top_k, int x_dtype, int y_dtype);
+MoePlan plan_moe(int T, int D, int I, int E, int top_k, int x_dtype, int y_dtype);
 hipError_t launch_mx4_moe(const MoeArgs& a, const MoePlan& p, hipStream_t s);
 
 }  // namespace qmm
