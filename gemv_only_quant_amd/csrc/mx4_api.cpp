@@ -87,12 +87,12 @@ qmm_status check_workspace(const char* fn, size_t need, const void* ws, size_t b
   return QMM_OK;
 }
 
-constexpr int64_t kMaxHidden = (int64_t(1) << 28) - (int64_t(1) << 16);  // a part of h fits 32-bit byte offsets
+constexpr int64_t kMaxHidden = (int64_t(1) << 28) - (int64_t(1) << 16);  // a part of h, and z, fit 32-bit byte offsets
 
 bool moe_sizes_ok(int T, int D, int I, int E, int top_k) {
   return T >= 0 && D >= 0 && I >= 0 && E >= 0 && top_k >= 0 && T <= QMM_MX4_MAX_TOKENS && D < kMaxK &&
          I < kMaxK && E <= QMM_MX4_MAX_EXPERTS && top_k <= QMM_MX4_MAX_TOP_K &&
-         (int64_t)T * top_k * I < kMaxHidden;
+         (int64_t)T * top_k * (I > D ? I : D) < kMaxHidden;
 }
 
 }  // namespace
@@ -213,7 +213,7 @@ qmm_status qmm_mx4_gemm(const void* x, int x_dtype, int64_t ldx, const uint8_t* 
 size_t qmm_mx4_moe_workspace_bytes(int T, int D, int I, int E, int top_k, int x_dtype, int y_dtype) {
   if (!moe_sizes_ok(T, D, I, E, top_k) || !value_type(x_dtype) || !value_type(y_dtype)) return 0;
   if (T == 0 || D == 0 || I == 0 || E == 0 || top_k == 0) return 0;
-  return qmm::plan_moe(T, D, I, E, top_k, x_dtype, y_dtype).bytes;
+  return qmm::plan_moe(T, D, I, top_k, x_dtype, y_dtype).bytes;
 }
 
 qmm_status qmm_mx4_moe(const void* x, int x_dtype, int64_t ldx, const void* Wg, const void* Wu,
@@ -230,7 +230,7 @@ qmm_status qmm_mx4_moe(const void* x, int x_dtype, int64_t ldx, const void* Wg, 
     QMM_REFUSE(QMM_ERR_ARG, "%s: negative size T=%d D=%d I=%d E=%d top_k=%d", fn, T, D, I, E, top_k);
   if (!moe_sizes_ok(T, D, I, E, top_k))
     QMM_REFUSE(QMM_ERR_UNSUPPORTED,
-               "%s: T=%d (at most %d), E=%d (%d), top_k=%d (%d), D=%d or I=%d (< %d) or T top_k I (< %lld) too large",
+               "%s: T=%d (at most %d), E=%d (%d), top_k=%d (%d), D=%d or I=%d (< %d) or T top_k max(D, I) (< %lld) too large",
                fn, T, QMM_MX4_MAX_TOKENS, E, QMM_MX4_MAX_EXPERTS, top_k, QMM_MX4_MAX_TOP_K, D, I, kMaxK,
                (long long)kMaxHidden);
   if (logits != nullptr) {
@@ -262,7 +262,7 @@ qmm_status qmm_mx4_moe(const void* x, int x_dtype, int64_t ldx, const void* Wg, 
     if (!aligned(ids, (uintptr_t)ids_size) || !aligned(weights, (uintptr_t)type_size(weights_dtype)))
       QMM_REFUSE(QMM_ERR_ARG, "%s: ids and weights must be aligned to their elements", fn);
   }
-  const qmm::MoePlan p = qmm::plan_moe(T, D, I, E, top_k, x_dtype, y_dtype);
+  const qmm::MoePlan p = qmm::plan_moe(T, D, I, top_k, x_dtype, y_dtype);
   QMM_CHECK(check_workspace(fn, p.bytes, workspace, workspace_bytes, 256));
   qmm::MoeArgs a{};
   a.x = x, a.x_dtype = x_dtype, a.ldx = ldx;

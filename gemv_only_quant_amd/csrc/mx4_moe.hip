@@ -53,129 +53,104 @@ __device__ __forceinline__ float value_of(uint32_t order) {
   return __builtin_bit_cast(float, order & 0x80000000u ? order & 0x7FFFFFFFu : ~order);
 }
 
+// Activations lie in rows of whole chunks, a chunk's 512 values in the order in which the matrix cores
+// take them: eight values i of blocks 4 q + j at 128 j + 32 i + 8 q, so that what a load takes of a row
+// are 64 consecutive bytes (in the order of K it would touch four lines of each row, and
+// the address units, one line at a time, would bound the kernel).
+__device__ __forceinline__ int operand_order(int k) {
+  const int b = k / 32;
+  return (k & ~511) + 128 * (b & 3) + 32 * ((k >> 3) & 3) + 8 * ((b >> 2) & 3) + (k & 7);
+}
+
 // What the first launch leaves for the others, in the workspace.
 struct MoeBufs {
-  int* slots;      // the experts that some token chose, ascending, then -1
-  uint64_t* who;   // the tokens of each of them, a bit each
-  uint2* place;    // (slot, token): the first of its places that holds the expert, and the sum of all
-                   // such places' weights
-  uint16_t* x;     // (parts, T, Dp)
+  int* ids;        // (T, top_k) experts, -1: none
+  float* w;        // and their weights
+  uint32_t* done;  // workgroups that have left their part of a strip of y, 0 at first
+  uint16_t* x;     // (parts, T, Dp): x as a sum of bf16 parts
   uint16_t* h;     // (parts, T top_k, Ip)
+  float* z;        // (T top_k, Dz): a token's rows of each of its experts
 };
 
-// Workgroup 0: the tokens' choices and the tables above.  The others: x as parts.
-constexpr int kRouteWaves = 16;
-
+// A wave for each token's choice (the first T), then threads for x as parts.
 template <int XP>
-__global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(MoeArgs g, MoeBufs o, int Dp, int slots) {
-  const int tid = threadIdx.x, lane = tid & 63, k = g.top_k;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  if (blockIdx.x > 0) {
+__global__ __launch_bounds__(256) void moe_route_kernel(MoeArgs g, MoeBufs o, int strips, int Dp) {
+  const int tid = (int)blockIdx.x * 256 + (int)threadIdx.x, lane = threadIdx.x & 63, k = g.top_k;
+  const int t = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int i = tid; i < strips; i += (int)gridDim.x * 256) o.done[i] = 0;
+  const int groups = (g.T + 3) / 4;  // workgroups that choose
+  if ((int)blockIdx.x >= groups) {
     const int units = Dp / 8;
-    for (int u = ((int)blockIdx.x - 1) * 64 * kRouteWaves + tid; u < g.T * units; u += ((int)gridDim.x - 1) * 64 * kRouteWaves) {
-      const int t = u / units, i = 8 * (u - t * units);
+    for (int u = tid - 256 * groups; u < g.T * units; u += ((int)gridDim.x - groups) * 256) {
+      const int r = u / units, i = 8 * (u - r * units);
       uint16_t p[8][XP];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        parts_of<XP>(i + j < g.D ? as_f32(g.x, (int64_t)t * g.ldx + i + j, g.x_dtype) : 0.f, p[j]);
+        parts_of<XP>(i + j < g.D ? as_f32(g.x, (int64_t)r * g.ldx + i + j, g.x_dtype) : 0.f, p[j]);
 #pragma unroll
       for (int q = 0; q < XP; ++q) {
         u32x4_t v;
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = p[2 * j][q] | ((uint32_t)p[2 * j + 1][q] << 16);
-        *reinterpret_cast<u32x4_t*>(o.x + ((int64_t)q * g.T + t) * Dp + i) = v;
+        *reinterpret_cast<u32x4_t*>(o.x + ((int64_t)q * g.T + r) * Dp + operand_order(i)) = v;
       }
     }
     return;
   }
-  __shared__ int ids[kMoeTokens * kMoeTopK];
-  __shared__ float ws[kMoeTokens * kMoeTopK];
-  __shared__ int list[kMoeExperts];
-  __shared__ int flag[kMoeExperts];
-  __shared__ int count;
-  for (int i = tid; i < g.E; i += 64 * kRouteWaves) flag[i] = 0;
-  __syncthreads();
+  if (t >= g.T) return;
   if (g.logits == nullptr) {
-    for (int i = tid; i < g.T * k; i += 64 * kRouteWaves) {
+    if (lane < k) {
+      const int64_t i = (int64_t)t * k + lane;
       const int64_t e = g.ids_size == 8 ? static_cast<const int64_t*>(g.ids)[i] : static_cast<const int32_t*>(g.ids)[i];
-      const bool ok = e >= 0 && e < g.E;
-      ids[i] = ok ? (int)e : -1;
-      ws[i] = as_f32(g.weights, i, g.weights_dtype);
-      if (ok) flag[(int)e] = 1;
+      o.ids[i] = e >= 0 && e < g.E ? (int)e : -1;
+      o.w[i] = as_f32(g.weights, i, g.weights_dtype);
     }
-  } else {
-    for (int t = wave; t < g.T; t += kRouteWaves) {
-      // k times the largest key (order, then lowest index) that is below the last; the first
-      // 128 experts' keys stay in registers
-      constexpr int HELD = 2;
-      auto key_of = [&](int e) -> uint64_t {
-        if (e >= g.E) return 0;
-        const float v = as_f32(g.logits, (int64_t)t * g.ldl + e, g.logits_dtype);
-        return v == -__builtin_inff() ? 0 : ((uint64_t)order_of(v) << 32) | (uint32_t)(kMoeExperts - e);
-      };
-      uint64_t held[HELD];
-#pragma unroll
-      for (int i = 0; i < HELD; ++i) held[i] = key_of(64 * i + lane);
-      float first = 0.f, sum = 0.f, mine = 0.f;
-      uint64_t last = ~uint64_t(0);
-      int chosen = -1;
-      for (int j = 0; j < k; ++j) {
-        uint64_t best = 0;
-#pragma unroll
-        for (int i = 0; i < HELD; ++i) best = held[i] < last && held[i] > best ? held[i] : best;
-        for (int e = 64 * HELD + lane; e < g.E; e += 64) {
-          const uint64_t key = key_of(e);
-          best = key < last && key > best ? key : best;
-        }
-        // the largest order, and of its lanes the largest rest (the lowest index)
-        const uint32_t hi = wave_max_u32((uint32_t)(best >> 32));
-        const uint32_t lo = wave_max_u32((uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
-        if (hi == 0) break;  // no expert is left
-        last = ((uint64_t)hi << 32) | lo;
-        const float v = value_of(hi);
-        if (j == 0) first = v;
-        // (NaN, and infinity less infinity: the whole row)
-        const float p = first - first == 0.f ? exp_f32(v - first) : __builtin_nanf("");
-        sum += p;
-        if (lane == j) mine = p, chosen = kMoeExperts - (int)lo;
-      }
-      if (!g.renormalize) {
-        float all = 0.f;
-        for (int e = lane; e < g.E; e += 64) all += exp_f32(as_f32(g.logits, (int64_t)t * g.ldl + e, g.logits_dtype) - first);
-        sum = sum == sum ? wave_sum(all) : sum;
-      }
-      if (lane < k) {
-        ids[t * k + lane] = chosen;
-        ws[t * k + lane] = mine / sum;
-        if (chosen >= 0) flag[chosen] = 1;
-      }
-    }
+    return;
   }
-  __syncthreads();
-  if (wave == 0) {
-    int c = 0;
-    for (int b = 0; b < g.E; b += 64) {
-      const bool on = b + lane < g.E && flag[b + lane] != 0;
-      const uint64_t m = __ballot(on);
-      if (on) list[c + __popcll(m & ((uint64_t(1) << lane) - 1))] = b + lane;
-      c += __popcll(m);
-    }
-    if (lane == 0) count = c;
+  // k times the largest key (order, then lowest index) that is below the last; the first
+  // 256 experts' stay in registers
+  constexpr int HELD = 4;
+  auto order_at = [&](int e) -> uint32_t {
+    if (e >= g.E) return 0;
+    const float v = as_f32(g.logits, (int64_t)t * g.ldl + e, g.logits_dtype);
+    return v == -__builtin_inff() ? 0 : order_of(v);
+  };
+  uint32_t held[HELD];
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) held[i] = order_at(64 * i + lane);
+  float first = 0.f, sum = 0.f, mine = 0.f;
+  uint32_t last = 0xFFFFFFFFu;  // the last one's order, and its index
+  int last_e = -1, chosen = -1;
+  for (int j = 0; j < k; ++j) {
+    // this lane's largest of those behind the last one, its lowest index
+    uint32_t best = 0;
+    int at = 0;
+    auto consider = [&](uint32_t v, int e) {
+      const bool open = v < last || (v == last && e > last_e);
+      if (open && v > best) best = v, at = e;
+    };
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) consider(held[i], 64 * i + lane);
+    for (int e = 64 * HELD + lane; e < g.E; e += 64) consider(order_at(e), e);
+    const uint32_t top = wave_max_u32(best);
+    if (top == 0) break;  // no expert is left
+    last = top;
+    last_e = kMoeExperts - (int)wave_max_u32(best == top ? (uint32_t)(kMoeExperts - at) : 0u);
+    const float v = value_of(top);
+    if (j == 0) first = v;
+    // (NaN, and infinity less infinity: the whole row)
+    const float p = first - first == 0.f ? exp_f32(v - first) : __builtin_nanf("");
+    sum += p;
+    if (lane == j) mine = p, chosen = last_e;
   }
-  __syncthreads();
-  for (int s = wave; s < slots; s += kRouteWaves) {
-    const int e = s < count ? list[s] : -1;
-    int at = -1;
-    float w = 0.f;
-    if (lane < g.T && e >= 0)
-      for (int j = 0; j < k; ++j)
-        if (ids[lane * k + j] == e) {
-          at = at < 0 ? j : at;
-          w += ws[lane * k + j];
-        }
-    const uint64_t m = __ballot(at >= 0);
-    if (lane == 0) o.slots[s] = e, o.who[s] = m;
-    o.place[64 * s + lane] = uint2{(uint32_t)at, __builtin_bit_cast(uint32_t, w)};
+  if (!g.renormalize) {
+    float all = 0.f;
+    for (int e = lane; e < g.E; e += 64) all += exp_f32(as_f32(g.logits, (int64_t)t * g.ldl + e, g.logits_dtype) - first);
+    sum = sum == sum ? wave_sum(all) : sum;
+  }
+  if (lane < k) {
+    o.ids[t * k + lane] = chosen;
+    o.w[t * k + lane] = mine / sum;
   }
 }
 
@@ -201,11 +176,11 @@ __device__ __forceinline__ void load_chunk(MoeChunk& w, const uint8_t* p, int nb
 template <int P> struct MoeRows {
   u32x4_t a[P][4];
   __device__ __forceinline__ void load(const buf_t (&b)[P], int off, int j, int nb, int lane) {
-    const int at = 4 * (lane >> 4) + j < nb ? off + 256 * (lane >> 4) + 64 * j : kNowhere;
+    const int at = 4 * (lane >> 4) + j < nb ? off + 16 * (lane >> 4) + 256 * j : kNowhere;
 #pragma unroll
     for (int q = 0; q < P; ++q)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[q][i] = buf_load128(b[q], at + 16 * i);
+      for (int i = 0; i < 4; ++i) a[q][i] = buf_load128(b[q], at + 64 * i);
   }
 };
 // Buffers of the parts of `rows` rows of `ld` bf16 values.
@@ -225,158 +200,222 @@ __device__ __forceinline__ void multiply(f32x4_t& acc, const MoeRows<P>& r, cons
   }
 }
 
+// An expert's tokens, from the slot of a workgroup: expert `slot` itself, or (`pairs`) the expert of
+// place `slot` of all tokens' choices unless an earlier place has it too.
+struct MoeGroup {
+  int e;          // -1: none
+  uint64_t who;   // its tokens, a bit each
+  int place;      // lane t: the first of token t's places that holds it, or -1
+  float w;        // and the sum of all such places' weights
+};
+__device__ __forceinline__ MoeGroup group_of(const MoeBufs& o, int slot, bool pairs, int T, int k, int lane) {
+  MoeGroup m;
+  m.e = slot;
+  if (pairs) {
+    m.e = __builtin_amdgcn_readfirstlane(o.ids[slot]);
+    bool before = m.e < 0;
+    for (int p = lane; p < slot; p += 64) before |= o.ids[p] == m.e;
+    if (__ballot(before) != 0) m.e = -1;
+  }
+  m.place = -1;
+  m.w = 0.f;
+  if (lane < T && m.e >= 0) {
+    const int* ids = o.ids + lane * k;
+    const float* w = o.w + lane * k;
+#pragma unroll 4
+    for (int j = k - 1; j >= 0; --j) {
+      const bool same = ids[j] == m.e;
+      m.place = same ? j : m.place;
+      m.w += same ? w[j] : 0.f;
+    }
+  }
+  m.who = __ballot(m.place >= 0);
+  if (m.who == 0) m.e = -1;
+  return m;
+}
+
+// acc[p] += rows times w[p] over what a wave has of K: with TWO weights the same chunk of both, else two chunks
+// of one, whose sums are added.  The loads of the next pair go out before the last two of four
+// steps, behind all loads that these wait for (loads return in order).
+template <int P, bool TWO, class Fetch>
+__device__ __forceinline__ void sweep(f32x4_t (&acc)[2], MoeChunk (&w)[2], const buf_t (&rows)[P], int off, int first,
+                                      int stride, int chunks, int blocks, int lane, Fetch&& fetch) {
+  constexpr int A = TWO ? 1 : 2;  // row chunks at once
+  for (int c = first; c < chunks; c += stride) {
+    MoeChunk wn[2];
+    MoeRows<P> a[2];
+    constexpr int STEPS = 4 * A;
+    auto take = [&](int s) {
+      const int cc = c + (TWO ? 0 : s / 4);
+      a[s & 1].load(rows, off + 1024 * cc, s % 4, blocks - 16 * cc, lane);
+    };
+    take(0);
+    take(1);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      if (s == STEPS - 2) fetch(wn, c + stride);
+#pragma unroll
+      for (int p = 0; p < (TWO ? 2 : 1); ++p) {
+        const MoeChunk& m = w[TWO ? p : s / 4];
+        multiply<P>(acc[TWO ? p : s & 1], a[s & 1], m.c[s % 4], scale_f32((m.s >> (8 * (s % 4))) & 255));
+      }
+      if (s + 2 < STEPS) take(s + 2);
+    }
+    w[0] = wn[0], w[1] = wn[1];
+  }
+}
+
 // ---- first half ----------------------------------------------------------------
 // A workgroup: 16 columns of h of one expert, the waves taking chunks of K in turn.
 constexpr int kUpWaves = 4;
 
 template <int XP, int HP>
-__global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(MoeArgs g, MoeBufs o, int Dp, int Ip) {
+__global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(MoeArgs g, MoeBufs o, int Dp, int Ip, int pairs) {
   __shared__ float sums[kUpWaves][2][16][17];
-  __shared__ int tok[kMoeTokens];
-  __shared__ uint2 place[kMoeTokens];
+  __shared__ int tok[kMoeTokens], place[kMoeTokens];
+  __shared__ float wt[kMoeTokens];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
-  const int strip = (int)blockIdx.x, slot = (int)blockIdx.y;
-  const int e = o.slots[slot];
-  const uint64_t who = o.who[slot];
-  if (e < 0) return;
+  const int strip = (int)blockIdx.x;
+  const MoeGroup m = group_of(o, (int)blockIdx.y, pairs != 0, g.T, g.top_k, lane);
+  if (m.e < 0) return;
   const int chunks = mx4_chunks(g.D), blocks = mx4_blocks(g.D);
-  const int64_t at = (int64_t)e * mx4_weight_bytes(g.I, g.D) + (int64_t)strip * mx4_strip_bytes(g.D);
+  const int64_t at = (int64_t)m.e * mx4_weight_bytes(g.I, g.D) + (int64_t)strip * mx4_strip_bytes(g.D);
   const bool real = 16 * strip < g.I;  // h's columns are padded to whole blocks, with zeros
   auto fetch = [&](MoeChunk (&w)[2], int c) {
-    load_chunk(w[0], real ? g.wg + at + (int64_t)kChunkBytes * c : nullptr, blocks - 16 * c, lane);
-    load_chunk(w[1], real ? g.wu + at + (int64_t)kChunkBytes * c : nullptr, blocks - 16 * c, lane);
+    const bool ok = real && c < chunks;
+    load_chunk(w[0], ok ? g.wg + at + (int64_t)kChunkBytes * c : nullptr, blocks - 16 * c, lane);
+    load_chunk(w[1], ok ? g.wu + at + (int64_t)kChunkBytes * c : nullptr, blocks - 16 * c, lane);
   };
-  MoeChunk w[2], wn[2];
-  int c0 = wave;
-  if (c0 < chunks) fetch(w, c0);
-  const int members = __popcll(who);
-  if (wave == 0) {
-    place[lane] = o.place[64 * slot + lane];
-    if ((who >> lane) & 1) tok[__popcll(who & ((uint64_t(1) << lane) - 1))] = lane;
+  MoeChunk w[2];
+  fetch(w, wave);
+  const int members = __popcll(m.who);
+  if (wave == 0 && m.place >= 0) {
+    const int r = __popcll(m.who & ((uint64_t(1) << lane) - 1));
+    tok[r] = lane, place[r] = m.place, wt[r] = m.w;
   }
   __syncthreads();
   buf_t xb[XP];
   part_buffers<XP>(xb, o.x, g.T, Dp);
   for (int r0 = 0; r0 < members; r0 += 16) {
     const int row = r0 + l16;
-    const int xoff = row < members ? 2 * tok[row] * Dp : kNowhere;
+    const int off = row < members ? 2 * tok[row] * Dp : kNowhere;
     f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    if (r0 > 0 && wave < chunks) fetch(w, wave);
-    for (int c = wave; c < chunks; c += kUpWaves) {
-      const int nb = blocks - 16 * c;
-      MoeRows<XP> a[2];
-      a[0].load(xb, xoff + 1024 * c, 0, nb, lane);
-      if (c + kUpWaves < chunks) fetch(wn, c + kUpWaves);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j < 3) a[(j + 1) & 1].load(xb, xoff + 1024 * c, j + 1, nb, lane);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) multiply<XP>(acc[p], a[j & 1], w[p].c[j], scale_f32((w[p].s >> (8 * j)) & 255));
-      }
-      w[0] = wn[0], w[1] = wn[1];
-    }
+    if (r0 > 0) fetch(w, wave);
+    sweep<XP, true>(acc, w, xb, off, wave, kUpWaves, chunks, blocks, lane, fetch);
     if (r0 > 0) __syncthreads();
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int q = 0; q < 4; ++q) sums[wave][p][4 * quad + q][l16] = acc[p][q];
     __syncthreads();
-    const int rr = threadIdx.x / 16, col = threadIdx.x % 16;
-    if (r0 + rr < members) {
-      const int t = tok[r0 + rr];
-      const uint2 pl = place[t];
+    const int rr = threadIdx.x / 16, col = threadIdx.x % 16, r = r0 + rr;
+    if (r < members) {
       float gv = 0.f, uv = 0.f;
 #pragma unroll
       for (int q = 0; q < kUpWaves; ++q) gv += sums[q][0][rr][col], uv += sums[q][1][rr][col];
       float h = 0.f;
       with_act(g.act, [&](auto a) {
         float d;
-        h = act_parts<decltype(a)::value>(gv, &d) * uv * __builtin_bit_cast(float, pl.y);
+        h = act_parts<decltype(a)::value>(gv, &d) * uv * wt[r];
       });
       uint16_t p[HP];
       parts_of<HP>(16 * strip + col < g.I ? h : 0.f, p);  // the padding is 0 whatever x is
 #pragma unroll
       for (int q = 0; q < HP; ++q)
-        o.h[((int64_t)q * g.T * g.top_k + t * g.top_k + (int)pl.x) * Ip + 16 * strip + col] = p[q];
+        o.h[((int64_t)q * g.T * g.top_k + tok[r] * g.top_k + place[r]) * Ip + operand_order(16 * strip + col)] = p[q];
     }
   }
 }
 
 // ---- second half ---------------------------------------------------------------
-// A workgroup: COLS columns of y (16, or 8 or 4 of a strip where strips are too few to occupy the chip), all
-// experts; the waves take shares of (expert, chunk), one after the other.  An expert's rows are added to the
-// wave's sums of its tokens in LDS, the waves' sums in their order at the end.
-constexpr int kDownWaves = 16;
+// A workgroup: 16 columns of one expert's rows of y, the waves taking pairs of chunks in turn.  The last
+// of a strip's workgroups to come adds each token's rows in the order of its choices.
+constexpr int kDownWaves = 4;
 
-template <int TMAX, int HP>
-__global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeArgs g, MoeBufs o, int Ip, int slots, int cols) {
-  __shared__ float sums[kDownWaves][TMAX][17];
-  __shared__ int toks[kDownWaves][kMoeTokens];
+template <int HP>
+__global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int Dz) {
+  __shared__ float sums[kDownWaves][16][17];
+  __shared__ int tok[kMoeTokens], place[kMoeTokens];
+  __shared__ uint32_t arrived;
+  __shared__ bool valid[kMoeTokens * kMoeTopK];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
-  const int per = 16 / cols, strip = (int)blockIdx.x / per, part = (int)blockIdx.x % per;
-  const bool mine = l16 / cols == part;
-  const int chunks = mx4_chunks(g.I), blocks = mx4_blocks(g.I);
-  int count = 0;
-  for (int s = 0; s < slots; s += 64) count += __popcll(__ballot(s + lane < slots && o.slots[min(s + lane, slots - 1)] >= 0));
-  for (int i = lane; i < TMAX * 17; i += 64) (&sums[wave][0][0])[i] = 0.f;
-  buf_t hb[HP];
-  part_buffers<HP>(hb, o.h, g.T * g.top_k, Ip);
-  const int items = count * chunks;
-  const int end = (int)((int64_t)items * (wave + 1) / kDownWaves);
-  int it = (int)((int64_t)items * wave / kDownWaves);
-  auto where = [&](int i) -> const uint8_t* {
-    if (i >= end) return nullptr;
-    const int s = i / chunks;
-    return g.wd + (int64_t)o.slots[s] * mx4_weight_bytes(g.D, g.I) + (int64_t)strip * mx4_strip_bytes(g.I) +
-           (int64_t)kChunkBytes * (i - s * chunks);
-  };
-  auto fetch = [&](MoeChunk& w, int i) { load_chunk(w, where(i), mine ? blocks - 16 * (i % chunks) : 0, lane); };
-  MoeChunk w, wn;
-  fetch(w, it);
-  while (it < end) {
-    const int slot = it / chunks, c0 = it - slot * chunks, c1 = min(chunks, c0 + end - it);
-    const uint64_t who = o.who[slot];
-    const uint2 pl = o.place[64 * slot + lane];
-    const int members = __popcll(who);
-    if ((who >> lane) & 1) toks[wave][__popcll(who & ((uint64_t(1) << lane) - 1))] = lane | ((int)pl.x << 8);
+  const int strip = (int)blockIdx.x, k = g.top_k;
+  const MoeGroup m = group_of(o, (int)blockIdx.y, pairs != 0, g.T, k, lane);
+  const buf_t zb = make_buf(o.z, 4u * (uint32_t)(g.T * k) * (uint32_t)Dz);
+  const int rr = threadIdx.x / 16, col = threadIdx.x % 16, n = 16 * strip + col;
+  if (m.e >= 0) {
+    const int chunks = mx4_chunks(g.I), blocks = mx4_blocks(g.I);
+    const uint8_t* wd = g.wd + (int64_t)m.e * mx4_weight_bytes(g.D, g.I) + (int64_t)strip * mx4_strip_bytes(g.I);
+    auto fetch = [&](MoeChunk (&w)[2], int c) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        load_chunk(w[i], c + i < chunks ? wd + (int64_t)kChunkBytes * (c + i) : nullptr, blocks - 16 * (c + i), lane);
+    };
+    MoeChunk w[2];
+    fetch(w, 2 * wave);
+    const int members = __popcll(m.who);
+    if (wave == 0 && m.place >= 0) {
+      const int r = __popcll(m.who & ((uint64_t(1) << lane) - 1));
+      tok[r] = lane, place[r] = m.place;
+    }
+    __syncthreads();
+    buf_t hb[HP];
+    part_buffers<HP>(hb, o.h, g.T * k, Ip);
     for (int r0 = 0; r0 < members; r0 += 16) {
       const int row = r0 + l16;
-      const int tk = row < members ? toks[wave][row] : 0;
-      const int hoff = row < members ? 2 * ((tk & 255) * g.top_k + (tk >> 8)) * Ip : kNowhere;
-      const bool again = r0 + 16 < members;
-      f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-      for (int c = c0; c < c1; ++c) {
-        const int nb = blocks - 16 * c;
-        MoeRows<HP> a[2];
-        a[0].load(hb, hoff + 1024 * c, 0, nb, lane);
-        const int next = c + 1 < c1 ? it + c + 1 - c0 : (again ? it : it + c1 - c0);
-        fetch(wn, next);
+      const int off = row < members ? 2 * (tok[row] * k + place[row]) * Ip : kNowhere;
+      f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      if (r0 > 0) fetch(w, 2 * wave);
+      sweep<HP, false>(acc, w, hb, off, 2 * wave, 2 * kDownWaves, chunks, blocks, lane, fetch);
+      if (r0 > 0) __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j < 3) a[(j + 1) & 1].load(hb, hoff + 1024 * c, j + 1, nb, lane);
-          multiply<HP>(acc, a[j & 1], w.c[j], scale_f32((w.s >> (8 * j)) & 255));
-        }
-        w = wn;
-      }
+      for (int q = 0; q < 4; ++q) sums[wave][4 * quad + q][l16] = acc[0][q] + acc[1][q];
+      __syncthreads();
+      const int r = r0 + rr;
+      if (r < members) {
+        float v = 0.f;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int r = r0 + 4 * quad + q;
-        if (r < members) sums[wave][toks[wave][r] & 255][l16] += acc[q];
+        for (int q = 0; q < kDownWaves; ++q) v += sums[q][rr][col];
+        // past this XCD's L2: another XCD's workgroup may read it
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), zb, 4 * ((tok[r] * k + place[r]) * Dz + n), 0,
+                                              kCoherent);
       }
     }
-    it += c1 - c0;
+  }
+  // every wave's rows are in memory before the workgroup counts as arrived
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  __syncthreads();
+  if (threadIdx.x == 0)
+    arrived = __hip_atomic_fetch_add(&o.done[strip], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (arrived + 1 != gridDim.y) return;
+  // which of a token's places have rows: those of an expert that no earlier place has
+  for (int i = threadIdx.x; i < g.T * k; i += 64 * kDownWaves) {
+    const int e = o.ids[i], t = i / k;
+    bool first = e >= 0;
+    for (int b = t * k; b < i; ++b) first = first && o.ids[b] != e;
+    valid[i] = first;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < g.T * 16; i += 64 * kDownWaves) {
-    const int t = i / 16, col = i % 16, n = 16 * strip + col;
-    if (n >= g.D || col / cols != part) continue;
+  for (int i = threadIdx.x; i < 16 * g.T; i += 64 * kDownWaves) {
+    const int t = i / 16;
+    if (n >= g.D) continue;
     float v = 0.f;
+    for (int j0 = 0; j0 < k; j0 += 8) {  // 8 loads at once
+      float r[8];
 #pragma unroll
-    for (int q = 0; q < kDownWaves; ++q) v += sums[q][t][col];
+      for (int j = 0; j < 8; ++j) {
+        const int at = t * k + j0 + j;
+        const bool ok = j0 + j < k && valid[at];
+        r[j] = __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(zb, ok ? 4 * (at * Dz + n) : kNowhere, 0, kCoherent));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v += r[j];
+    }
     with_y(g.y, g.y_dtype, [&](auto* yt) {
       typedef typename std::remove_pointer<decltype(yt)>::type Y;
       yt[(int64_t)t * g.ldy + n] = (Y)v;
@@ -385,40 +424,40 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeArgs g, Mo
 }
 
 // ---------------------------------------------------------------- host side
-MoePlan plan_moe(int T, int D, int I, int E, int top_k, int x_dtype, int y_dtype) {
+MoePlan plan_moe(int T, int D, int I, int top_k, int x_dtype, int y_dtype) {
   MoePlan p{};
   p.xparts = x_dtype == YF32 ? 3 : x_dtype == XF16 ? 2 : 1;
   p.hparts = y_dtype == YF32 ? 3 : 2;
-  p.Dp = (int)round_up(D, kBlock);
-  p.Ip = (int)round_up(I, kBlock);
-  p.slots = (int64_t)T * top_k < E ? T * top_k : E;
+  p.Dp = (int)round_up(D, 512);
+  p.Ip = (int)round_up(I, 512);
+  p.Dz = (int)round_up(D, 16);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
     at += (size_t)round_up((int64_t)bytes, 256);
     return o;
   };
-  p.list = take((size_t)p.slots * 4);
-  p.who = take((size_t)p.slots * 8);
-  p.place = take((size_t)p.slots * 64 * 8);
+  p.ids = take((size_t)T * top_k * 4);
+  p.w = take((size_t)T * top_k * 4);
+  p.done = take((size_t)p.Dz / 16 * 4);
   p.x = take((size_t)p.xparts * T * p.Dp * 2);
   p.h = take((size_t)p.hparts * T * top_k * p.Ip * 2);
+  p.z = take((size_t)T * top_k * p.Dz * 4);
   p.bytes = at;
   return p;
 }
 
 template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
-  const int units = a.T * (p.Dp / 8), most = 64;
-  const int xg = (units + 64 * kRouteWaves - 1) / (64 * kRouteWaves);
-  hipError_t e = launch_kernel(moe_route_kernel<XP>, dim3((unsigned)(1 + (xg < most ? xg : most))), dim3(64 * kRouteWaves), s,
-                               a, o, p.Dp, p.slots);
+  const int xg = (a.T * (p.Dp / 8) + 255) / 256, strips = p.Dz / 16;
+  hipError_t e = launch_kernel(moe_route_kernel<XP>, dim3((unsigned)((a.T + 3) / 4 + (xg < 256 ? xg : 256))), dim3(256), s, a, o,
+                               strips, p.Dp);
   if (e != hipSuccess) return e;
-  e = launch_kernel(moe_up_kernel<XP, HP>, dim3((unsigned)(p.Ip / 16), (unsigned)p.slots), dim3(64 * kUpWaves), s, a, o,
-                    p.Dp, p.Ip);
+  // a workgroup for each expert, or for each place of the tokens' choices if these are fewer
+  const int pairs = a.T * a.top_k < a.E, slots = pairs ? a.T * a.top_k : a.E;
+  e = launch_kernel(moe_up_kernel<XP, HP>, dim3((unsigned)(round_up(a.I, kBlock) / 16), (unsigned)slots), dim3(64 * kUpWaves), s,
+                    a, o, p.Dp, p.Ip, pairs);
   if (e != hipSuccess) return e;
-  const int strips = (a.D + 15) / 16, cols = strips >= 192 ? 16 : strips >= 96 ? 8 : 4;
-  return launch_kernel(a.T <= 16 ? moe_down_kernel<16, HP> : moe_down_kernel<64, HP>,
-                       dim3((unsigned)(strips * (16 / cols))), dim3(64 * kDownWaves), s, a, o, p.Ip, p.slots, cols);
+  return launch_kernel(moe_down_kernel<HP>, dim3((unsigned)strips, (unsigned)slots), dim3(64 * kDownWaves), s, a, o, p.Ip, pairs, p.Dz);
 }
 
 template <int XP> static hipError_t moe_h(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
@@ -427,9 +466,13 @@ template <int XP> static hipError_t moe_h(const MoeArgs& a, const MoePlan& p, co
 
 hipError_t launch_mx4_moe(const MoeArgs& a, const MoePlan& p, hipStream_t s) {
   char* ws = static_cast<char*>(a.ws);
-  const MoeBufs o{reinterpret_cast<int*>(ws + p.list), reinterpret_cast<uint64_t*>(ws + p.who),
-                  reinterpret_cast<uint2*>(ws + p.place), reinterpret_cast<uint16_t*>(ws + p.x),
-                  reinterpret_cast<uint16_t*>(ws + p.h)};
+  MoeBufs o{};
+  o.ids = reinterpret_cast<int*>(ws + p.ids);
+  o.w = reinterpret_cast<float*>(ws + p.w);
+  o.done = reinterpret_cast<uint32_t*>(ws + p.done);
+  o.x = reinterpret_cast<uint16_t*>(ws + p.x);
+  o.h = reinterpret_cast<uint16_t*>(ws + p.h);
+  o.z = reinterpret_cast<float*>(ws + p.z);
   switch (p.xparts) {
     case 1: return moe_h<1>(a, p, o, s);
     case 2: return moe_h<2>(a, p, o, s);

@@ -121,7 +121,8 @@ QMM_API size_t qmm_mx4_moe_workspace_bytes(int T, int D, int I, int E, int top_k
  *   else ids (T, top_k) of ids_size bytes each (4 or 8) and weights (T, top_k) of
  *     weights_dtype, contiguous.  An index outside [0, E) counts for nothing;
  *     one that a token has twice counts with both weights.
- * A token without experts has y = 0.  T top_k I stays below 2^28 - 2^16.
+ * A token without experts has y = 0.  T top_k D and T top_k I stay below
+ * 2^28 - 2^16.
  */
 QMM_API qmm_status qmm_mx4_moe(const void* x, int x_dtype, int64_t ldx, const void* Wg,
                                const void* Wu, const void* Wd, void* y, int y_dtype, int64_t ldy,
