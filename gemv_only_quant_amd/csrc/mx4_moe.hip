@@ -54,9 +54,7 @@ __device__ __forceinline__ float value_of(uint32_t order) {
 }
 
 // Activations lie in rows of whole chunks, a chunk's 512 values in the order in which the matrix cores
-// take them: eight values i of blocks 4 q + j at 128 j + 32 i + 8 q, so that what a load takes of a row
-// are 64 consecutive bytes (in the order of K it would touch four lines of each row, and
-// the address units, one line at a time, would bound the kernel).
+// take them: eight values i of blocks 4 q + j at 128 j + 32 i + 8 q.
 __device__ __forceinline__ int operand_order(int k) {
   const int b = k / 32;
   return (k & ~511) + 128 * (b & 3) + 32 * ((k >> 3) & 3) + 8 * ((b >> 2) & 3) + (k & 7);
@@ -171,33 +169,10 @@ __device__ __forceinline__ void load_chunk(MoeChunk& w, const uint8_t* p, int nb
   w.s = __builtin_amdgcn_raw_buffer_load_b32(b, 4096 + 4 * lane, 0, kStream);
 }
 
-// Row r of the product is the r-th token of the expert; its rows of activations from `off` bytes on
-// (kNowhere: no such row), blocks 4 (lane / 16) + j of a chunk.
-template <int P> struct MoeRows {
-  u32x4_t a[P][4];
-  __device__ __forceinline__ void load(const buf_t (&b)[P], int off, int j, int nb, int lane) {
-    const int at = 4 * (lane >> 4) + j < nb ? off + 16 * (lane >> 4) + 256 * j : kNowhere;
-#pragma unroll
-    for (int q = 0; q < P; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a[q][i] = buf_load128(b[q], at + 64 * i);
-  }
-};
 // Buffers of the parts of `rows` rows of `ld` bf16 values.
 template <int P> __device__ __forceinline__ void part_buffers(buf_t (&b)[P], const uint16_t* p, int rows, int ld) {
 #pragma unroll
   for (int q = 0; q < P; ++q) b[q] = make_buf(p + (int64_t)q * rows * ld, 2u * (uint32_t)rows * (uint32_t)ld);
-}
-
-template <int P>
-__device__ __forceinline__ void multiply(f32x4_t& acc, const MoeRows<P>& r, const u32x4_t& c, float scale) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bf16x8_t b = __builtin_bit_cast(bf16x8_t, bf16_of_codes(c[i], scale));
-#pragma unroll
-    for (int q = 0; q < P; ++q)
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, r.a[q][i]), b, acc, 0, 0, 0);
-  }
 }
 
 // An expert's tokens, from the slot of a workgroup: expert `slot` itself, or (`pairs`) the expert of
@@ -234,44 +209,98 @@ __device__ __forceinline__ MoeGroup group_of(const MoeBufs& o, int slot, bool pa
   return m;
 }
 
-// acc[p] += rows times w[p] over what a wave has of K: with TWO weights the same chunk of both, else two chunks
-// of one, whose sums are added.  The loads of the next pair go out before the last two of four
-// steps, behind all loads that these wait for (loads return in order).
-template <int P, bool TWO, class Fetch>
-__device__ __forceinline__ void sweep(f32x4_t (&acc)[2], MoeChunk (&w)[2], const buf_t (&rows)[P], int off, int first,
-                                      int stride, int chunks, int blocks, int lane, Fetch&& fetch) {
-  constexpr int A = TWO ? 1 : 2;  // row chunks at once
-  for (int c = first; c < chunks; c += stride) {
-    MoeChunk wn[2];
-    MoeRows<P> a[2];
-    constexpr int STEPS = 4 * A;
-    auto take = [&](int s) {
-      const int cc = c + (TWO ? 0 : s / 4);
-      a[s & 1].load(rows, off + 1024 * cc, s % 4, blocks - 16 * cc, lane);
-    };
-    take(0);
-    take(1);
+// acc[g][p] += rows 16 g .. + 15 of the expert times weight p's 16 columns, over the chunks that a wave has of K.
+// The rows of a chunk come as whole lines, 1 KiB a load, and through the wave's own part of LDS to the
+// operands' places (straight from memory a load touches 16 lines for 256 bytes: 16 tokens, 8 experts of
+// 4096 x 14336, second half 103 us).  A step is one part of 16 rows; the next step's rows are on
+// their way while one is multiplied, and with a chunk's last step the next chunk's weights, behind all
+// loads that are waited for before them (loads return in order).
+constexpr int kRowBytes = 1024 + 16;  // of LDS: neighbouring rows start in different banks
+constexpr int kStageBytes16 = 16 * kRowBytes;
+constexpr int kMoeWaves = 4;
+
+template <int P, int G, class Fetch>
+__device__ __forceinline__ void sweep(f32x4_t (&acc)[G][2], MoeChunk (&w)[2], const buf_t (&parts)[P], int offs, int members,
+                                      int first, int chunks, int blocks, char* lds, int lane, Fetch&& fetch) {
+  const int l16 = lane & 15, quad = lane >> 4;
+  u32x4_t v[8];
+  // 8 rows from `r0` on of a part's chunk c to registers: lane r has the offset of row r.  16 bytes of lane L are 8
+  // values of block 4 (L % 4) + L / 16.
+  auto request = [&](int q, int r0, int c) {
+    const int at = 4 * (lane & 3) + (lane >> 4) < blocks - 16 * c ? 16 * lane + 1024 * c : kNowhere;
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      if (s == STEPS - 2) fetch(wn, c + stride);
+    for (int r = 0; r < 8; r += 4) {
+      if (r0 + r >= members) break;
 #pragma unroll
-      for (int p = 0; p < (TWO ? 2 : 1); ++p) {
-        const MoeChunk& m = w[TWO ? p : s / 4];
-        multiply<P>(acc[TWO ? p : s & 1], a[s & 1], m.c[s % 4], scale_f32((m.s >> (8 * (s % 4))) & 255));
+      for (int i = 0; i < 4; ++i) {
+        const int row = __builtin_amdgcn_readlane(offs, r0 + r + i);
+        v[r + i] = __builtin_amdgcn_raw_buffer_load_b128(parts[q], at, row, 0);
       }
-      if (s + 2 < STEPS) take(s + 2);
+    }
+  };
+  auto leave = [&](int half, int r0) {
+#pragma unroll
+    for (int r = 0; r < 8; r += 4) {
+      if (r0 + r >= members) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4_t*>(lds + (8 * half + r + i) * kRowBytes + 16 * lane) = v[r + i];
+    }
+  };
+  if (first < chunks) request(0, 0, first);
+  for (int c = first; c < chunks; c += kMoeWaves) {
+    MoeChunk wn[2];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (16 * g >= members) break;
+      const bool last_g = g + 1 == G || 16 * (g + 1) >= members;
+#pragma unroll
+      for (int q = 0; q < P; ++q) {
+        leave(0, 16 * g);
+        if (16 * g + 8 < members) {
+          request(q, 16 * g + 8, c);
+          leave(1, 16 * g + 8);
+        }
+        if (q + 1 < P) {
+          request(q + 1, 16 * g, c);
+        } else if (!last_g) {
+          request(0, 16 * (g + 1), c);
+        } else {
+          if (c + kMoeWaves < chunks) request(0, 0, c + kMoeWaves);
+          fetch(wn, c + kMoeWaves);
+        }
+        // (converted anew for every part: kept, the operands would fill the registers)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(w[0].c[j]), "+v"(w[1].c[j]));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float s0 = scale_f32((w[0].s >> (8 * j)) & 255), s1 = scale_f32((w[1].s >> (8 * j)) & 255);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const u32x4_t a = *reinterpret_cast<const u32x4_t*>(lds + l16 * kRowBytes + 256 * j + 64 * i + 16 * quad);
+            const bf16x8_t av = __builtin_bit_cast(bf16x8_t, a);
+            acc[g][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                av, __builtin_bit_cast(bf16x8_t, bf16_of_codes(w[0].c[j][i], s0)), acc[g][0], 0, 0, 0);
+            acc[g][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                av, __builtin_bit_cast(bf16x8_t, bf16_of_codes(w[1].c[j][i], s1)), acc[g][1], 0, 0, 0);
+          }
+        }
+      }
     }
     w[0] = wn[0], w[1] = wn[1];
   }
 }
 
+// Both halves' workgroups: the waves' shares of K, and in their place the waves' sums of a row tile.
+union MoeLds {
+  char rows[kMoeWaves][kStageBytes16];
+  float sums[kMoeWaves][2][16][17];
+};
+
 // ---- first half ----------------------------------------------------------------
 // A workgroup: 16 columns of h of one expert, the waves taking chunks of K in turn.
-constexpr int kUpWaves = 4;
-
-template <int XP, int HP>
-__global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(MoeArgs g, MoeBufs o, int Dp, int Ip, int pairs) {
-  __shared__ float sums[kUpWaves][2][16][17];
+template <int XP, int HP, int G>
+__global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs g, MoeBufs o, int Dp, int Ip, int pairs) {
+  __shared__ MoeLds lds;
   __shared__ int tok[kMoeTokens], place[kMoeTokens];
   __shared__ float wt[kMoeTokens];
   const int lane = threadIdx.x & 63;
@@ -298,23 +327,24 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(MoeArgs g, MoeBuf
   __syncthreads();
   buf_t xb[XP];
   part_buffers<XP>(xb, o.x, g.T, Dp);
-  for (int r0 = 0; r0 < members; r0 += 16) {
-    const int row = r0 + l16;
-    const int off = row < members ? 2 * tok[row] * Dp : kNowhere;
-    f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    if (r0 > 0) fetch(w, wave);
-    sweep<XP, true>(acc, w, xb, off, wave, kUpWaves, chunks, blocks, lane, fetch);
-    if (r0 > 0) __syncthreads();
+  f32x4_t acc[G][2];
+#pragma unroll
+  for (int i = 0; i < G; ++i) acc[i][0] = acc[i][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  sweep<XP, G>(acc, w, xb, lane < members ? 2 * tok[lane] * Dp : 0, members, wave, chunks, blocks, lds.rows[wave], lane, fetch);
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    if (16 * i >= members) break;
+    __syncthreads();
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) sums[wave][p][4 * quad + q][l16] = acc[p][q];
+      for (int q = 0; q < 4; ++q) lds.sums[wave][p][4 * quad + q][l16] = acc[i][p][q];
     __syncthreads();
-    const int rr = threadIdx.x / 16, col = threadIdx.x % 16, r = r0 + rr;
+    const int rr = threadIdx.x / 16, col = threadIdx.x % 16, r = 16 * i + rr;
     if (r < members) {
       float gv = 0.f, uv = 0.f;
 #pragma unroll
-      for (int q = 0; q < kUpWaves; ++q) gv += sums[q][0][rr][col], uv += sums[q][1][rr][col];
+      for (int q = 0; q < kMoeWaves; ++q) gv += lds.sums[q][0][rr][col], uv += lds.sums[q][1][rr][col];
       float h = 0.f;
       with_act(g.act, [&](auto a) {
         float d;
@@ -330,33 +360,32 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(MoeArgs g, MoeBuf
 }
 
 // ---- second half ---------------------------------------------------------------
-// A workgroup: 16 columns of one expert's rows of y, the waves taking pairs of chunks in turn.  The last
-// of a strip's workgroups to come adds each token's rows in the order of its choices.
-constexpr int kDownWaves = 4;
-
-template <int HP>
-__global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int Dz) {
-  __shared__ float sums[kDownWaves][16][17];
+// A workgroup: 32 columns of one expert's rows of y, the waves taking chunks in turn.  The last of
+// those columns' workgroups to come adds each token's rows in the order of its choices.
+template <int HP, int G>
+__global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int Dz) {
+  __shared__ MoeLds lds;
   __shared__ int tok[kMoeTokens], place[kMoeTokens];
   __shared__ uint32_t arrived;
   __shared__ bool valid[kMoeTokens * kMoeTopK];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
-  const int strip = (int)blockIdx.x, k = g.top_k;
+  const int k = g.top_k, n0 = 32 * (int)blockIdx.x;
   const MoeGroup m = group_of(o, (int)blockIdx.y, pairs != 0, g.T, k, lane);
   const buf_t zb = make_buf(o.z, 4u * (uint32_t)(g.T * k) * (uint32_t)Dz);
-  const int rr = threadIdx.x / 16, col = threadIdx.x % 16, n = 16 * strip + col;
   if (m.e >= 0) {
     const int chunks = mx4_chunks(g.I), blocks = mx4_blocks(g.I);
-    const uint8_t* wd = g.wd + (int64_t)m.e * mx4_weight_bytes(g.D, g.I) + (int64_t)strip * mx4_strip_bytes(g.I);
+    const int64_t strip_bytes = mx4_strip_bytes(g.I);
+    const uint8_t* wd = g.wd + (int64_t)m.e * mx4_weight_bytes(g.D, g.I) + 2 * (int)blockIdx.x * strip_bytes;
     auto fetch = [&](MoeChunk (&w)[2], int c) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        load_chunk(w[i], c + i < chunks ? wd + (int64_t)kChunkBytes * (c + i) : nullptr, blocks - 16 * (c + i), lane);
+        load_chunk(w[i], c < chunks && n0 + 16 * i < g.D ? wd + i * strip_bytes + (int64_t)kChunkBytes * c : nullptr,
+                   blocks - 16 * c, lane);
     };
     MoeChunk w[2];
-    fetch(w, 2 * wave);
+    fetch(w, wave);
     const int members = __popcll(m.who);
     if (wave == 0 && m.place >= 0) {
       const int r = __popcll(m.who & ((uint64_t(1) << lane) - 1));
@@ -365,24 +394,30 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeArgs g, Mo
     __syncthreads();
     buf_t hb[HP];
     part_buffers<HP>(hb, o.h, g.T * k, Ip);
-    for (int r0 = 0; r0 < members; r0 += 16) {
-      const int row = r0 + l16;
-      const int off = row < members ? 2 * (tok[row] * k + place[row]) * Ip : kNowhere;
-      f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      if (r0 > 0) fetch(w, 2 * wave);
-      sweep<HP, false>(acc, w, hb, off, 2 * wave, 2 * kDownWaves, chunks, blocks, lane, fetch);
-      if (r0 > 0) __syncthreads();
+    f32x4_t acc[G][2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) sums[wave][4 * quad + q][l16] = acc[0][q] + acc[1][q];
+    for (int i = 0; i < G; ++i) acc[i][0] = acc[i][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    sweep<HP, G>(acc, w, hb, lane < members ? 2 * (tok[lane] * k + place[lane]) * Ip : 0, members, wave, chunks, blocks,
+                 lds.rows[wave], lane, fetch);
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      if (16 * i >= members) break;
       __syncthreads();
-      const int r = r0 + rr;
-      if (r < members) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) lds.sums[wave][p][4 * quad + q][l16] = acc[i][p][q];
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int rr = threadIdx.x / 32 + 8 * s, r = 16 * i + rr, col = threadIdx.x % 32;
+        if (r >= members) continue;
         float v = 0.f;
 #pragma unroll
-        for (int q = 0; q < kDownWaves; ++q) v += sums[q][rr][col];
+        for (int q = 0; q < kMoeWaves; ++q) v += lds.sums[q][col / 16][rr][col % 16];
         // past this XCD's L2: another XCD's workgroup may read it
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), zb, 4 * ((tok[r] * k + place[r]) * Dz + n), 0,
-                                              kCoherent);
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), zb,
+                                              4 * ((tok[r] * k + place[r]) * Dz + n0 + col), 0, kCoherent);
       }
     }
   }
@@ -390,19 +425,19 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeArgs g, Mo
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
   __syncthreads();
   if (threadIdx.x == 0)
-    arrived = __hip_atomic_fetch_add(&o.done[strip], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    arrived = __hip_atomic_fetch_add(&o.done[blockIdx.x], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   if (arrived + 1 != gridDim.y) return;
   // which of a token's places have rows: those of an expert that no earlier place has
-  for (int i = threadIdx.x; i < g.T * k; i += 64 * kDownWaves) {
+  for (int i = threadIdx.x; i < g.T * k; i += 64 * kMoeWaves) {
     const int e = o.ids[i], t = i / k;
     bool first = e >= 0;
     for (int b = t * k; b < i; ++b) first = first && o.ids[b] != e;
     valid[i] = first;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * g.T; i += 64 * kDownWaves) {
-    const int t = i / 16;
+  for (int i = threadIdx.x; i < 32 * g.T; i += 64 * kMoeWaves) {
+    const int t = i / 32, n = n0 + i % 32;
     if (n >= g.D) continue;
     float v = 0.f;
     for (int j0 = 0; j0 < k; j0 += 8) {  // 8 loads at once
@@ -430,7 +465,7 @@ MoePlan plan_moe(int T, int D, int I, int top_k, int x_dtype, int y_dtype) {
   p.hparts = y_dtype == YF32 ? 3 : 2;
   p.Dp = (int)round_up(D, 512);
   p.Ip = (int)round_up(I, 512);
-  p.Dz = (int)round_up(D, 16);
+  p.Dz = (int)round_up(D, 32);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -439,7 +474,7 @@ MoePlan plan_moe(int T, int D, int I, int top_k, int x_dtype, int y_dtype) {
   };
   p.ids = take((size_t)T * top_k * 4);
   p.w = take((size_t)T * top_k * 4);
-  p.done = take((size_t)p.Dz / 16 * 4);
+  p.done = take((size_t)p.Dz / 32 * 4);
   p.x = take((size_t)p.xparts * T * p.Dp * 2);
   p.h = take((size_t)p.hparts * T * top_k * p.Ip * 2);
   p.z = take((size_t)T * top_k * p.Dz * 4);
@@ -447,19 +482,21 @@ MoePlan plan_moe(int T, int D, int I, int top_k, int x_dtype, int y_dtype) {
   return p;
 }
 
-template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
-  const int xg = (a.T * (p.Dp / 8) + 255) / 256, strips = p.Dz / 16;
+template <int XP, int HP, int G> static hipError_t moe_g(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
+  const int xg = (a.T * (p.Dp / 8) + 255) / 256, cols = p.Dz / 32;
   hipError_t e = launch_kernel(moe_route_kernel<XP>, dim3((unsigned)((a.T + 3) / 4 + (xg < 256 ? xg : 256))), dim3(256), s, a, o,
-                               strips, p.Dp);
+                               cols, p.Dp);
   if (e != hipSuccess) return e;
   // a workgroup for each expert, or for each place of the tokens' choices if these are fewer
   const int pairs = a.T * a.top_k < a.E, slots = pairs ? a.T * a.top_k : a.E;
-  e = launch_kernel(moe_up_kernel<XP, HP>, dim3((unsigned)(round_up(a.I, kBlock) / 16), (unsigned)slots), dim3(64 * kUpWaves), s,
-                    a, o, p.Dp, p.Ip, pairs);
+  e = launch_kernel(moe_up_kernel<XP, HP, G>, dim3((unsigned)(round_up(a.I, kBlock) / 16), (unsigned)slots),
+                    dim3(64 * kMoeWaves), s, a, o, p.Dp, p.Ip, pairs);
   if (e != hipSuccess) return e;
-  return launch_kernel(moe_down_kernel<HP>, dim3((unsigned)strips, (unsigned)slots), dim3(64 * kDownWaves), s, a, o, p.Ip, pairs, p.Dz);
+  return launch_kernel(moe_down_kernel<HP, G>, dim3((unsigned)cols, (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs, p.Dz);
 }
-
+template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
+  return a.T <= 16 ? moe_g<XP, HP, 1>(a, p, o, s) : moe_g<XP, HP, 4>(a, p, o, s);
+}
 template <int XP> static hipError_t moe_h(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
   return p.hparts == 3 ? moe_t<XP, 3>(a, p, o, s) : moe_t<XP, 2>(a, p, o, s);
 }
