@@ -184,23 +184,35 @@ struct MoeGroup {
   float w;        // and the sum of all such places' weights
 };
 __device__ __forceinline__ MoeGroup group_of(const MoeBufs& o, int slot, bool pairs, int T, int k, int lane) {
+  // (what does not depend on the expert is requested first, so that the loads' latencies overlap)
+  constexpr int HELD = 8;
+  const int* ids = o.ids + (lane < T ? lane * k : 0);
+  const float* w = o.w + (lane < T ? lane * k : 0);
+  int own[HELD];
+  float ow[HELD];
+#pragma unroll
+  for (int j = 0; j < HELD; ++j) own[j] = ids[j < k ? j : 0], ow[j] = w[j < k ? j : 0];
   MoeGroup m;
   m.e = slot;
   if (pairs) {
+    int earlier = lane < slot ? o.ids[lane] : -1;
     m.e = __builtin_amdgcn_readfirstlane(o.ids[slot]);
-    bool before = m.e < 0;
-    for (int p = lane; p < slot; p += 64) before |= o.ids[p] == m.e;
+    bool before = m.e < 0 || earlier == m.e;
+    for (int p = 64 + lane; p < slot; p += 64) before |= o.ids[p] == m.e;
     if (__ballot(before) != 0) m.e = -1;
   }
   m.place = -1;
   m.w = 0.f;
   if (lane < T && m.e >= 0) {
-    const int* ids = o.ids + lane * k;
-    const float* w = o.w + lane * k;
-#pragma unroll 4
-    for (int j = k - 1; j >= 0; --j) {
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+      const bool same = j < k && own[j] == m.e;
+      m.place = same && m.place < 0 ? j : m.place;
+      m.w += same ? ow[j] : 0.f;
+    }
+    for (int j = HELD; j < k; ++j) {
       const bool same = ids[j] == m.e;
-      m.place = same ? j : m.place;
+      m.place = same && m.place < 0 ? j : m.place;
       m.w += same ? w[j] : 0.f;
     }
   }
@@ -209,66 +221,74 @@ __device__ __forceinline__ MoeGroup group_of(const MoeBufs& o, int slot, bool pa
   return m;
 }
 
-// acc[g][p] += rows 16 g .. + 15 of the expert times weight p's 16 columns, over the chunks that a wave has of K.
+// A workgroup's products: tiles (pairs of 16 columns of an expert) one after the other, in each of which a wave
+// takes chunks of K in turn; put(tile, sums) is called by all waves when a tile's sums of a wave are
+// complete: acc[g][p] of rows RG g .. of `members` and of column half p.
 // The rows of a chunk come as whole lines, 1 KiB a load, and through the wave's own part of LDS to the
 // operands' places (straight from memory a load touches 16 lines for 256 bytes: 16 tokens, 8 experts of
-// 4096 x 14336, second half 103 us).  A step is one part of 16 rows; the next step's rows are on
-// their way while one is multiplied, and with a chunk's last step the next chunk's weights, behind all
-// loads that are waited for before them (loads return in order).
+// 4096 x 14336, second half 103 us).  LDS holds RG rows in all their parts; the next ones are on
+// their way while these are multiplied, and behind them the next chunk's weights (the next tile's
+// after a tile's last): loads return in order, and what is waited for first goes first.
 constexpr int kRowBytes = 1024 + 16;  // of LDS: neighbouring rows start in different banks
-constexpr int kStageBytes16 = 16 * kRowBytes;
 constexpr int kMoeWaves = 4;
+template <int P> constexpr int kRowGroup = 16 / P;  // rows of which a wave holds all P parts
 
-template <int P, int G, class Fetch>
-__device__ __forceinline__ void sweep(f32x4_t (&acc)[G][2], MoeChunk (&w)[2], const buf_t (&parts)[P], int offs, int members,
-                                      int first, int chunks, int blocks, char* lds, int lane, Fetch&& fetch) {
+struct MoeLds {
+  char rows[kMoeWaves][16 * kRowBytes];
+  float sums[kMoeWaves][2][16][17];
+};
+
+template <int P, int G, class Fetch, class Put>
+__device__ __forceinline__ void sweep(const buf_t (&parts)[P], int offs, int members, int wave, int tile, int tiles, int chunks,
+                                      int blocks, char* lds, int lane, Fetch&& fetch, Put&& put) {
+  constexpr int RG = kRowGroup<P>;
   const int l16 = lane & 15, quad = lane >> 4;
-  u32x4_t v[8];
-  // 8 rows from `r0` on of a part's chunk c to registers: lane r has the offset of row r.  16 bytes of lane L are 8
-  // values of block 4 (L % 4) + L / 16.
-  auto request = [&](int q, int r0, int c) {
+  u32x4_t v[P][RG];
+  // row group g of chunk c to registers: lane r has the offset of row r.  16 bytes of lane L are 8 values of
+  // block 4 (L % 4) + L / 16.
+  auto request = [&](int g, int c) {
     const int at = 4 * (lane & 3) + (lane >> 4) < blocks - 16 * c ? 16 * lane + 1024 * c : kNowhere;
 #pragma unroll
-    for (int r = 0; r < 8; r += 4) {
-      if (r0 + r >= members) break;
+    for (int r = 0; r < RG; ++r) {
+      if (r % 4 == 0 && RG * g + r >= members) break;
+      const int row = __builtin_amdgcn_readlane(offs, RG * g + r);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = __builtin_amdgcn_readlane(offs, r0 + r + i);
-        v[r + i] = __builtin_amdgcn_raw_buffer_load_b128(parts[q], at, row, 0);
-      }
+      for (int q = 0; q < P; ++q) v[q][r] = __builtin_amdgcn_raw_buffer_load_b128(parts[q], at, row, 0);
     }
   };
-  auto leave = [&](int half, int r0) {
+  auto leave = [&](int g) {
 #pragma unroll
-    for (int r = 0; r < 8; r += 4) {
-      if (r0 + r >= members) break;
+    for (int r = 0; r < RG; ++r) {
+      if (r % 4 == 0 && RG * g + r >= members) break;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4_t*>(lds + (8 * half + r + i) * kRowBytes + 16 * lane) = v[r + i];
+      for (int q = 0; q < P; ++q) *reinterpret_cast<u32x4_t*>(lds + (RG * q + r) * kRowBytes + 16 * lane) = v[q][r];
     }
   };
-  if (first < chunks) request(0, 0, first);
-  for (int c = first; c < chunks; c += kMoeWaves) {
-    MoeChunk wn[2];
+  MoeChunk w[2], wn[2];
+  fetch(w, tile, wave);
+  // rows that fit LDS at once and serve every tile stay there
+  const bool stay = members <= RG && chunks <= kMoeWaves;
+  if (wave < chunks) request(0, wave);
+  bool staged = false;
+  for (; tile < tiles; ++tile) {
+    f32x4_t acc[G][2];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      if (16 * g >= members) break;
-      const bool last_g = g + 1 == G || 16 * (g + 1) >= members;
+    for (int g = 0; g < G; ++g) acc[g][0] = acc[g][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int c = wave; c < chunks; c += kMoeWaves) {
+      const bool more = c + kMoeWaves < chunks;
 #pragma unroll
-      for (int q = 0; q < P; ++q) {
-        leave(0, 16 * g);
-        if (16 * g + 8 < members) {
-          request(q, 16 * g + 8, c);
-          leave(1, 16 * g + 8);
+      for (int g = 0; g < G; ++g) {
+        if (RG * g >= members) break;
+        const bool last = g + 1 == G || RG * (g + 1) >= members;
+        if (!staged) {
+          leave(g);
+          staged = stay;
+          if (!last) request(g + 1, c);
+          else if (!stay && (more || tile + 1 < tiles)) request(0, more ? c + kMoeWaves : wave);
         }
-        if (q + 1 < P) {
-          request(q + 1, 16 * g, c);
-        } else if (!last_g) {
-          request(0, 16 * (g + 1), c);
-        } else {
-          if (c + kMoeWaves < chunks) request(0, 0, c + kMoeWaves);
-          fetch(wn, c + kMoeWaves);
-        }
-        // (converted anew for every part: kept, the operands would fill the registers)
+        if (last) fetch(wn, more ? tile : tile + 1, more ? c + kMoeWaves : wave);
+        const char* from = lds + min(l16, RG - 1) * kRowBytes + 16 * quad;
+        // (weights are converted anew for every group: kept, the operands would fill the registers)
 #pragma unroll
         for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(w[0].c[j]), "+v"(w[1].c[j]));
 #pragma unroll
@@ -276,49 +296,57 @@ __device__ __forceinline__ void sweep(f32x4_t (&acc)[G][2], MoeChunk (&w)[2], co
           const float s0 = scale_f32((w[0].s >> (8 * j)) & 255), s1 = scale_f32((w[1].s >> (8 * j)) & 255);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const u32x4_t a = *reinterpret_cast<const u32x4_t*>(lds + l16 * kRowBytes + 256 * j + 64 * i + 16 * quad);
-            const bf16x8_t av = __builtin_bit_cast(bf16x8_t, a);
-            acc[g][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                av, __builtin_bit_cast(bf16x8_t, bf16_of_codes(w[0].c[j][i], s0)), acc[g][0], 0, 0, 0);
-            acc[g][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                av, __builtin_bit_cast(bf16x8_t, bf16_of_codes(w[1].c[j][i], s1)), acc[g][1], 0, 0, 0);
+            const bf16x8_t b0 = __builtin_bit_cast(bf16x8_t, bf16_of_codes(w[0].c[j][i], s0));
+            const bf16x8_t b1 = __builtin_bit_cast(bf16x8_t, bf16_of_codes(w[1].c[j][i], s1));
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+              const u32x4_t a = *reinterpret_cast<const u32x4_t*>(from + RG * q * kRowBytes + 256 * j + 64 * i);
+              const bf16x8_t av = __builtin_bit_cast(bf16x8_t, a);
+              acc[g][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, b0, acc[g][0], 0, 0, 0);
+              acc[g][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, b1, acc[g][1], 0, 0, 0);
+            }
           }
         }
       }
+      w[0] = wn[0], w[1] = wn[1];
     }
-    w[0] = wn[0], w[1] = wn[1];
+    put(tile, acc);
   }
 }
 
-// Both halves' workgroups: the waves' shares of K, and in their place the waves' sums of a row tile.
-union MoeLds {
-  char rows[kMoeWaves][kStageBytes16];
-  float sums[kMoeWaves][2][16][17];
-};
+// The waves' sums of row group i to LDS, where all may read them afterwards.  The first barrier keeps the
+// readers of what was there apart.
+template <int G>
+__device__ __forceinline__ void meet(MoeLds& lds, const f32x4_t (&acc)[G][2], int i, int wave, int lane) {
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) lds.sums[wave][p][4 * (lane >> 4) + q][lane & 15] = acc[i][p][q];
+  __syncthreads();
+}
 
 // ---- first half ----------------------------------------------------------------
-// A workgroup: 16 columns of h of one expert, the waves taking chunks of K in turn.
+// A workgroup: `per` strips of 16 columns of h of one expert.
 template <int XP, int HP, int G>
-__global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs g, MoeBufs o, int Dp, int Ip, int pairs) {
+__global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs g, MoeBufs o, int Dp, int Ip, int pairs, int per) {
   __shared__ MoeLds lds;
   __shared__ int tok[kMoeTokens], place[kMoeTokens];
   __shared__ float wt[kMoeTokens];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l16 = lane & 15, quad = lane >> 4;
-  const int strip = (int)blockIdx.x;
   const MoeGroup m = group_of(o, (int)blockIdx.y, pairs != 0, g.T, g.top_k, lane);
   if (m.e < 0) return;
   const int chunks = mx4_chunks(g.D), blocks = mx4_blocks(g.D);
-  const int64_t at = (int64_t)m.e * mx4_weight_bytes(g.I, g.D) + (int64_t)strip * mx4_strip_bytes(g.D);
-  const bool real = 16 * strip < g.I;  // h's columns are padded to whole blocks, with zeros
-  auto fetch = [&](MoeChunk (&w)[2], int c) {
-    const bool ok = real && c < chunks;
-    load_chunk(w[0], ok ? g.wg + at + (int64_t)kChunkBytes * c : nullptr, blocks - 16 * c, lane);
-    load_chunk(w[1], ok ? g.wu + at + (int64_t)kChunkBytes * c : nullptr, blocks - 16 * c, lane);
+  const int strips = 2 * mx4_blocks(g.I);  // h's columns are padded to whole blocks, with zeros
+  const int tile = per * (int)blockIdx.x, tiles = min(tile + per, strips);
+  const int64_t strip_bytes = mx4_strip_bytes(g.D), at = (int64_t)m.e * mx4_weight_bytes(g.I, g.D);
+  auto fetch = [&](MoeChunk (&w)[2], int t, int c) {
+    const bool ok = t < tiles && 16 * t < g.I && c < chunks;
+    const int64_t to = at + t * strip_bytes + (int64_t)kChunkBytes * c;
+    load_chunk(w[0], ok ? g.wg + to : nullptr, blocks - 16 * c, lane);
+    load_chunk(w[1], ok ? g.wu + to : nullptr, blocks - 16 * c, lane);
   };
-  MoeChunk w[2];
-  fetch(w, wave);
   const int members = __popcll(m.who);
   if (wave == 0 && m.place >= 0) {
     const int r = __popcll(m.who & ((uint64_t(1) << lane) - 1));
@@ -327,21 +355,17 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs g, Mo
   __syncthreads();
   buf_t xb[XP];
   part_buffers<XP>(xb, o.x, g.T, Dp);
-  f32x4_t acc[G][2];
+  const int rr = threadIdx.x / 16, col = threadIdx.x % 16;
+  constexpr int RG = kRowGroup<XP>;
+  for (int r0 = 0; r0 < members; r0 += G * RG)
+  sweep<XP, G>(xb, r0 + lane < members ? 2 * tok[r0 + lane] * Dp : 0, members - r0, wave, tile, tiles, chunks, blocks,
+               lds.rows[wave], lane, fetch, [&](int t, const f32x4_t (&acc)[G][2]) {
 #pragma unroll
-  for (int i = 0; i < G; ++i) acc[i][0] = acc[i][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  sweep<XP, G>(acc, w, xb, lane < members ? 2 * tok[lane] * Dp : 0, members, wave, chunks, blocks, lds.rows[wave], lane, fetch);
-#pragma unroll
-  for (int i = 0; i < G; ++i) {
-    if (16 * i >= members) break;
-    __syncthreads();
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) lds.sums[wave][p][4 * quad + q][l16] = acc[i][p][q];
-    __syncthreads();
-    const int rr = threadIdx.x / 16, col = threadIdx.x % 16, r = 16 * i + rr;
-    if (r < members) {
+    for (int i = 0; i < G; ++i) {
+      if (r0 + RG * i >= members) break;
+      meet<G>(lds, acc, i, wave, lane);
+      const int r = r0 + RG * i + rr;
+      if (rr >= RG || r >= members) continue;
       float gv = 0.f, uv = 0.f;
 #pragma unroll
       for (int q = 0; q < kMoeWaves; ++q) gv += lds.sums[q][0][rr][col], uv += lds.sums[q][1][rr][col];
@@ -351,41 +375,39 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs g, Mo
         h = act_parts<decltype(a)::value>(gv, &d) * uv * wt[r];
       });
       uint16_t p[HP];
-      parts_of<HP>(16 * strip + col < g.I ? h : 0.f, p);  // the padding is 0 whatever x is
+      parts_of<HP>(16 * t + col < g.I ? h : 0.f, p);  // the padding is 0 whatever x is
 #pragma unroll
       for (int q = 0; q < HP; ++q)
-        o.h[((int64_t)q * g.T * g.top_k + tok[r] * g.top_k + place[r]) * Ip + operand_order(16 * strip + col)] = p[q];
+        o.h[((int64_t)q * g.T * g.top_k + tok[r] * g.top_k + place[r]) * Ip + operand_order(16 * t + col)] = p[q];
     }
-  }
+  });
 }
 
 // ---- second half ---------------------------------------------------------------
-// A workgroup: 32 columns of one expert's rows of y, the waves taking chunks in turn.  The last of
-// those columns' workgroups to come adds each token's rows in the order of its choices.
+// A workgroup: `per` times 32 columns of one expert's rows of y.  The last of those columns' workgroups
+// to come adds each token's rows in the order of its choices.
 template <int HP, int G>
-__global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int Dz) {
+__global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int Dz, int per) {
   __shared__ MoeLds lds;
   __shared__ int tok[kMoeTokens], place[kMoeTokens];
   __shared__ uint32_t arrived;
   __shared__ bool valid[kMoeTokens * kMoeTopK];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l16 = lane & 15, quad = lane >> 4;
-  const int k = g.top_k, n0 = 32 * (int)blockIdx.x;
+  const int k = g.top_k;
+  const int tile = per * (int)blockIdx.x, tiles = min(tile + per, Dz / 32);
   const MoeGroup m = group_of(o, (int)blockIdx.y, pairs != 0, g.T, k, lane);
   const buf_t zb = make_buf(o.z, 4u * (uint32_t)(g.T * k) * (uint32_t)Dz);
   if (m.e >= 0) {
     const int chunks = mx4_chunks(g.I), blocks = mx4_blocks(g.I);
-    const int64_t strip_bytes = mx4_strip_bytes(g.I);
-    const uint8_t* wd = g.wd + (int64_t)m.e * mx4_weight_bytes(g.D, g.I) + 2 * (int)blockIdx.x * strip_bytes;
-    auto fetch = [&](MoeChunk (&w)[2], int c) {
+    const int64_t strip_bytes = mx4_strip_bytes(g.I), at = (int64_t)m.e * mx4_weight_bytes(g.D, g.I);
+    auto fetch = [&](MoeChunk (&w)[2], int t, int c) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        load_chunk(w[i], c < chunks && n0 + 16 * i < g.D ? wd + i * strip_bytes + (int64_t)kChunkBytes * c : nullptr,
+        load_chunk(w[i], t < tiles && 32 * t + 16 * i < g.D && c < chunks
+                             ? g.wd + at + (2 * t + i) * strip_bytes + (int64_t)kChunkBytes * c : nullptr,
                    blocks - 16 * c, lane);
     };
-    MoeChunk w[2];
-    fetch(w, wave);
     const int members = __popcll(m.who);
     if (wave == 0 && m.place >= 0) {
       const int r = __popcll(m.who & ((uint64_t(1) << lane) - 1));
@@ -394,32 +416,27 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
     __syncthreads();
     buf_t hb[HP];
     part_buffers<HP>(hb, o.h, g.T * k, Ip);
-    f32x4_t acc[G][2];
+    constexpr int RG = kRowGroup<HP>;
+    for (int r0 = 0; r0 < members; r0 += G * RG)
+    sweep<HP, G>(hb, r0 + lane < members ? 2 * (tok[r0 + lane] * k + place[r0 + lane]) * Ip : 0, members - r0, wave, tile, tiles,
+                 chunks, blocks, lds.rows[wave], lane, fetch, [&](int t, const f32x4_t (&acc)[G][2]) {
 #pragma unroll
-    for (int i = 0; i < G; ++i) acc[i][0] = acc[i][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    sweep<HP, G>(acc, w, hb, lane < members ? 2 * (tok[lane] * k + place[lane]) * Ip : 0, members, wave, chunks, blocks,
-                 lds.rows[wave], lane, fetch);
+      for (int i = 0; i < G; ++i) {
+        if (r0 + RG * i >= members) break;
+        meet<G>(lds, acc, i, wave, lane);
+        // (8 rows at once: RG is at most that)
+        {
+          const int rr = threadIdx.x / 32, r = r0 + RG * i + rr, col = threadIdx.x % 32;
+          if (rr >= RG || r >= members) continue;
+          float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      if (16 * i >= members) break;
-      __syncthreads();
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) lds.sums[wave][p][4 * quad + q][l16] = acc[i][p][q];
-      __syncthreads();
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int rr = threadIdx.x / 32 + 8 * s, r = 16 * i + rr, col = threadIdx.x % 32;
-        if (r >= members) continue;
-        float v = 0.f;
-#pragma unroll
-        for (int q = 0; q < kMoeWaves; ++q) v += lds.sums[q][col / 16][rr][col % 16];
-        // past this XCD's L2: another XCD's workgroup may read it
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), zb,
-                                              4 * ((tok[r] * k + place[r]) * Dz + n0 + col), 0, kCoherent);
+          for (int q = 0; q < kMoeWaves; ++q) v += lds.sums[q][col / 16][rr][col % 16];
+          // past this XCD's L2: another XCD's workgroup may read it
+          __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), zb,
+                                                4 * ((tok[r] * k + place[r]) * Dz + 32 * t + col), 0, kCoherent);
+        }
       }
-    }
+    });
   }
   // every wave's rows are in memory before the workgroup counts as arrived
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
@@ -436,9 +453,9 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
     valid[i] = first;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 32 * g.T; i += 64 * kMoeWaves) {
-    const int t = i / 32, n = n0 + i % 32;
-    if (n >= g.D) continue;
+  const int n0 = 32 * tile, cols = min(32 * tiles, g.D) - n0;
+  for (int i = threadIdx.x; i < cols * g.T; i += 64 * kMoeWaves) {
+    const int t = i / cols, n = n0 + i % cols;
     float v = 0.f;
     for (int j0 = 0; j0 < k; j0 += 8) {  // 8 loads at once
       float r[8];
@@ -482,20 +499,21 @@ MoePlan plan_moe(int T, int D, int I, int top_k, int x_dtype, int y_dtype) {
   return p;
 }
 
-template <int XP, int HP, int G> static hipError_t moe_g(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
-  const int xg = (a.T * (p.Dp / 8) + 255) / 256, cols = p.Dz / 32;
-  hipError_t e = launch_kernel(moe_route_kernel<XP>, dim3((unsigned)((a.T + 3) / 4 + (xg < 256 ? xg : 256))), dim3(256), s, a, o,
-                               cols, p.Dp);
-  if (e != hipSuccess) return e;
-  // a workgroup for each expert, or for each place of the tokens' choices if these are fewer
-  const int pairs = a.T * a.top_k < a.E, slots = pairs ? a.T * a.top_k : a.E;
-  e = launch_kernel(moe_up_kernel<XP, HP, G>, dim3((unsigned)(round_up(a.I, kBlock) / 16), (unsigned)slots),
-                    dim3(64 * kMoeWaves), s, a, o, p.Dp, p.Ip, pairs);
-  if (e != hipSuccess) return e;
-  return launch_kernel(moe_down_kernel<HP, G>, dim3((unsigned)cols, (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs, p.Dz);
-}
 template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
-  return a.T <= 16 ? moe_g<XP, HP, 1>(a, p, o, s) : moe_g<XP, HP, 4>(a, p, o, s);
+  // a workgroup for each expert, or for each place of the tokens' choices if these are fewer; of more tiles than
+  // about 3 rounds of workgroups (2 on a CU) would be, a workgroup takes several in turn
+  const int pairs = a.T * a.top_k < a.E, slots = pairs ? a.T * a.top_k : a.E;
+  auto each = [&](int tiles) { return (int)(((int64_t)tiles * slots + 1535) / 1536); };
+  const int up = 2 * mx4_blocks(a.I), down = p.Dz / 32, per_up = each(up), per_down = each(down);
+  const int xg = (a.T * (p.Dp / 8) + 255) / 256, gd = (down + per_down - 1) / per_down;
+  hipError_t e = launch_kernel(moe_route_kernel<XP>, dim3((unsigned)((a.T + 3) / 4 + (xg < 256 ? xg : 256))), dim3(256), s, a, o,
+                               gd, p.Dp);
+  if (e != hipSuccess) return e;
+  e = launch_kernel(a.T <= kRowGroup<XP> ? moe_up_kernel<XP, HP, 1> : moe_up_kernel<XP, HP, 2>, dim3((unsigned)((up + per_up - 1) / per_up), (unsigned)slots), dim3(64 * kMoeWaves), s,
+                    a, o, p.Dp, p.Ip, pairs, per_up);
+  if (e != hipSuccess) return e;
+  return launch_kernel(a.T <= kRowGroup<HP> ? moe_down_kernel<HP, 1> : moe_down_kernel<HP, 2>, dim3((unsigned)gd, (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs,
+                       p.Dz, per_down);
 }
 template <int XP> static hipError_t moe_h(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
   return p.hparts == 3 ? moe_t<XP, 3>(a, p, o, s) : moe_t<XP, 2>(a, p, o, s);
