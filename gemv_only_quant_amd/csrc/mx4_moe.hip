@@ -384,9 +384,37 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs g, Mo
 }
 
 // ---- second half ---------------------------------------------------------------
-// A workgroup: `per` times 32 columns of one expert's rows of y.  The last of those columns' workgroups
-// to come adds each token's rows in the order of its choices.
-template <int HP, int G>
+// A workgroup: `per` times 32 columns of one expert's rows of y.  A token's rows are added in the order of its
+// choices: for a few tokens (JOIN) by the last of those columns' workgroups to come, else by another launch (64
+// tokens, 64 experts of 2048 x 1408: few workgroups would be left with 23 us of additions).
+// Whether place p of all tokens' choices has rows: that of an expert which no earlier place of its token has.
+__device__ __forceinline__ bool first_place(const int* ids, int p, int k) {
+  const int e = ids[p];
+  bool first = e >= 0;
+  for (int b = p - p % k; b < p; ++b) first = first && ids[b] != e;
+  return first;
+}
+
+// Column n of a token's rows, those of places p0 .. + k - 1 that exist, added in this order.
+template <bool COHERENT, class Valid>
+__device__ __forceinline__ float token_sum(buf_t z, int p0, int k, int Dz, int n, Valid&& valid) {
+  float v = 0.f;
+  for (int j0 = 0; j0 < k; j0 += 8) {  // 8 loads at once
+    float r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int p = p0 + j0 + j;
+      const bool ok = j0 + j < k && valid(p);
+      r[j] = __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(z, ok ? 4 * (p * Dz + n) : kNowhere, 0,
+                                                                                      COHERENT ? kCoherent : 0));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v += r[j];
+  }
+  return v;
+}
+
+template <int HP, int G, bool JOIN>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int Dz, int per) {
   __shared__ MoeLds lds;
   __shared__ int tok[kMoeTokens], place[kMoeTokens];
@@ -438,6 +466,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
       }
     });
   }
+  if (!JOIN) return;
   // every wave's rows are in memory before the workgroup counts as arrived
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
   __syncthreads();
@@ -445,34 +474,29 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
     arrived = __hip_atomic_fetch_add(&o.done[blockIdx.x], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   if (arrived + 1 != gridDim.y) return;
-  // which of a token's places have rows: those of an expert that no earlier place has
-  for (int i = threadIdx.x; i < g.T * k; i += 64 * kMoeWaves) {
-    const int e = o.ids[i], t = i / k;
-    bool first = e >= 0;
-    for (int b = t * k; b < i; ++b) first = first && o.ids[b] != e;
-    valid[i] = first;
-  }
+  for (int i = threadIdx.x; i < g.T * k; i += 64 * kMoeWaves) valid[i] = first_place(o.ids, i, k);
   __syncthreads();
   const int n0 = 32 * tile, cols = min(32 * tiles, g.D) - n0;
   for (int i = threadIdx.x; i < cols * g.T; i += 64 * kMoeWaves) {
     const int t = i / cols, n = n0 + i % cols;
-    float v = 0.f;
-    for (int j0 = 0; j0 < k; j0 += 8) {  // 8 loads at once
-      float r[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int at = t * k + j0 + j;
-        const bool ok = j0 + j < k && valid[at];
-        r[j] = __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(zb, ok ? 4 * (at * Dz + n) : kNowhere, 0, kCoherent));
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v += r[j];
-    }
+    const float v = token_sum<true>(zb, t * k, k, Dz, n, [&](int p) { return valid[p]; });
     with_y(g.y, g.y_dtype, [&](auto* yt) {
       typedef typename std::remove_pointer<decltype(yt)>::type Y;
       yt[(int64_t)t * g.ldy + n] = (Y)v;
     });
   }
+}
+
+// The same sums by a launch of its own, a workgroup for 256 columns of a token.
+__global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs g, MoeBufs o, int Dz, int blocks) {
+  const int t = (int)blockIdx.x / blocks, n = ((int)blockIdx.x % blocks) * 256 + (int)threadIdx.x, k = g.top_k;
+  if (n >= g.D) return;
+  const buf_t zb = make_buf(o.z, 4u * (uint32_t)(g.T * k) * (uint32_t)Dz);
+  const float v = token_sum<false>(zb, t * k, k, Dz, n, [&](int p) { return first_place(o.ids, p, k); });
+  with_y(g.y, g.y_dtype, [&](auto* yt) {
+    typedef typename std::remove_pointer<decltype(yt)>::type Y;
+    yt[(int64_t)t * g.ldy + n] = (Y)v;
+  });
 }
 
 // ---------------------------------------------------------------- host side
@@ -506,15 +530,22 @@ template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePla
   auto each = [&](int tiles) { return (int)(((int64_t)tiles * slots + 1535) / 1536); };
   const int up = 2 * mx4_blocks(a.I), down = p.Dz / 32, per_up = each(up), per_down = each(down);
   const int xg = (a.T * (p.Dp / 8) + 255) / 256, gd = (down + per_down - 1) / per_down;
+  const bool join = a.T <= 16;
   hipError_t e = launch_kernel(moe_route_kernel<XP>, dim3((unsigned)((a.T + 3) / 4 + (xg < 256 ? xg : 256))), dim3(256), s, a, o,
                                gd, p.Dp);
   if (e != hipSuccess) return e;
-  e = launch_kernel(a.T <= kRowGroup<XP> ? moe_up_kernel<XP, HP, 1> : moe_up_kernel<XP, HP, 2>, dim3((unsigned)((up + per_up - 1) / per_up), (unsigned)slots), dim3(64 * kMoeWaves), s,
-                    a, o, p.Dp, p.Ip, pairs, per_up);
+  e = launch_kernel(a.T <= kRowGroup<XP> ? moe_up_kernel<XP, HP, 1> : moe_up_kernel<XP, HP, 2>,
+                    dim3((unsigned)((up + per_up - 1) / per_up), (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Dp, p.Ip, pairs,
+                    per_up);
   if (e != hipSuccess) return e;
-  return launch_kernel(a.T <= kRowGroup<HP> ? moe_down_kernel<HP, 1> : moe_down_kernel<HP, 2>, dim3((unsigned)gd, (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs,
-                       p.Dz, per_down);
+  e = launch_kernel(!join ? moe_down_kernel<HP, 2, false>
+                          : a.T <= kRowGroup<HP> ? moe_down_kernel<HP, 1, true> : moe_down_kernel<HP, 2, true>,
+                    dim3((unsigned)gd, (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs, p.Dz, per_down);
+  if (e != hipSuccess || join) return e;
+  const int blocks = (a.D + 255) / 256;
+  return launch_kernel(moe_join_kernel, dim3((unsigned)(a.T * blocks)), dim3(256), s, a, o, p.Dz, blocks);
 }
+
 template <int XP> static hipError_t moe_h(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
   return p.hparts == 3 ? moe_t<XP, 3>(a, p, o, s) : moe_t<XP, 2>(a, p, o, s);
 }
