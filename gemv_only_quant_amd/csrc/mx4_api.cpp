@@ -149,11 +149,10 @@ qmm_status qmm_mx4_pack(const uint8_t* codes, int64_t ldc, const uint8_t* scales
 }
 
 size_t qmm_mx4_workspace_bytes(int M, int K, int x_dtype) {
-  if (M <= 0 || M > kMaxRows || K <= 0 || K >= kMaxK || !(x_dtype == QMM_MX4 || value_type(x_dtype))) return 0;
-  if (!qmm::mx4_skinny_fits(M)) return (size_t)qmm::mx4_weight_bytes(M, K);
-  if (x_dtype == QMM_MX4) return 0;
-  const size_t B = (size_t)qmm::mx4_blocks(K);
-  return (size_t)M * (16 * B + (size_t)qmm::round_up((int64_t)B, 4));
+  if (M <= 0 || M > kMaxRows || K <= 0 || K >= kMaxK) return 0;
+  if (x_dtype != QMM_MX4 && !value_type(x_dtype)) return 0;
+  if (x_dtype != QMM_MX4 && qmm::mx4_rows_fits(M, K)) return 0;  // quantized in LDS
+  return (size_t)qmm::mx4_weight_bytes(M, K);
 }
 
 qmm_status qmm_mx4_gemm(const void* x, int x_dtype, int64_t ldx, const uint8_t* sx, int64_t ldsx,
@@ -174,8 +173,8 @@ qmm_status qmm_mx4_gemm(const void* x, int x_dtype, int64_t ldx, const uint8_t* 
   if (K == 0) return device_status(fn, qmm::launch_fill_zero(y, type_size(y_dtype), ldy, M, N, s));
   const int B = qmm::mx4_blocks(K);
   if (coded) {
-    QMM_CHECK(check_matrix(fn, "x", x, ldx, 16 * (int64_t)B, 16, 16));
-    QMM_CHECK(check_matrix(fn, "sx", sx, ldsx, B, 4, 4));
+    QMM_CHECK(check_matrix(fn, "x", x, ldx, 16 * (int64_t)B, 1, 1));
+    QMM_CHECK(check_matrix(fn, "sx", sx, ldsx, B, 1, 1));
   } else {
     QMM_CHECK(check_values(fn, "x", x, ldx, K, x_dtype));
   }
@@ -185,29 +184,14 @@ qmm_status qmm_mx4_gemm(const void* x, int x_dtype, int64_t ldx, const uint8_t* 
   a.w = static_cast<const uint8_t*>(W);
   a.y = y, a.y_dtype = y_dtype, a.ldy = ldy;
   a.M = M, a.N = N, a.K = K;
-  uint8_t* scratch = static_cast<uint8_t*>(workspace);
-  hipError_t e = hipSuccess;
-  if (!qmm::mx4_skinny_fits(M)) {
-    // both operands in the matrix cores' layout
-    a.a = scratch;
-    e = coded ? qmm::launch_mx4_pack(static_cast<const uint8_t*>(x), ldx, sx, ldsx, scratch, 1, M, K, s)
-              : qmm::launch_mx4_quantize_packed(x, x_dtype, ldx, scratch, M, K, s);
-    return device_status(fn, e != hipSuccess ? e : qmm::launch_mx4_large(a, s));
-  }
-  if (coded) {
-    a.a = static_cast<const uint8_t*>(x);
-    a.lda = ldx;
-    a.sa = sx;
-    a.ldsa = ldsx;
-  } else {
-    a.lda = 16 * (int64_t)B;
-    a.ldsa = qmm::round_up(B, 4);
-    uint8_t* scales = scratch + (size_t)M * a.lda;
-    e = qmm::launch_mx4_quantize(x, x_dtype, ldx, scratch, a.lda, scales, a.ldsa, M, K, s);
-    a.a = scratch;
-    a.sa = scales;
-  }
-  return device_status(fn, e != hipSuccess ? e : qmm::launch_mx4_skinny(a, s));
+  if (!coded && qmm::mx4_rows_fits(M, K)) return device_status(fn, qmm::launch_mx4_rows(a, x, x_dtype, ldx, s));
+  // x in the matrix cores' layout, as the weight
+  uint8_t* packed = static_cast<uint8_t*>(workspace);
+  a.a = packed;
+  hipError_t e = coded ? qmm::launch_mx4_pack(static_cast<const uint8_t*>(x), ldx, sx, ldsx, packed, 1, M, K, s)
+                       : qmm::launch_mx4_quantize_packed(x, x_dtype, ldx, packed, M, K, s);
+  if (e == hipSuccess) e = qmm::mx4_skinny_fits(M) ? qmm::launch_mx4_skinny(a, s) : qmm::launch_mx4_large(a, s);
+  return device_status(fn, e);
 }
 
 size_t qmm_mx4_moe_workspace_bytes(int T, int D, int I, int E, int top_k, int x_dtype, int y_dtype) {

@@ -37,16 +37,17 @@ hipError_t launch_mx4_quantize_packed(const void* x, int x_dtype, int64_t ldx, u
 
 // ---- product ---------------------------------------------------------------
 struct Mx4Args {
-  const uint8_t* a;  // skinny: codes (M, 16 blocks bytes), scales (M, blocks); large: packed (M, K)
-  int64_t lda;
-  const uint8_t* sa;
-  int64_t ldsa;
+  const uint8_t* a;  // packed (M, K)
   const uint8_t* w;  // packed (N, K)
   void* y;
   int y_dtype;
   int64_t ldy;
   int M, N, K;
 };
+// Few values (mx4_skinny.hip): quantized within the launch; a.a counts for nothing.
+bool mx4_rows_fits(int M, int K);
+hipError_t launch_mx4_rows(const Mx4Args& a, const void* x, int x_dtype, int64_t ldx, hipStream_t s);
+// Up to 64 rows, and more (mx4_large.hip).
 bool mx4_skinny_fits(int M);
 hipError_t launch_mx4_skinny(const Mx4Args& a, hipStream_t s);
 hipError_t launch_mx4_large(const Mx4Args& a, hipStream_t s);

@@ -1,69 +1,300 @@
-// mx4_skinny.hip -- products of microscaled 4-bit codes, y = x^ W^t.
+// mx4_skinny.hip -- products of microscaled 4-bit codes for up to 64 rows, y = x^ W^t:
+// bound by reading the weights once.  The packed strip is the matrix cores' operand:
+// waves stream chunks of 512 values from memory straight to registers and multiply
+// them by v_mfma_scale_f32_16x16x128_f8f6f4, a few instructions for each KiB; what the
+// kernels differ in is where the activations' operand comes from.
 //
-// A workgroup owns 16 rows and one strip of 16 columns; its 4 waves take steps
-// of 128 values (a quarter of a chunk) in turn and add their sums in LDS.  The packed strip is the
-// matrix cores' operand: 1 KiB of consecutive bytes per step.
+//  rows    (few values) x is quantized by every workgroup itself, into LDS in the
+//          operand's order, while its first weights are on their way: one launch;
+//  packed  x comes packed as weights are, and is read as they are.
+//
+// The waves of a workgroup split K (chunks in turn) and add their sums in LDS in a fixed order.
+#include <type_traits>
+
 #include "mx4_device.h"
 
 namespace qmm {
 
-__global__ __launch_bounds__(256) void mx4_skinny_kernel(Mx4Args g, int strips) {
-  __shared__ float sums[4][16][17];
+// A chunk of a packed strip: a lane's 4 blocks and their scales.
+struct Chunk {
+  u32x4_t c[4];
+  uint32_t s;
+};
+// (p NULL: zeros)
+template <int AUX> __device__ __forceinline__ void load_chunk(Chunk& w, const uint8_t* p, int lane) {
+  const buf_t b = make_buf(p, p != nullptr ? kChunkBytes : 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w.c[j] = __builtin_amdgcn_raw_buffer_load_b128(b, 16 * lane, 1024 * j, AUX);
+  w.s = __builtin_amdgcn_raw_buffer_load_b32(b, 4096 + 4 * lane, 0, AUX);
+}
+
+// block J of the lane's 4: byte J of the scale words
+template <int J>
+__device__ __forceinline__ f32x4_t mfma_block(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c, uint32_t sa, uint32_t sb) {
+  const i32x8_t x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8_t y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, J, (int)sa, J, (int)sb);
+}
+
+// ---- rows ------------------------------------------------------------------------
+// LDS: x's codes, 16 bytes for each (chunk, j, q, row) of a block 4 q + j, then its scales, a
+// word for each (chunk, q, row), then the waves' sums of two strips in turn.
+__host__ __device__ constexpr int rows_code_bytes(int M, int chunks) { return chunks * M * 256; }
+__host__ __device__ constexpr int rows_x_bytes(int M, int chunks) { return chunks * M * 272; }
+
+// `opts`: bits 0-4 M, 5-6 the output's type, 7 whole 16-byte loads of x
+template <int XT, int KW>
+__global__ __launch_bounds__(64 * KW) void mx4_rows_kernel(const uint8_t* __restrict__ w, const void* __restrict__ x,
+                                                           int64_t ldx, int N, int K, int opts, int groups,
+                                                           void* __restrict__ y, int64_t ldy) {
+  typedef typename Elem<XT>::type T;
+  extern __shared__ __align__(16) unsigned char lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
-  const int strip = (int)(blockIdx.x % (unsigned)strips), m0 = 16 * (int)(blockIdx.x / (unsigned)strips);
-  const int steps = 4 * mx4_chunks(g.K), blocks = mx4_blocks(g.K);
-  const uint8_t* w = g.w + (int64_t)strip * mx4_strip_bytes(g.K);
-  const int m = m0 + l16;
-  const uint8_t* a = g.a + (int64_t)(m < g.M ? m : 0) * g.lda;
-  const uint8_t* sa = g.sa + (int64_t)(m < g.M ? m : 0) * g.ldsa;
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  for (int s = wave; s < steps; s += 4) {
-    const int b = 16 * (s / 4) + 4 * quad + s % 4;
-    const uint8_t* c = w + (int64_t)kChunkBytes * (s / 4);
-    const u32x4_t cb = *reinterpret_cast<const u32x4_t*>(c + 1024 * (s % 4) + 16 * lane);
-    const uint32_t eb = c[4096 + 4 * lane + s % 4];
-    u32x4_t ca = {0u, 0u, 0u, 0u};
-    uint32_t ea = 127;
-    if (b < blocks && m < g.M) {
-      ca = *reinterpret_cast<const u32x4_t*>(a + 16 * b);
-      ea = sa[b];
+  const int M = opts & 31, ydt = (opts >> 5) & 3;
+  const bool vec = (opts >> 7) & 1;
+  const int chunks = mx4_chunks(K), strips = (N + 15) / 16;
+  float* sums = reinterpret_cast<float*>(lds + rows_x_bytes(M, chunks));
+
+  // ---- this wave's chunks of the workgroup's strips, a ring of them on its way
+  constexpr int RING = 3;
+  Chunk ring[RING];
+  const int64_t strip_bytes = mx4_strip_bytes(K);
+  int ls = (int)blockIdx.x, lc = wave;  // what is requested next
+  auto request = [&](Chunk& c) {
+    load_chunk<kStream>(c, ls < strips && lc < chunks ? w + ls * strip_bytes + (int64_t)kChunkBytes * lc : nullptr, lane);
+    lc += KW;
+    if (lc >= chunks) lc = wave, ls += groups;
+  };
+
+  // ---- x to LDS, 8 values a thread and turn
+  const int per = 64 * chunks, units = M * per;  // a row's units; all
+  auto get = [&](int u) {
+    const int r = u / per, k = 8 * (u - r * per);
+    const T* p = static_cast<const T*>(x) + (int64_t)r * ldx + k;
+    const int n = u < units ? K - k : 0;
+    Raw8<XT> v = {};
+    if (vec) {
+      if (n > 0) {
+        const u32x4_t* q = reinterpret_cast<const u32x4_t*>(p);
+        v.w[0] = q[0];
+        if constexpr (XT == YF32) v.w[1] = q[1];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j >= n) break;
+        if constexpr (XT == YF32) v.w[j / 4][j % 4] = __builtin_bit_cast(uint32_t, p[j]);
+        else v.w[0][j / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[j]) << (16 * (j % 2));
+      }
     }
-    acc = mfma_mx4(ca, cb, acc, ea, eb);
+    return v;
+  };
+  auto put = [&](int u, const Raw8<XT>& v) {
+    uint32_t top = top_f32<XT>(top8<XT>(v, 0u));
+    uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, false);
+    top = o > top ? o : top;
+    o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xF, 0xF, false);
+    top = o > top ? o : top;
+    const uint32_t e = scale_byte(top);
+    float f[8];
+    floats8<XT>(v, f);
+    if (u >= units) return;
+    const int r = u / per, i = u - r * per, c = i / 64, b = (i >> 2) & 15, q = b >> 2, j = b & 3;
+    *reinterpret_cast<uint32_t*>(lds + ((16 * c + 4 * j + q) * M + r) * 16 + 4 * (i & 3)) = codes_of8(f, e);
+    if ((i & 3) == 0) lds[rows_code_bytes(M, chunks) + ((4 * c + q) * M + r) * 4 + j] = (uint8_t)e;
+  };
+  // loads return in order: all of x but each thread's last unit goes first, then that unit's
+  // values, then the weights, so that it is quantized while these are on their way
+  int u = threadIdx.x;
+  for (; u + 64 * KW < units; u += 64 * KW) put(u, get(u));
+  const Raw8<XT> held = get(u);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < RING; ++i) request(ring[i]);
+  __builtin_amdgcn_sched_barrier(0);
+  put(u, held);
+  __syncthreads();
+
+  // ---- products
+  const int row = l16 < M ? l16 : 0;
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  int c = wave, parity = 0;
+  auto use = [&](const Chunk& b) {
+    const int cc = c < chunks ? c : 0;  // (a wave without a chunk has zeros for weights)
+    const unsigned char* p = lds + ((16 * cc + quad) * M + row) * 16;
+    const uint32_t sa = *reinterpret_cast<const uint32_t*>(lds + rows_code_bytes(M, chunks) + ((4 * cc + quad) * M + row) * 4);
+    auto a = [&](int j) { return *reinterpret_cast<const u32x4_t*>(p + 64 * j * M); };
+    acc = mfma_block<0>(a(0), b.c[0], acc, sa, b.s);
+    acc = mfma_block<1>(a(1), b.c[1], acc, sa, b.s);
+    acc = mfma_block<2>(a(2), b.c[2], acc, sa, b.s);
+    acc = mfma_block<3>(a(3), b.c[3], acc, sa, b.s);
+  };
+  auto finish = [&](int strip) {
+    float* s = sums + parity * (KW * M * 16);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (4 * quad + r < M) s[(wave * M + 4 * quad + r) * 16 + l16] = acc[r];
+    acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    __syncthreads();
+    const int m = threadIdx.x / 16, n = 16 * strip + (int)threadIdx.x % 16;
+    if (m < M && n < N) {
+      float v = 0.f;
+#pragma unroll
+      for (int q = 0; q < KW; ++q) v += s[(q * M + m) * 16 + threadIdx.x % 16];
+      with_y(y, ydt, [&](auto* yt) {
+        typedef typename std::remove_pointer<decltype(yt)>::type Y;
+        yt[(int64_t)m * ldy + n] = (Y)v;
+      });
+    }
+    parity ^= 1;
+  };
+  for (int strip = (int)blockIdx.x; strip < strips;) {
+#pragma unroll
+    for (int i = 0; i < RING; ++i) {
+      if (strip < strips) {
+        use(ring[i]);
+        request(ring[i]);
+        c += KW;
+        if (c >= chunks) {
+          finish(strip);
+          c = wave;
+          strip += groups;
+        }
+      }
+    }
+  }
+}
+
+// ---- packed ----------------------------------------------------------------------
+// A workgroup: all rows (MT strips of the packed x) and PS strips of columns.
+template <int MT, int PS, int KW, class Y>
+__global__ __launch_bounds__(64 * KW, 1) void mx4_packed_kernel(Mx4Args g) {
+  __shared__ float sums[KW][PS][16 * MT][17];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, quad = lane >> 4;
+  const int chunks = mx4_chunks(g.K), s0 = PS * (int)blockIdx.x;
+  const int strips = (g.N + 15) / 16, mt = (g.M + 15) / 16;
+  const int64_t strip_bytes = mx4_strip_bytes(g.K);
+  struct Stage {
+    Chunk a[MT], b[PS];
+  };
+  auto request = [&](Stage& s, int c) {
+    const int64_t at = (int64_t)kChunkBytes * c;
+#pragma unroll
+    for (int p = 0; p < PS; ++p)
+      load_chunk<kStream>(s.b[p], c < chunks && s0 + p < strips ? g.w + (s0 + p) * strip_bytes + at : nullptr, lane);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) load_chunk<0>(s.a[i], c < chunks && i < mt ? g.a + i * strip_bytes + at : nullptr, lane);
+  };
+  f32x4_t acc[MT][PS];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int p = 0; p < PS; ++p) acc[i][p] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto use = [&](const Stage& s) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int p = 0; p < PS; ++p) {
+        acc[i][p] = mfma_block<0>(s.a[i].c[0], s.b[p].c[0], acc[i][p], s.a[i].s, s.b[p].s);
+        acc[i][p] = mfma_block<1>(s.a[i].c[1], s.b[p].c[1], acc[i][p], s.a[i].s, s.b[p].s);
+        acc[i][p] = mfma_block<2>(s.a[i].c[2], s.b[p].c[2], acc[i][p], s.a[i].s, s.b[p].s);
+        acc[i][p] = mfma_block<3>(s.a[i].c[3], s.b[p].c[3], acc[i][p], s.a[i].s, s.b[p].s);
+      }
+  };
+  Stage st[2];
+  request(st[0], wave);
+  request(st[1], wave + KW);
+  for (int c = wave; c < chunks; c += 2 * KW) {
+    use(st[0]);
+    request(st[0], c + 2 * KW);
+    use(st[1]);
+    request(st[1], c + 3 * KW);
   }
 #pragma unroll
-  for (int r = 0; r < 4; ++r) sums[wave][4 * quad + r][l16] = acc[r];
+  for (int p = 0; p < PS; ++p)
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sums[wave][p][16 * i + 4 * quad + r][l16] = acc[i][p][r];
   __syncthreads();
-  const int row = threadIdx.x / 16, col = threadIdx.x % 16;
-  const int n = 16 * strip + col;
-  if (m0 + row >= g.M || n >= g.N) return;
-  const float v = (sums[0][row][col] + sums[1][row][col]) + (sums[2][row][col] + sums[3][row][col]);
-  with_y(g.y, g.y_dtype, [&](auto* yt) {
-    typedef typename std::remove_pointer<decltype(yt)>::type Y;
-    yt[(int64_t)(m0 + row) * g.ldy + n] = (Y)v;
-  });
+  for (int i = threadIdx.x; i < 16 * MT * 16 * PS; i += 64 * KW) {
+    const int m = i / (16 * PS), col = i % (16 * PS), n = 16 * s0 + col;
+    if (m >= g.M || n >= g.N) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < KW; ++q) v += sums[q][col / 16][m][col % 16];
+    static_cast<Y*>(g.y)[(int64_t)m * g.ldy + n] = (Y)v;
+  }
 }
 
 // ---------------------------------------------------------------- host side
+constexpr int kRowsLds = 64 << 10;
+
+static int rows_lds(int M, int K, int waves) { return rows_x_bytes(M, mx4_chunks(K)) + 2 * waves * M * 16 * 4; }
+// Where strips are too few to occupy the chip, more waves share each.
+static int rows_waves(int M, int N, int K) { return (N + 15) / 16 <= 128 && rows_lds(M, K, 16) <= kRowsLds ? 16 : 8; }
+
 bool mx4_skinny_fits(int M) { return M <= 64; }
 
-hipError_t launch_mx4_skinny(const Mx4Args& a, hipStream_t s) {
-  const int strips = (a.N + 15) / 16;
-  const int64_t tiles = ((int64_t)a.M + 15) / 16;
-  const int64_t most = kMaxGroups / strips > 0 ? kMaxGroups / strips : 1;
-  if (strips > kMaxGroups) return hipErrorInvalidValue;
+// Every workgroup quantizes all of x: up to 64 Ki values this costs less than a launch.
+bool mx4_rows_fits(int M, int K) {
+  return M <= 16 && (int64_t)M * K <= (1 << 16) && rows_lds(M, K, 8) <= kRowsLds;
+}
+
+template <int XT, int KW>
+static hipError_t rows_k(const Mx4Args& a, const void* x, int64_t ldx, bool vec, hipStream_t s) {
+  const int strips = (a.N + 15) / 16, lds = rows_lds(a.M, a.K, KW);
+  // workgroups that are on the chip at once
+  const int most = KW == 16 ? 256 : 512;
+  int groups = strips < most ? strips : most, N = a.N, K = a.K, opts = a.M | (a.y_dtype << 5) | (vec ? 128 : 0);
+  const uint8_t* w = a.w;
+  void* y = a.y;
+  int64_t ldy = a.ldy;
+  void* p[] = {&w, &x, &ldx, &N, &K, &opts, &groups, &y, &ldy};
+  return hipLaunchKernel(reinterpret_cast<const void*>(mx4_rows_kernel<XT, KW>), dim3((unsigned)groups), dim3(64 * KW), p,
+                         (size_t)lds, s);
+}
+template <int XT> static hipError_t rows_t(const Mx4Args& a, const void* x, int64_t ldx, hipStream_t s) {
+  const bool vec = vec8_ok(x, ldx, a.K, XT == YF32 ? 4 : 2) && a.K % 8 == 0;
+  return rows_waves(a.M, a.N, a.K) == 16 ? rows_k<XT, 16>(a, x, ldx, vec, s) : rows_k<XT, 8>(a, x, ldx, vec, s);
+}
+hipError_t launch_mx4_rows(const Mx4Args& a, const void* x, int x_dtype, int64_t ldx, hipStream_t s) {
+  switch (x_dtype) {
+    case XF16: return rows_t<XF16>(a, x, ldx, s);
+    case XBF16: return rows_t<XBF16>(a, x, ldx, s);
+  }
+  return rows_t<YF32>(a, x, ldx, s);
+}
+
+template <int MT, int PS, int KW> static hipError_t packed_y(const Mx4Args& a, hipStream_t s) {
+  const int64_t strips = ((int64_t)a.N + 15) / 16, most = kMaxGroups * 256 / (64 * KW) * PS;  // of a launch
   hipError_t e = hipSuccess;
-  for (int64_t t = 0; t < tiles && e == hipSuccess; t += most) {
+  for (int64_t f = 0; f < strips && e == hipSuccess; f += most) {
     Mx4Args g = a;
-    g.a += 16 * t * a.lda;
-    g.sa += 16 * t * a.ldsa;
-    g.y = static_cast<char*>(a.y) + 16 * t * a.ldy * (a.y_dtype == YF32 ? 4 : 2);
-    g.M = (int)(a.M - 16 * t < 16 * most ? a.M - 16 * t : 16 * most);
-    const int64_t now = ((int64_t)g.M + 15) / 16;
-    e = launch_kernel(mx4_skinny_kernel, dim3((unsigned)(now * strips)), dim3(256), s, g, strips);
+    g.w += f * mx4_strip_bytes(a.K);
+    g.y = static_cast<char*>(a.y) + 16 * f * (a.y_dtype == YF32 ? 4 : 2);
+    g.N = (int)(a.N - 16 * f < 16 * most ? a.N - 16 * f : 16 * most);
+    const dim3 grid((unsigned)((((int64_t)g.N + 15) / 16 + PS - 1) / PS)), block(64 * KW);
+    switch (a.y_dtype) {
+      case XF16: e = launch_kernel(mx4_packed_kernel<MT, PS, KW, _Float16>, grid, block, s, g); break;
+      case XBF16: e = launch_kernel(mx4_packed_kernel<MT, PS, KW, __bf16>, grid, block, s, g); break;
+      default: e = launch_kernel(mx4_packed_kernel<MT, PS, KW, float>, grid, block, s, g);
+    }
   }
   return e;
+}
+template <int MT> static hipError_t packed_m(const Mx4Args& a, hipStream_t s) {
+  const int strips = (a.N + 15) / 16;
+  if (strips >= 4 * 192) return packed_y<MT, 4, 4>(a, s);
+  if (strips >= 2 * 192) return packed_y<MT, 2, MT == 4 ? 4 : 8>(a, s);
+  return packed_y<MT, 1, MT == 1 ? 16 : 8>(a, s);
+}
+hipError_t launch_mx4_skinny(const Mx4Args& a, hipStream_t s) {
+  return a.M <= 16 ? packed_m<1>(a, s) : a.M <= 32 ? packed_m<2>(a, s) : packed_m<4>(a, s);
 }
 
 }  // namespace qmm

@@ -22,7 +22,7 @@ import ctypes
 
 import torch
 
-from . import (QMM_BF16, QMM_ERR_ARG, QMM_ERR_UNSUPPORTED, QMM_F16, QMM_F32, _lib)
+from . import QMM_BF16, QMM_F16, QMM_F32, _lib
 from .int8 import _act, _float_type, _matrix, _one_gpu, _output, _refuse, _run
 
 QMM_MX4 = 4  # x_dtype of activations that are codes already
@@ -152,13 +152,6 @@ def mx4_gemm(x, W, N, sx=None, out=None, out_dtype=torch.float32):
             _refuse(fn, "uint8 x needs its scales (sx)")
         px, ldx, ps, lds, B = _coded(fn, x, sx)
         code, K = QMM_MX4, 32 * B
-        if x.shape[0] <= 1:
-            lds = -(-lds // 4) * 4
-        if B % 4 and x.shape[0]:
-            end = sx.storage_offset() + (x.shape[0] - 1) * lds + -(-B // 4) * 4
-            if end > sx.untyped_storage().nbytes():
-                _refuse(fn, f"sx has rows of {B} scales: its storage must hold whole 4 bytes for each row (pad "
-                            f"the rows; mx4_quantize does)", QMM_ERR_UNSUPPORTED)
     else:
         px, ldx = _matrix(fn, "x", x)
         if sx is not None:

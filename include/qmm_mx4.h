@@ -84,18 +84,15 @@ QMM_API size_t qmm_mx4_packed_bytes(int N, int K);
 QMM_API qmm_status qmm_mx4_pack(const uint8_t* codes, int64_t ldc, const uint8_t* scales,
                                 int64_t lds, void* W, int batch, int N, int K, void* stream);
 
-/* Scratch of qmm_mx4_gemm for activations that the call quantizes itself (x_dtype
- * other than QMM_MX4) or, where there are many, lays out.  Device memory, 16-byte
- * aligned, any contents; in use until the call's work on the stream is done.  0
- * where none is needed and for invalid arguments. */
+/* Scratch of qmm_mx4_gemm: x laid out as the weight is.  Device memory, 16-byte aligned,
+ * any contents; in use until the call's work on the stream is done.  0 for a few
+ * values (which are quantized within the product's launch) and for invalid arguments. */
 QMM_API size_t qmm_mx4_workspace_bytes(int M, int K, int x_dtype);
 
 /*
  * qmm_mx4_gemm: y (M, N) of y_dtype (QMM_F32, QMM_F16, QMM_BF16) = x^ W^t.
- * x is either codes (x_dtype QMM_MX4, (M, 16 B), 16-byte aligned, ldx a multiple
- * of 16) with their scales sx ((M, B), 4-byte aligned, ldsx a multiple of 4: the
- * bytes of a row up to a multiple of 4 are read, and those from B on take no
- * part), or values (sx NULL), which the call quantizes as qmm_mx4_quantize does.
+ * x is either codes (x_dtype QMM_MX4, (M, 16 B), any alignment and ld) with their scales
+ * sx (M, B), or values (sx NULL), which the call quantizes as qmm_mx4_quantize does.
  * W is a packed weight (N, K).  Sums are fp32, rounded to y's type once.
  */
 QMM_API qmm_status qmm_mx4_gemm(const void* x, int x_dtype, int64_t ldx, const uint8_t* sx,

@@ -60,11 +60,10 @@ BAD = [
     (gemm, dict(t=3), ARG, "x_dtype"), (gemm, dict(yt=4), ARG, "y_dtype"), (gemm, dict(N=-1), ARG, "negative"),
     (gemm, dict(x=None), ARG, "NULL x"), (gemm, dict(sx=None), ARG, "NULL sx"), (gemm, dict(W=None), ARG, "NULL W"),
     (gemm, dict(W=MIS), ARG, "16-byte"), (gemm, dict(y=None), ARG, "NULL y"), (gemm, dict(ldy=31), ARG, "of y"),
-    (gemm, dict(x=MIS), ARG, "16-byte"), (gemm, dict(ldx=40), UNS, "multiple of 16"), (gemm, dict(ldx=16), ARG, "of x"),
-    (gemm, dict(sx=A + 2), ARG, "4-byte"), (gemm, dict(ldsx=6), UNS, "multiple of 4"), (gemm, dict(ldsx=1), ARG, "of sx"),
-    (gemm, dict(t=1), ARG, "must be NULL for values"), (gemm, dict(t=1, sx=None, ldx=64), ARG, "workspace of"),
-    (gemm, dict(t=1, sx=None, ldx=64, ws=A, n=10), ARG, "workspace of"),
-    (gemm, dict(t=1, sx=None, ldx=64, ws=MIS, n=1 << 20), ARG, "16-byte aligned"),
+    (gemm, dict(ldx=16), ARG, "of x"), (gemm, dict(ldsx=1), ARG, "of sx"), (gemm, dict(t=2, sx=None, ldx=64, x=A + 2), ARG, "4-byte"),
+    (gemm, dict(t=1), ARG, "must be NULL for values"), (gemm, dict(), ARG, "workspace of"),
+    (gemm, dict(t=1, sx=None, ldx=64, M=17), ARG, "workspace of"), (gemm, dict(ws=A, n=10), ARG, "workspace of"),
+    (gemm, dict(ws=MIS, n=1 << 20), ARG, "16-byte aligned"),
     (gemm, dict(K=1 << 20, ldx=1 << 19, ldsx=1 << 15), UNS, "too large"), (gemm, dict(M=2 ** 31 - 1), UNS, "too large"),
     (moe, dict(t=4), ARG, "x_dtype"), (moe, dict(yt=3), ARG, "y_dtype"), (moe, dict(act=3), ARG, "act must be"),
     (moe, dict(T=-1), ARG, "negative"), (moe, dict(T=65), UNS, "too large"), (moe, dict(E=1025, ldl=1025), UNS, "too large"),
@@ -100,8 +99,10 @@ def test_sizes():
     assert L.qmm_mx4_packed_bytes(16, 512) == L.qmm_mx4_packed_bytes(1, 1) == 4352
     assert L.qmm_mx4_packed_bytes(17, 512) == 2 * 4352 and L.qmm_mx4_packed_bytes(16, 513) == 2 * 4352
     assert L.qmm_mx4_packed_bytes(0, 128) == L.qmm_mx4_packed_bytes(16, 0) == L.qmm_mx4_packed_bytes(16, 1 << 20) == 0
-    assert L.qmm_mx4_workspace_bytes(100, 4096, 4) == 0 and L.qmm_mx4_workspace_bytes(0, 64, 1) == 0
-    assert L.qmm_mx4_workspace_bytes(100, 1 << 20, 1) == 0 and L.qmm_mx4_workspace_bytes(2 ** 31 - 1, 64, 1) == 0
+    need = L.qmm_mx4_workspace_bytes
+    assert need(0, 64, 1) == need(100, 1 << 20, 1) == need(2 ** 31 - 1, 64, 1) == need(4, 64, 3) == 0
+    assert need(1, 4096, 1) == 0 and need(16, 4096, 0) == 0  # a few values: quantized within the launch
+    assert need(16, 8192, 0) == need(1, 8192, 4) == 16 * 4352 and need(100, 4096, 4) == 7 * 8 * 4352
     need = L.qmm_mx4_moe_workspace_bytes
     assert need(65, 64, 64, 8, 2, 1, 1) == need(4, 64, 64, 8, 2, 4, 1) == need(0, 64, 64, 8, 2, 1, 1) == 0
     assert 0 < need(4, 64, 64, 8, 2, 1, 1) <= need(4, 64, 64, 8, 2, 2, 2)
@@ -134,7 +135,7 @@ def test_binding_checks():
     raises(lambda: qmm.mx4_gemm(x, W.int(), 32), "W must be a uint8")
     raises(lambda: qmm.mx4_gemm(u8(4, 32), W, 32), "needs its scales")
     raises(lambda: qmm.mx4_gemm(x, W, 32, sx=u8(4, 2)), "goes with uint8")
-    raises(lambda: qmm.mx4_gemm(u8(4, 32), W, 32, sx=u8(4, 2)), "whole 4 bytes", UNS)
+    raises(lambda: qmm.mx4_gemm(u8(4, 32), W, 32, sx=u8(4, 3)), "scales must be")
     raises(lambda: qmm.mx4_gemm(x[0], W, 32), "2-D")
     raises(lambda: qmm.mx4_gemm(x, W, 32, out=torch.zeros(4, 31)), "GPU tensors")
     up, down = u8(8, qmm.mx4_packed_bytes(32, 64)), u8(8, qmm.mx4_packed_bytes(64, 32))
