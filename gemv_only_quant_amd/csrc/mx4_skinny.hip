@@ -42,8 +42,8 @@ __device__ __forceinline__ f32x4_t mfma_block(const u32x4_t& a, const u32x4_t& b
 __host__ __device__ constexpr int rows_code_bytes(int M, int chunks) { return chunks * M * 256; }
 __host__ __device__ constexpr int rows_x_bytes(int M, int chunks) { return chunks * M * 272; }
 
-// `opts`: bits 0-4 M, 5-6 the output's type, 7 whole 16-byte loads of x
-template <int XT, int KW>
+// VEC: whole 16-byte loads of x; `opts`: bits 0-4 M, 5-6 the output's type
+template <int XT, int KW, bool VEC>
 __global__ __launch_bounds__(64 * KW) void mx4_rows_kernel(const uint8_t* __restrict__ w, const void* __restrict__ x,
                                                            int64_t ldx, int N, int K, int opts, int groups,
                                                            void* __restrict__ y, int64_t ldy) {
@@ -53,7 +53,6 @@ __global__ __launch_bounds__(64 * KW) void mx4_rows_kernel(const uint8_t* __rest
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
   const int M = opts & 31, ydt = (opts >> 5) & 3;
-  const bool vec = (opts >> 7) & 1;
   const int chunks = mx4_chunks(K), strips = (N + 15) / 16;
   float* sums = reinterpret_cast<float*>(lds + rows_x_bytes(M, chunks));
 
@@ -68,14 +67,14 @@ __global__ __launch_bounds__(64 * KW) void mx4_rows_kernel(const uint8_t* __rest
     if (lc >= chunks) lc = wave, ls += groups;
   };
 
-  // ---- x to LDS, 8 values a thread and turn
-  const int per = 64 * chunks, units = M * per;  // a row's units; all
-  auto get = [&](int u) {
-    const int r = u / per, k = 8 * (u - r * per);
+  // ---- x to LDS: a turn of a wave is a chunk of a row, 8 values a lane
+  const int turns = M * chunks;
+  auto get = [&](int t) {
+    const int r = t / chunks, k = 512 * (t - r * chunks) + 8 * lane;
     const T* p = static_cast<const T*>(x) + (int64_t)r * ldx + k;
-    const int n = u < units ? K - k : 0;
+    const int n = K - k;
     Raw8<XT> v = {};
-    if (vec) {
+    if constexpr (VEC) {
       if (n > 0) {
         const u32x4_t* q = reinterpret_cast<const u32x4_t*>(p);
         v.w[0] = q[0];
@@ -91,7 +90,10 @@ __global__ __launch_bounds__(64 * KW) void mx4_rows_kernel(const uint8_t* __rest
     }
     return v;
   };
-  auto put = [&](int u, const Raw8<XT>& v) {
+  // lane: quarter lane % 4 of block lane / 4 = 4 q + j
+  const int pq = lane >> 4, pj = (lane >> 2) & 3;
+  auto put = [&](int t, const Raw8<XT>& v) {
+    const int r = t / chunks, c = t - r * chunks;
     uint32_t top = top_f32<XT>(top8<XT>(v, 0u));
     uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, false);
     top = o > top ? o : top;
@@ -100,21 +102,30 @@ __global__ __launch_bounds__(64 * KW) void mx4_rows_kernel(const uint8_t* __rest
     const uint32_t e = scale_byte(top);
     float f[8];
     floats8<XT>(v, f);
-    if (u >= units) return;
-    const int r = u / per, i = u - r * per, c = i / 64, b = (i >> 2) & 15, q = b >> 2, j = b & 3;
-    *reinterpret_cast<uint32_t*>(lds + ((16 * c + 4 * j + q) * M + r) * 16 + 4 * (i & 3)) = codes_of8(f, e);
-    if ((i & 3) == 0) lds[rows_code_bytes(M, chunks) + ((4 * c + q) * M + r) * 4 + j] = (uint8_t)e;
+    *reinterpret_cast<uint32_t*>(lds + ((16 * c + 4 * pj + pq) * M + r) * 16 + 4 * (lane & 3)) = codes_of8(f, e);
+    if ((lane & 3) == 0) lds[rows_code_bytes(M, chunks) + ((4 * c + pq) * M + r) * 4 + pj] = (uint8_t)e;
   };
-  // loads return in order: all of x but each thread's last unit goes first, then that unit's
-  // values, then the weights, so that it is quantized while these are on their way
-  int u = threadIdx.x;
-  for (; u + 64 * KW < units; u += 64 * KW) put(u, get(u));
-  const Raw8<XT> held = get(u);
+  // loads return in order: all of x but each wave's last few turns goes first, then these turns'
+  // values, then the weights, so that they are quantized while the weights are on their way
+  constexpr int HELD = XT == YF32 ? 2 : 4;
+  Raw8<XT> held[HELD];
+  int t = wave;
+  for (; t + HELD * KW < turns; t += HELD * KW) {
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) held[i] = get(t + i * KW);
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) put(t + i * KW, held[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < HELD; ++i)
+    if (t + i * KW < turns) held[i] = get(t + i * KW);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int i = 0; i < RING; ++i) request(ring[i]);
   __builtin_amdgcn_sched_barrier(0);
-  put(u, held);
+#pragma unroll
+  for (int i = 0; i < HELD; ++i)
+    if (t + i * KW < turns) put(t + i * KW, held[i]);
   __syncthreads();
 
   // ---- products
@@ -240,27 +251,29 @@ static int rows_waves(int M, int N, int K) { return (N + 15) / 16 <= 128 && rows
 
 bool mx4_skinny_fits(int M) { return M <= 64; }
 
-// Every workgroup quantizes all of x: up to 64 Ki values this costs less than a launch.
+// Every workgroup quantizes all of x: up to 32 Ki values this costs less than a launch (4096 x 4096, us: 1 row
+// 3.8, 4 5.0, 8 6.2, 16 9.1; packed first 7.8 to 8.5).
 bool mx4_rows_fits(int M, int K) {
-  return M <= 16 && (int64_t)M * K <= (1 << 16) && rows_lds(M, K, 8) <= kRowsLds;
+  return M <= 16 && (int64_t)M * K <= (1 << 15) && rows_lds(M, K, 8) <= kRowsLds;
 }
 
-template <int XT, int KW>
-static hipError_t rows_k(const Mx4Args& a, const void* x, int64_t ldx, bool vec, hipStream_t s) {
+template <int XT, int KW, bool VEC>
+static hipError_t rows_k(const Mx4Args& a, const void* x, int64_t ldx, hipStream_t s) {
   const int strips = (a.N + 15) / 16, lds = rows_lds(a.M, a.K, KW);
   // workgroups that are on the chip at once
   const int most = KW == 16 ? 256 : 512;
-  int groups = strips < most ? strips : most, N = a.N, K = a.K, opts = a.M | (a.y_dtype << 5) | (vec ? 128 : 0);
+  int groups = strips < most ? strips : most, N = a.N, K = a.K, opts = a.M | (a.y_dtype << 5);
   const uint8_t* w = a.w;
   void* y = a.y;
   int64_t ldy = a.ldy;
   void* p[] = {&w, &x, &ldx, &N, &K, &opts, &groups, &y, &ldy};
-  return hipLaunchKernel(reinterpret_cast<const void*>(mx4_rows_kernel<XT, KW>), dim3((unsigned)groups), dim3(64 * KW), p,
+  return hipLaunchKernel(reinterpret_cast<const void*>(mx4_rows_kernel<XT, KW, VEC>), dim3((unsigned)groups), dim3(64 * KW), p,
                          (size_t)lds, s);
 }
 template <int XT> static hipError_t rows_t(const Mx4Args& a, const void* x, int64_t ldx, hipStream_t s) {
   const bool vec = vec8_ok(x, ldx, a.K, XT == YF32 ? 4 : 2) && a.K % 8 == 0;
-  return rows_waves(a.M, a.N, a.K) == 16 ? rows_k<XT, 16>(a, x, ldx, vec, s) : rows_k<XT, 8>(a, x, ldx, vec, s);
+  if (rows_waves(a.M, a.N, a.K) == 16) return vec ? rows_k<XT, 16, true>(a, x, ldx, s) : rows_k<XT, 16, false>(a, x, ldx, s);
+  return vec ? rows_k<XT, 8, true>(a, x, ldx, s) : rows_k<XT, 8, false>(a, x, ldx, s);
 }
 hipError_t launch_mx4_rows(const Mx4Args& a, const void* x, int x_dtype, int64_t ldx, hipStream_t s) {
   switch (x_dtype) {
