@@ -70,38 +70,15 @@ struct MoeBufs {
   float* z;        // (T top_k, Dz): a token's rows of each of its experts
 };
 
-// A wave for each token's choice (the first T), then threads for x as parts.
-template <int XP>
-__global__ __launch_bounds__(256) void moe_route_kernel(MoeArgs g, MoeBufs o, int strips, int Dp) {
-  const int tid = (int)blockIdx.x * 256 + (int)threadIdx.x, lane = threadIdx.x & 63, k = g.top_k;
-  const int t = __builtin_amdgcn_readfirstlane(tid >> 6);
-  for (int i = tid; i < strips; i += (int)gridDim.x * 256) o.done[i] = 0;
-  const int groups = (g.T + 3) / 4;  // workgroups that choose
-  if ((int)blockIdx.x >= groups) {
-    const int units = Dp / 8;
-    for (int u = tid - 256 * groups; u < g.T * units; u += ((int)gridDim.x - groups) * 256) {
-      const int r = u / units, i = 8 * (u - r * units);
-      uint16_t p[8][XP];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        parts_of<XP>(i + j < g.D ? as_f32(g.x, (int64_t)r * g.ldx + i + j, g.x_dtype) : 0.f, p[j]);
-#pragma unroll
-      for (int q = 0; q < XP; ++q) {
-        u32x4_t v;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = p[2 * j][q] | ((uint32_t)p[2 * j + 1][q] << 16);
-        *reinterpret_cast<u32x4_t*>(o.x + ((int64_t)q * g.T + r) * Dp + operand_order(i)) = v;
-      }
-    }
-    return;
-  }
-  if (t >= g.T) return;
+// A wave's choice for token t: its experts and weights to ids and w, t k on.
+__device__ __forceinline__ void choose(const MoeArgs& g, int t, int lane, int* ids, float* w) {
+  const int k = g.top_k;
   if (g.logits == nullptr) {
     if (lane < k) {
       const int64_t i = (int64_t)t * k + lane;
       const int64_t e = g.ids_size == 8 ? static_cast<const int64_t*>(g.ids)[i] : static_cast<const int32_t*>(g.ids)[i];
-      o.ids[i] = e >= 0 && e < g.E ? (int)e : -1;
-      o.w[i] = as_f32(g.weights, i, g.weights_dtype);
+      ids[i] = e >= 0 && e < g.E ? (int)e : -1;
+      w[i] = as_f32(g.weights, i, g.weights_dtype);
     }
     return;
   }
@@ -133,7 +110,9 @@ __global__ __launch_bounds__(256) void moe_route_kernel(MoeArgs g, MoeBufs o, in
     const uint32_t top = wave_max_u32(best);
     if (top == 0) break;  // no expert is left
     last = top;
-    last_e = kMoeExperts - (int)wave_max_u32(best == top ? (uint32_t)(kMoeExperts - at) : 0u);
+    const uint64_t equal = __ballot(best == top);
+    last_e = (equal & (equal - 1)) == 0 ? __builtin_amdgcn_readlane(at, (int)__builtin_ctzll(equal))
+                                        : kMoeExperts - (int)wave_max_u32(best == top ? (uint32_t)(kMoeExperts - at) : 0u);
     const float v = value_of(top);
     if (j == 0) first = v;
     // (NaN, and infinity less infinity: the whole row)
@@ -147,8 +126,36 @@ __global__ __launch_bounds__(256) void moe_route_kernel(MoeArgs g, MoeBufs o, in
     sum = sum == sum ? wave_sum(all) : sum;
   }
   if (lane < k) {
-    o.ids[t * k + lane] = chosen;
-    o.w[t * k + lane] = mine / sum;
+    ids[t * k + lane] = chosen;
+    w[t * k + lane] = mine / sum;
+  }
+}
+
+// A wave for each token's choice (the first T), then threads for x as parts.
+template <int XP>
+__global__ __launch_bounds__(256) void moe_route_kernel(MoeArgs g, MoeBufs o, int strips, int Dp) {
+  const int tid = (int)blockIdx.x * 256 + (int)threadIdx.x, lane = threadIdx.x & 63;
+  const int t = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int i = tid; i < strips; i += (int)gridDim.x * 256) o.done[i] = 0;
+  const int groups = (g.T + 3) / 4;  // workgroups that choose
+  if ((int)blockIdx.x < groups) {
+    if (t < g.T) choose(g, t, lane, o.ids, o.w);
+    return;
+  }
+  const int units = Dp / 8;
+  for (int u = tid - 256 * groups; u < g.T * units; u += ((int)gridDim.x - groups) * 256) {
+    const int r = u / units, i = 8 * (u - r * units);
+    uint16_t p[8][XP];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      parts_of<XP>(i + j < g.D ? as_f32(g.x, (int64_t)r * g.ldx + i + j, g.x_dtype) : 0.f, p[j]);
+#pragma unroll
+    for (int q = 0; q < XP; ++q) {
+      u32x4_t v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = p[2 * j][q] | ((uint32_t)p[2 * j + 1][q] << 16);
+      *reinterpret_cast<u32x4_t*>(o.x + ((int64_t)q * g.T + r) * Dp + operand_order(i)) = v;
+    }
   }
 }
 
@@ -238,15 +245,15 @@ struct MoeLds {
   float sums[kMoeWaves][2][16][17];
 };
 
-template <int P, int G, class Fetch, class Put>
-__device__ __forceinline__ void sweep(const buf_t (&parts)[P], int offs, int members, int wave, int tile, int tiles, int chunks,
-                                      int blocks, char* lds, int lane, Fetch&& fetch, Put&& put) {
-  constexpr int RG = kRowGroup<P>;
-  const int l16 = lane & 15, quad = lane >> 4;
+// Where rows come from.  Parts: rows of bf16 parts in operand order; lane r has the offset of row r.
+template <int P> struct Parts {
+  static constexpr int RG = kRowGroup<P>;
+  buf_t parts[P];
+  int offs, members, blocks, lane;
+  char* lds;
   u32x4_t v[P][RG];
-  // row group g of chunk c to registers: lane r has the offset of row r.  16 bytes of lane L are 8 values of
-  // block 4 (L % 4) + L / 16.
-  auto request = [&](int g, int c) {
+  // row group g of chunk c to registers: 16 bytes of lane L are 8 values of block 4 (L % 4) + L / 16
+  __device__ __forceinline__ void request(int g, int c) {
     const int at = 4 * (lane & 3) + (lane >> 4) < blocks - 16 * c ? 16 * lane + 1024 * c : kNowhere;
 #pragma unroll
     for (int r = 0; r < RG; ++r) {
@@ -255,20 +262,74 @@ __device__ __forceinline__ void sweep(const buf_t (&parts)[P], int offs, int mem
 #pragma unroll
       for (int q = 0; q < P; ++q) v[q][r] = __builtin_amdgcn_raw_buffer_load_b128(parts[q], at, row, 0);
     }
-  };
-  auto leave = [&](int g) {
+  }
+  // and from there to LDS
+  __device__ __forceinline__ void leave(int g) {
 #pragma unroll
     for (int r = 0; r < RG; ++r) {
       if (r % 4 == 0 && RG * g + r >= members) break;
 #pragma unroll
       for (int q = 0; q < P; ++q) *reinterpret_cast<u32x4_t*>(lds + (RG * q + r) * kRowBytes + 16 * lane) = v[q][r];
     }
-  };
+  }
+};
+// x itself, up to 4 tokens whose rows are whole 16 bytes: 8 values a lane, made parts on the way to LDS.
+template <int XT, int P> struct Values {
+  static constexpr int RG = kRowGroup<P>, SIZE = XT == YF32 ? 4 : 2;
+  static_assert(RG >= 4, "rows");
+  buf_t rows[4];
+  int members, lane;
+  char* lds;
+  Raw8<XT> v[4];
+  __device__ __forceinline__ Values(const MoeArgs& g, int lane, char* lds) : members(g.T), lane(lane), lds(lds) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      rows[r] = make_buf(static_cast<const char*>(g.x) + (int64_t)(r < g.T ? r : 0) * g.ldx * SIZE,
+                         r < g.T ? (uint32_t)(g.D * SIZE) : 0u);
+  }
+  __device__ __forceinline__ void request(int, int c) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (r >= members) break;
+      v[r] = load8<XT, true>(rows[r], 512 * c + 8 * lane);
+    }
+  }
+  __device__ __forceinline__ void leave(int) {
+    // 8 values i = lane % 4 of block lane / 4 = 4 q + j
+    char* to = lds + 256 * ((lane >> 2) & 3) + 64 * (lane & 3) + 16 * (lane >> 4);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (r >= members) break;
+      if constexpr (P == 1) {
+        *reinterpret_cast<u32x4_t*>(to + r * kRowBytes) = v[r].w[0];
+      } else {
+        float f[8];
+        floats8<XT>(v[r], f);
+        uint16_t p[8][P];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) parts_of<P>(f[j], p[j]);
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+          u32x4_t o;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = p[2 * j][q] | ((uint32_t)p[2 * j + 1][q] << 16);
+          *reinterpret_cast<u32x4_t*>(to + (RG * q + r) * kRowBytes) = o;
+        }
+      }
+    }
+  }
+};
+
+template <int P, int G, class Source, class Fetch, class Put>
+__device__ __forceinline__ void sweep(Source& rows, int members, int wave, int tile, int tiles, int chunks, char* lds, int lane,
+                                      Fetch&& fetch, Put&& put) {
+  constexpr int RG = kRowGroup<P>;
+  const int l16 = lane & 15, quad = lane >> 4;
   MoeChunk w[2], wn[2];
   fetch(w, tile, wave);
   // rows that fit LDS at once and serve every tile stay there
   const bool stay = members <= RG && chunks <= kMoeWaves;
-  if (wave < chunks) request(0, wave);
+  if (wave < chunks) rows.request(0, wave);
   bool staged = false;
   for (; tile < tiles; ++tile) {
     f32x4_t acc[G][2];
@@ -281,13 +342,14 @@ __device__ __forceinline__ void sweep(const buf_t (&parts)[P], int offs, int mem
         if (RG * g >= members) break;
         const bool last = g + 1 == G || RG * (g + 1) >= members;
         if (!staged) {
-          leave(g);
+          rows.leave(g);
           staged = stay;
-          if (!last) request(g + 1, c);
-          else if (!stay && (more || tile + 1 < tiles)) request(0, more ? c + kMoeWaves : wave);
+          if (!last) rows.request(g + 1, c);
+          else if (!stay && (more || tile + 1 < tiles)) rows.request(0, more ? c + kMoeWaves : wave);
         }
         if (last) fetch(wn, more ? tile : tile + 1, more ? c + kMoeWaves : wave);
-        const char* from = lds + min(l16, RG - 1) * kRowBytes + 16 * quad;
+        // a row's parts are rows of the product, RG apart, and their sums are added afterwards
+        const char* from = lds + min(l16, P * RG - 1) * kRowBytes + 16 * quad;
         // (weights are converted anew for every group: kept, the operands would fill the registers)
 #pragma unroll
         for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(w[0].c[j]), "+v"(w[1].c[j]));
@@ -298,13 +360,9 @@ __device__ __forceinline__ void sweep(const buf_t (&parts)[P], int offs, int mem
           for (int i = 0; i < 4; ++i) {
             const bf16x8_t b0 = __builtin_bit_cast(bf16x8_t, bf16_of_codes(w[0].c[j][i], s0));
             const bf16x8_t b1 = __builtin_bit_cast(bf16x8_t, bf16_of_codes(w[1].c[j][i], s1));
-#pragma unroll
-            for (int q = 0; q < P; ++q) {
-              const u32x4_t a = *reinterpret_cast<const u32x4_t*>(from + RG * q * kRowBytes + 256 * j + 64 * i);
-              const bf16x8_t av = __builtin_bit_cast(bf16x8_t, a);
-              acc[g][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, b0, acc[g][0], 0, 0, 0);
-              acc[g][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, b1, acc[g][1], 0, 0, 0);
-            }
+            const bf16x8_t a = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t*>(from + 256 * j + 64 * i));
+            acc[g][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b0, acc[g][0], 0, 0, 0);
+            acc[g][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b1, acc[g][1], 0, 0, 0);
           }
         }
       }
@@ -326,7 +384,34 @@ __device__ __forceinline__ void meet(MoeLds& lds, const f32x4_t (&acc)[G][2], in
   __syncthreads();
 }
 
+// Column `col` of half `p` of row rr of the group that met: its parts' sums of all waves, the smallest part first.
+template <int P> __device__ __forceinline__ float met(const MoeLds& lds, int p, int rr, int col) {
+  float v = 0.f;
+#pragma unroll
+  for (int i = P; i-- > 0;)
+#pragma unroll
+    for (int q = 0; q < kMoeWaves; ++q) v += lds.sums[q][p][kRowGroup<P> * i + rr][col];
+  return v;
+}
+
 // ---- first half ----------------------------------------------------------------
+// Column threadIdx.x % 16 of strip t of h, from the waves' sums of row rr, for `place` of token `tok`.
+template <int XP, int HP>
+__device__ __forceinline__ void put_hidden(const MoeArgs& g, const MoeBufs& o, const MoeLds& lds, int rr, int t, int tok, int place,
+                                           float wt, int Ip) {
+  const int col = threadIdx.x % 16;
+  const float gv = met<XP>(lds, 0, rr, col), uv = met<XP>(lds, 1, rr, col);
+  float h = 0.f;
+  with_act(g.act, [&](auto a) {
+    float d;
+    h = act_parts<decltype(a)::value>(gv, &d) * uv * wt;
+  });
+  uint16_t p[HP];
+  parts_of<HP>(16 * t + col < g.I ? h : 0.f, p);  // the padding is 0 whatever x is
+#pragma unroll
+  for (int q = 0; q < HP; ++q) o.h[((int64_t)q * g.T * g.top_k + tok * g.top_k + place) * Ip + operand_order(16 * t + col)] = p[q];
+}
+
 // A workgroup: `per` strips of 16 columns of h of one expert.
 template <int XP, int HP, int G>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs g, MoeBufs o, int Dp, int Ip, int pairs, int per) {
@@ -353,33 +438,72 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs g, Mo
     tok[r] = lane, place[r] = m.place, wt[r] = m.w;
   }
   __syncthreads();
-  buf_t xb[XP];
-  part_buffers<XP>(xb, o.x, g.T, Dp);
-  const int rr = threadIdx.x / 16, col = threadIdx.x % 16;
   constexpr int RG = kRowGroup<XP>;
-  for (int r0 = 0; r0 < members; r0 += G * RG)
-  sweep<XP, G>(xb, r0 + lane < members ? 2 * tok[r0 + lane] * Dp : 0, members - r0, wave, tile, tiles, chunks, blocks,
-               lds.rows[wave], lane, fetch, [&](int t, const f32x4_t (&acc)[G][2]) {
+  for (int r0 = 0; r0 < members; r0 += G * RG) {
+    Parts<XP> rows;
+    part_buffers<XP>(rows.parts, o.x, g.T, Dp);
+    rows.offs = r0 + lane < members ? 2 * tok[r0 + lane] * Dp : 0;
+    rows.members = members - r0, rows.blocks = blocks, rows.lane = lane, rows.lds = lds.rows[wave];
+    sweep<XP, G>(rows, members - r0, wave, tile, tiles, chunks, lds.rows[wave], lane, fetch, [&](int t, const f32x4_t (&acc)[G][2]) {
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      if (r0 + RG * i >= members) break;
-      meet<G>(lds, acc, i, wave, lane);
-      const int r = r0 + RG * i + rr;
-      if (rr >= RG || r >= members) continue;
-      float gv = 0.f, uv = 0.f;
-#pragma unroll
-      for (int q = 0; q < kMoeWaves; ++q) gv += lds.sums[q][0][rr][col], uv += lds.sums[q][1][rr][col];
-      float h = 0.f;
-      with_act(g.act, [&](auto a) {
-        float d;
-        h = act_parts<decltype(a)::value>(gv, &d) * uv * wt[r];
-      });
-      uint16_t p[HP];
-      parts_of<HP>(16 * t + col < g.I ? h : 0.f, p);  // the padding is 0 whatever x is
-#pragma unroll
-      for (int q = 0; q < HP; ++q)
-        o.h[((int64_t)q * g.T * g.top_k + tok[r] * g.top_k + place[r]) * Ip + operand_order(16 * t + col)] = p[q];
+      for (int i = 0; i < G; ++i) {
+        if (r0 + RG * i >= members) break;
+        meet<G>(lds, acc, i, wave, lane);
+        const int rr = threadIdx.x / 16, r = r0 + RG * i + rr;
+        if (rr < RG && r < members) put_hidden<XP, HP>(g, o, lds, rr, t, tok[r], place[r], wt[r], Ip);
+      }
+    });
+  }
+}
+
+// The same for up to 4 tokens, with their choices made by every workgroup itself (a launch less), rows of the product
+// the tokens in their order.  The first workgroup leaves the choices for the second half.
+template <int XT, int XP, int HP>
+__global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_few_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int per, int strips_y) {
+  __shared__ MoeLds lds;
+  __shared__ int ids[4 * kMoeTopK];
+  __shared__ float ws[4 * kMoeTopK];
+  const int lane = threadIdx.x & 63, k = g.top_k, slot = (int)blockIdx.y;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int chunks = mx4_chunks(g.D), blocks = mx4_blocks(g.D);
+  if (wave < g.T) choose(g, wave, lane, ids, ws);
+  __syncthreads();
+  if (blockIdx.x == 0 && slot == 0) {
+    for (int i = threadIdx.x; i < g.T * k; i += 64 * kMoeWaves) o.ids[i] = ids[i], o.w[i] = ws[i];
+    for (int i = threadIdx.x; i < strips_y; i += 64 * kMoeWaves) o.done[i] = 0;
+  }
+  int e = slot;
+  if (pairs) {
+    e = __builtin_amdgcn_readfirstlane(ids[slot]);
+    bool before = e < 0;
+    for (int p = lane; p < slot; p += 64) before |= ids[p] == e;
+    if (__ballot(before) != 0) return;
+  }
+  int place = -1;
+  float wt = 0.f;
+  if (lane < g.T)
+    for (int j = 0; j < k; ++j) {
+      const bool same = ids[lane * k + j] == e;
+      place = same && place < 0 ? j : place;
+      wt += same ? ws[lane * k + j] : 0.f;
     }
+  if (__ballot(place >= 0) == 0) return;
+  const int strips = 2 * mx4_blocks(g.I), tile = per * (int)blockIdx.x, tiles = min(tile + per, strips);
+  const int64_t strip_bytes = mx4_strip_bytes(g.D), at = (int64_t)e * mx4_weight_bytes(g.I, g.D);
+  auto fetch = [&](MoeChunk (&w)[2], int t, int c) {
+    const bool ok = t < tiles && 16 * t < g.I && c < chunks;
+    const int64_t to = at + t * strip_bytes + (int64_t)kChunkBytes * c;
+    load_chunk(w[0], ok ? g.wg + to : nullptr, blocks - 16 * c, lane);
+    load_chunk(w[1], ok ? g.wu + to : nullptr, blocks - 16 * c, lane);
+  };
+  Values<XT, XP> rows(g, lane, lds.rows[wave]);
+  sweep<XP, 1>(rows, g.T, wave, tile, tiles, chunks, lds.rows[wave], lane, fetch, [&](int t, const f32x4_t (&acc)[1][2]) {
+    meet<1>(lds, acc, 0, wave, lane);
+    // thread: column % 16 of token / 16; its lane in the wave's first lanes knows the token's place
+    const int r = threadIdx.x / 16;
+    const int at_r = __shfl(place, r & 63, 64);
+    const float w_r = __shfl(wt, r & 63, 64);
+    if (r < g.T && at_r >= 0) put_hidden<XP, HP>(g, o, lds, r, t, r, at_r, w_r, Ip);
   });
 }
 
@@ -442,29 +566,27 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
       tok[r] = lane, place[r] = m.place;
     }
     __syncthreads();
-    buf_t hb[HP];
-    part_buffers<HP>(hb, o.h, g.T * k, Ip);
     constexpr int RG = kRowGroup<HP>;
-    for (int r0 = 0; r0 < members; r0 += G * RG)
-    sweep<HP, G>(hb, r0 + lane < members ? 2 * (tok[r0 + lane] * k + place[r0 + lane]) * Ip : 0, members - r0, wave, tile, tiles,
-                 chunks, blocks, lds.rows[wave], lane, fetch, [&](int t, const f32x4_t (&acc)[G][2]) {
+    static_assert(RG <= 8, "rows that the workgroup's threads take at once");
+    for (int r0 = 0; r0 < members; r0 += G * RG) {
+      Parts<HP> rows;
+      part_buffers<HP>(rows.parts, o.h, g.T * k, Ip);
+      rows.offs = r0 + lane < members ? 2 * (tok[r0 + lane] * k + place[r0 + lane]) * Ip : 0;
+      rows.members = members - r0, rows.blocks = blocks, rows.lane = lane, rows.lds = lds.rows[wave];
+      sweep<HP, G>(rows, members - r0, wave, tile, tiles, chunks, lds.rows[wave], lane, fetch, [&](int t, const f32x4_t (&acc)[G][2]) {
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        if (r0 + RG * i >= members) break;
-        meet<G>(lds, acc, i, wave, lane);
-        // (8 rows at once: RG is at most that)
-        {
+        for (int i = 0; i < G; ++i) {
+          if (r0 + RG * i >= members) break;
+          meet<G>(lds, acc, i, wave, lane);
           const int rr = threadIdx.x / 32, r = r0 + RG * i + rr, col = threadIdx.x % 32;
           if (rr >= RG || r >= members) continue;
-          float v = 0.f;
-#pragma unroll
-          for (int q = 0; q < kMoeWaves; ++q) v += lds.sums[q][col / 16][rr][col % 16];
+          const float v = met<HP>(lds, col / 16, rr, col % 16);
           // past this XCD's L2: another XCD's workgroup may read it
           __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), zb,
-                                                4 * ((tok[r] * k + place[r]) * Dz + 32 * t + col), 0, kCoherent);
+                                                4 * ((tok[r] * k + place[r]) * Dz + 32 * t + col), 0, JOIN ? kCoherent : 0);
         }
-      }
-    });
+      });
+    }
   }
   if (!JOIN) return;
   // every wave's rows are in memory before the workgroup counts as arrived
@@ -485,6 +607,110 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
       yt[(int64_t)t * g.ldy + n] = (Y)v;
     });
   }
+}
+
+// The same for up to 4 tokens and 64 choices whose h fits LDS: a workgroup has 16 columns of y whole, its 16 waves taking
+// chunks of all chosen experts in turn; nothing is left to add across workgroups.
+constexpr int kFewWaves = 16, kFewLds = 120 << 10;
+
+template <int HP>
+__global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g, MoeBufs o, int Ip) {
+  __shared__ __align__(16) char hs[kFewLds];  // h's rows, of each its parts, 16 bytes apart
+  __shared__ float sums[kFewWaves][16][17];
+  const int lane = threadIdx.x & 63, k = g.top_k, places = g.T * k;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  static_assert(HP <= 4, "a row's parts are rows of the product");
+  const int l16 = lane & 15, quad = lane >> 4, strip = (int)blockIdx.x;
+  const int chunks = mx4_chunks(g.I), blocks = mx4_blocks(g.I), row_bytes = 2 * Ip + 16;
+  const int id = lane < places ? o.ids[lane] : -1;
+  // h to LDS, a chunk of a row's part a turn
+  constexpr int HELD = 4;
+  const int turns = places * HP * chunks;
+  u32x4_t v[HELD];
+  auto get = [&](int t) {
+    const int r = t / chunks, q = r / places, c = t - r * chunks;  // r: part q's row r - q places
+    return *reinterpret_cast<const u32x4_t*>(o.h + ((int64_t)q * places + (r - q * places)) * Ip + 512 * c + 8 * lane);
+  };
+  auto put = [&](int t, const u32x4_t& x) {
+    const int r = t / chunks, c = t - r * chunks;
+    *reinterpret_cast<u32x4_t*>(hs + r * row_bytes + 1024 * c + 16 * lane) = x;
+  };
+  int t = wave;
+#pragma unroll
+  for (int i = 0; i < HELD; ++i)
+    if (t + i * kFewWaves < turns) v[i] = get(t + i * kFewWaves);
+  __builtin_amdgcn_sched_barrier(0);
+  // the places whose expert no earlier one has
+  bool first = id >= 0;
+  for (int p = 0; p + 1 < places; ++p) first = first && !(p < lane && __builtin_amdgcn_readlane(id, p) == id);
+  const uint64_t firsts = __ballot(first);
+  const int rank = __popcll(firsts & ((uint64_t(1) << lane) - 1)), items = __popcll(firsts) * chunks;
+  auto expert = [&](int n) {
+    const uint64_t m = __ballot(first && rank == n / chunks);
+    return __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(m | (uint64_t(1) << 63)));
+  };
+  auto request = [&](MoeChunk& w, int n) {
+    const uint8_t* p = nullptr;
+    int nb = 0;
+    if (n < items) {
+      const int c = n % chunks;
+      p = g.wd + (int64_t)expert(n) * mx4_weight_bytes(g.D, g.I) + (int64_t)strip * mx4_strip_bytes(g.I) + (int64_t)kChunkBytes * c;
+      nb = blocks - 16 * c;
+    }
+    load_chunk(w, p, nb, lane);
+  };
+  MoeChunk w[2];
+  request(w[0], wave);
+  request(w[1], wave + kFewWaves);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < HELD; ++i)
+    if (t + i * kFewWaves < turns) put(t + i * kFewWaves, v[i]);
+  for (t += HELD * kFewWaves; t < turns; t += kFewWaves) put(t, get(t));
+  __syncthreads();
+
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  auto use = [&](const MoeChunk& m, int n) {
+    const int c = n % chunks, e = expert(n);
+    // row l16 is part l16 / 4 of token l16 % 4, its first place with this expert
+    const uint64_t same = __ballot(id == e);
+    const int token = l16 % 4, part = l16 / 4;
+    const uint32_t own = token < g.T && part < HP ? (uint32_t)(same >> (token * k)) & (uint32_t)((uint64_t(1) << k) - 1) : 0u;
+    const char* from = own == 0 ? hs : hs + (part * places + token * k + __builtin_ctz(own)) * row_bytes + 1024 * c + 16 * quad;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool ok = own != 0 && 4 * quad + j < blocks - 16 * c;
+      const float sc = scale_f32((m.s >> (8 * j)) & 255);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bf16x8_t b = __builtin_bit_cast(bf16x8_t, bf16_of_codes(m.c[j][i], sc));
+        u32x4_t a = *reinterpret_cast<const u32x4_t*>(from + (ok ? 256 * j + 64 * i : 0));
+        if (!ok) a = u32x4_t{0u, 0u, 0u, 0u};
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), b, acc, 0, 0, 0);
+      }
+    }
+  };
+  for (int n = wave; n < items; n += 2 * kFewWaves) {
+    use(w[0], n);
+    request(w[0], n + 2 * kFewWaves);
+    if (n + kFewWaves >= items) break;
+    use(w[1], n + kFewWaves);
+    request(w[1], n + 3 * kFewWaves);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) sums[wave][4 * quad + r][l16] = acc[r];
+  __syncthreads();
+  const int m = threadIdx.x / 16, n = 16 * strip + (int)threadIdx.x % 16;
+  if (m >= g.T || n >= g.D) return;
+  float y = 0.f;
+#pragma unroll
+  for (int i = HP; i-- > 0;)
+#pragma unroll
+    for (int q = 0; q < kFewWaves; ++q) y += sums[q][4 * i + m][threadIdx.x % 16];
+  with_y(g.y, g.y_dtype, [&](auto* yt) {
+    typedef typename std::remove_pointer<decltype(yt)>::type Y;
+    yt[(int64_t)m * g.ldy + n] = (Y)y;
+  });
 }
 
 // The same sums by a launch of its own, a workgroup for 256 columns of a token.
@@ -530,20 +756,29 @@ template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePla
   auto each = [&](int tiles) { return (int)(((int64_t)tiles * slots + 1535) / 1536); };
   const int up = 2 * mx4_blocks(a.I), down = p.Dz / 32, per_up = each(up), per_down = each(down);
   const int xg = (a.T * (p.Dp / 8) + 255) / 256, gd = (down + per_down - 1) / per_down;
+  hipError_t e = hipSuccess;
+  if (a.T <= 4 && vec8_ok(a.x, a.ldx, a.D, a.x_dtype == YF32 ? 4 : 2) && a.D % 8 == 0) {
+    constexpr int XT = XP == 1 ? XBF16 : XP == 2 ? XF16 : YF32;
+    e = launch_kernel(moe_up_few_kernel<XT, XP, HP>, dim3((unsigned)((up + per_up - 1) / per_up), (unsigned)slots),
+                      dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs, per_up, gd);
+  } else {
+    e = launch_kernel(moe_route_kernel<XP>, dim3((unsigned)((a.T + 3) / 4 + (xg < 256 ? xg : 256))), dim3(256), s, a, o, gd, p.Dp);
+    if (e != hipSuccess) return e;
+    e = launch_kernel(a.T <= kRowGroup<XP> ? moe_up_kernel<XP, HP, 1> : moe_up_kernel<XP, HP, 2>,
+                      dim3((unsigned)((up + per_up - 1) / per_up), (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Dp, p.Ip,
+                      pairs, per_up);
+  }
+  if (e != hipSuccess) return e;
+  const int places = a.T * a.top_k;
+  if (a.T <= 4 && places <= 64 && (int64_t)places * HP * (2 * p.Ip + 16) <= kFewLds)
+    return launch_kernel(moe_down_few_kernel<HP>, dim3((unsigned)((a.D + 15) / 16)), dim3(64 * kFewWaves), s, a, o, p.Ip);
   const bool join = a.T <= 16;
-  hipError_t e = launch_kernel(moe_route_kernel<XP>, dim3((unsigned)((a.T + 3) / 4 + (xg < 256 ? xg : 256))), dim3(256), s, a, o,
-                               gd, p.Dp);
-  if (e != hipSuccess) return e;
-  e = launch_kernel(a.T <= kRowGroup<XP> ? moe_up_kernel<XP, HP, 1> : moe_up_kernel<XP, HP, 2>,
-                    dim3((unsigned)((up + per_up - 1) / per_up), (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Dp, p.Ip, pairs,
-                    per_up);
-  if (e != hipSuccess) return e;
   e = launch_kernel(!join ? moe_down_kernel<HP, 2, false>
                           : a.T <= kRowGroup<HP> ? moe_down_kernel<HP, 1, true> : moe_down_kernel<HP, 2, true>,
                     dim3((unsigned)gd, (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs, p.Dz, per_down);
   if (e != hipSuccess || join) return e;
-  const int blocks = (a.D + 255) / 256;
-  return launch_kernel(moe_join_kernel, dim3((unsigned)(a.T * blocks)), dim3(256), s, a, o, p.Dz, blocks);
+  const int columns = (a.D + 255) / 256;
+  return launch_kernel(moe_join_kernel, dim3((unsigned)(a.T * columns)), dim3(256), s, a, o, p.Dz, columns);
 }
 
 template <int XP> static hipError_t moe_h(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
