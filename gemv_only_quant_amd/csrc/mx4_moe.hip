@@ -329,7 +329,6 @@ __device__ __forceinline__ void sweep(Source& rows, int members, int wave, int t
   fetch(w, tile, wave);
   // rows that fit LDS at once and serve every tile stay there
   const bool stay = members <= RG && chunks <= kMoeWaves;
-  if (wave < chunks) rows.request(0, wave);
   bool staged = false;
   for (; tile < tiles; ++tile) {
     f32x4_t acc[G][2];
@@ -444,6 +443,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs g, Mo
     part_buffers<XP>(rows.parts, o.x, g.T, Dp);
     rows.offs = r0 + lane < members ? 2 * tok[r0 + lane] * Dp : 0;
     rows.members = members - r0, rows.blocks = blocks, rows.lane = lane, rows.lds = lds.rows[wave];
+    if (wave < chunks) rows.request(0, wave);
     sweep<XP, G>(rows, members - r0, wave, tile, tiles, chunks, lds.rows[wave], lane, fetch, [&](int t, const f32x4_t (&acc)[G][2]) {
 #pragma unroll
       for (int i = 0; i < G; ++i) {
@@ -466,28 +466,22 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_few_kernel(MoeArgs g
   const int lane = threadIdx.x & 63, k = g.top_k, slot = (int)blockIdx.y;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int chunks = mx4_chunks(g.D), blocks = mx4_blocks(g.D);
+  Values<XT, XP> rows(g, lane, lds.rows[wave]);
+  if (wave < chunks) rows.request(0, wave);
   if (wave < g.T) choose(g, wave, lane, ids, ws);
   __syncthreads();
+  const int places = g.T * k;
   if (blockIdx.x == 0 && slot == 0) {
-    for (int i = threadIdx.x; i < g.T * k; i += 64 * kMoeWaves) o.ids[i] = ids[i], o.w[i] = ws[i];
+    for (int i = threadIdx.x; i < places; i += 64 * kMoeWaves) o.ids[i] = ids[i], o.w[i] = ws[i];
     for (int i = threadIdx.x; i < strips_y; i += 64 * kMoeWaves) o.done[i] = 0;
   }
-  int e = slot;
-  if (pairs) {
-    e = __builtin_amdgcn_readfirstlane(ids[slot]);
-    bool before = e < 0;
-    for (int p = lane; p < slot; p += 64) before |= ids[p] == e;
-    if (__ballot(before) != 0) return;
-  }
-  int place = -1;
-  float wt = 0.f;
-  if (lane < g.T)
-    for (int j = 0; j < k; ++j) {
-      const bool same = ids[lane * k + j] == e;
-      place = same && place < 0 ? j : place;
-      wt += same ? ws[lane * k + j] : 0.f;
-    }
-  if (__ballot(place >= 0) == 0) return;
+  // the places with this workgroup's expert, a bit each
+  const int e = pairs ? __builtin_amdgcn_readfirstlane(ids[slot]) : slot;
+  const uint64_t same[2] = {__ballot(lane < places && ids[lane] == e), __ballot(64 + lane < places && ids[64 + lane] == e)};
+  if (e < 0 || (same[0] | same[1]) == 0) return;
+  const uint64_t below = slot < 64 ? same[0] & ((uint64_t(1) << slot) - 1)
+                                   : same[0] | (same[1] & ((uint64_t(1) << (slot - 64)) - 1));
+  if (pairs && below != 0) return;
   const int strips = 2 * mx4_blocks(g.I), tile = per * (int)blockIdx.x, tiles = min(tile + per, strips);
   const int64_t strip_bytes = mx4_strip_bytes(g.D), at = (int64_t)e * mx4_weight_bytes(g.I, g.D);
   auto fetch = [&](MoeChunk (&w)[2], int t, int c) {
@@ -496,14 +490,17 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_few_kernel(MoeArgs g
     load_chunk(w[0], ok ? g.wg + to : nullptr, blocks - 16 * c, lane);
     load_chunk(w[1], ok ? g.wu + to : nullptr, blocks - 16 * c, lane);
   };
-  Values<XT, XP> rows(g, lane, lds.rows[wave]);
   sweep<XP, 1>(rows, g.T, wave, tile, tiles, chunks, lds.rows[wave], lane, fetch, [&](int t, const f32x4_t (&acc)[1][2]) {
     meet<1>(lds, acc, 0, wave, lane);
-    // thread: column % 16 of token / 16; its lane in the wave's first lanes knows the token's place
-    const int r = threadIdx.x / 16;
-    const int at_r = __shfl(place, r & 63, 64);
-    const float w_r = __shfl(wt, r & 63, 64);
-    if (r < g.T && at_r >= 0) put_hidden<XP, HP>(g, o, lds, r, t, r, at_r, w_r, Ip);
+    const int r = threadIdx.x / 16, p = r * k;
+    if (r >= g.T) return;
+    uint64_t own = p >= 64 ? same[1] >> (p - 64) : p == 0 ? same[0] : same[0] >> p | same[1] << (64 - p);
+    own &= (uint64_t(1) << k) - 1;
+    if (own == 0) return;
+    const int place = (int)__builtin_ctzll(own);
+    float wt = 0.f;
+    for (; own != 0; own &= own - 1) wt += ws[p + (int)__builtin_ctzll(own)];
+    put_hidden<XP, HP>(g, o, lds, r, t, r, place, wt, Ip);
   });
 }
 
@@ -573,6 +570,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
       part_buffers<HP>(rows.parts, o.h, g.T * k, Ip);
       rows.offs = r0 + lane < members ? 2 * (tok[r0 + lane] * k + place[r0 + lane]) * Ip : 0;
       rows.members = members - r0, rows.blocks = blocks, rows.lane = lane, rows.lds = lds.rows[wave];
+      if (wave < chunks) rows.request(0, wave);
       sweep<HP, G>(rows, members - r0, wave, tile, tiles, chunks, lds.rows[wave], lane, fetch, [&](int t, const f32x4_t (&acc)[G][2]) {
 #pragma unroll
         for (int i = 0; i < G; ++i) {
