@@ -393,6 +393,114 @@ template <int P> __device__ __forceinline__ float met(const MoeLds& lds, int p, 
   return v;
 }
 
+// Where an expert's rows fit LDS whole and there are tiles enough, a wave has whole tiles instead: nothing is left to
+// add across waves, and no barrier stands between a wave and its next weights.
+constexpr int kHeldWaves = 12, kHeldBytes = 32 * (4096 + 16);
+template <int P> constexpr int kHeldRows = P == 1 ? 16 : P == 2 ? 8 : 4;  // a product's rows, of each its P parts
+
+struct HeldLds {
+  char rows[kHeldBytes];
+  int row[kMoeTokens];    // of members: token top_k + place
+  int tok[kMoeTokens];
+  float wt[kMoeTokens];
+};
+
+// `rows` rows of bf16 parts in operand order to LDS, a chunk a turn; first() is called when the first ones are requested.
+template <int P, class Offset, class First>
+__device__ __forceinline__ void hold_rows(HeldLds& lds, const buf_t (&parts)[P], int rows, int ld, int chunks, int blocks, int wave,
+                                          int lane, Offset&& offset, First&& first) {
+  constexpr int RG = kHeldRows<P>, AHEAD = 4;
+  const int turns = rows * P * chunks;
+  u32x4_t v[AHEAD];
+  auto get = [&](int t) {
+    const int m = t / (P * chunks), q = (t / chunks) % P, c = t % chunks;
+    const bool ok = t < turns && 4 * (lane & 3) + (lane >> 4) < blocks - 16 * c;
+    u32x4_t x = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (i == q) x = __builtin_amdgcn_raw_buffer_load_b128(parts[i], ok ? 1024 * c + 16 * lane : kNowhere, t < turns ? offset(m) : 0, 0);
+    return x;
+  };
+  auto put = [&](int t, const u32x4_t& x) {
+    const int m = t / (P * chunks), q = (t / chunks) % P, c = t % chunks;
+    if (t < turns) *reinterpret_cast<u32x4_t*>(lds.rows + (16 * (m / RG) + RG * q + m % RG) * ld + 1024 * c + 16 * lane) = x;
+  };
+  for (int t = wave; t == wave || t < turns; t += AHEAD * kHeldWaves) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) v[i] = get(t + i * kHeldWaves);
+    if (t == wave) first();
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) put(t + i * kHeldWaves, v[i]);
+  }
+  __syncthreads();
+}
+
+// The tiles tile, tile + 16 .. of a wave, their weights in two sets of registers in turn; put(tile, sums of rows).
+template <int P, int G> struct HeldSweep {
+  MoeChunk w[2][2];
+  int t, c, tn, cn;  // the unit whose weights come first, and the one requested last
+  template <class Fetch> __device__ __forceinline__ void begin(int tile, int tiles, int chunks, Fetch&& fetch) {
+    t = tn = tile, c = cn = 0;
+    fetch(w[0], tn, cn);
+    after(tn, cn, chunks);
+    fetch(w[1], tn, cn);
+  }
+  static __device__ __forceinline__ void after(int& t, int& c, int chunks) {
+    if (++c == chunks) c = 0, t += kHeldWaves;
+  }
+  template <class Fetch, class Put>
+  __device__ __forceinline__ void run(const char* rows, int ld, int groups, int tiles, int chunks, int lane, Fetch&& fetch, Put&& put) {
+    f32x4_t acc[G][2] = {};
+    const char* from0 = rows + (lane & 15) * ld + 16 * (lane >> 4);
+    auto use = [&](const MoeChunk (&m)[2]) {
+      const char* from = from0 + 1024 * c;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float s0 = scale_f32((m[0].s >> (8 * j)) & 255), s1 = scale_f32((m[1].s >> (8 * j)) & 255);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bf16x8_t b0 = __builtin_bit_cast(bf16x8_t, bf16_of_codes(m[0].c[j][i], s0));
+          const bf16x8_t b1 = __builtin_bit_cast(bf16x8_t, bf16_of_codes(m[1].c[j][i], s1));
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            if (g > 0 && g >= groups) break;
+            const bf16x8_t a = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t*>(from + 16 * g * ld + 256 * j + 64 * i));
+            acc[g][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b0, acc[g][0], 0, 0, 0);
+            acc[g][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b1, acc[g][1], 0, 0, 0);
+          }
+        }
+      }
+      if (c == chunks - 1) {
+        // a row's parts lie in different lanes of a column
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float v = acc[g][p][r];
+              if (P == 2) acc[g][p][r] = v + __shfl_xor(v, 32, 64);
+              if (P == 3) acc[g][p][r] = v + (__shfl(v, (lane & 15) + 16, 64) + __shfl(v, (lane & 15) + 32, 64));
+            }
+        }
+        put(t, acc);
+#pragma unroll
+        for (int g = 0; g < G; ++g) acc[g][0] = acc[g][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+      after(t, c, chunks);
+    };
+    while (t < tiles) {
+      use(w[0]);
+      after(tn, cn, chunks);
+      fetch(w[0], tn, cn);
+      if (t >= tiles) break;
+      use(w[1]);
+      after(tn, cn, chunks);
+      fetch(w[1], tn, cn);
+    }
+  }
+};
+
 // ---- first half ----------------------------------------------------------------
 // Column threadIdx.x % 16 of strip t of h, from the waves' sums of row rr, for `place` of token `tok`.
 template <int XP, int HP>
@@ -452,6 +560,60 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs g, Mo
         const int rr = threadIdx.x / 16, r = r0 + RG * i + rr;
         if (rr < RG && r < members) put_hidden<XP, HP>(g, o, lds, rr, t, tok[r], place[r], wt[r], Ip);
       }
+    });
+  }
+}
+
+template <int XP, int HP, int G>
+__global__ __launch_bounds__(64 * kHeldWaves) void moe_up_held_kernel(MoeArgs g, MoeBufs o, int Dp, int Ip, int pairs, int per) {
+  __shared__ HeldLds lds;
+  constexpr int RG = kHeldRows<XP>;
+  const int lane = threadIdx.x & 63, quad = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const MoeGroup m = group_of(o, (int)blockIdx.y, pairs != 0, g.T, g.top_k, lane);
+  if (m.e < 0) return;
+  const int chunks = mx4_chunks(g.D), blocks = mx4_blocks(g.D), members = __popcll(m.who), ld = 2 * Dp + 16;
+  const int strips = 2 * mx4_blocks(g.I);  // h's columns are padded to whole blocks, with zeros
+  const int tile = per * (int)blockIdx.x, tiles = min(tile + per, strips);
+  const int64_t strip_bytes = mx4_strip_bytes(g.D), at = (int64_t)m.e * mx4_weight_bytes(g.I, g.D);
+  auto fetch = [&](MoeChunk (&w)[2], int t, int c) {
+    const bool ok = t < tiles && 16 * t < g.I;
+    const int64_t to = at + t * strip_bytes + (int64_t)kChunkBytes * c;
+    load_chunk(w[0], ok ? g.wg + to : nullptr, blocks - 16 * c, lane);
+    load_chunk(w[1], ok ? g.wu + to : nullptr, blocks - 16 * c, lane);
+  };
+  if (wave == 0 && m.place >= 0) {
+    const int r = __popcll(m.who & ((uint64_t(1) << lane) - 1));
+    lds.tok[r] = lane, lds.row[r] = lane * g.top_k + m.place, lds.wt[r] = m.w;
+  }
+  __syncthreads();
+  buf_t parts[XP];
+  part_buffers<XP>(parts, o.x, g.T, Dp);
+  HeldSweep<XP, G> sweep;
+  for (int r0 = 0; r0 < members; r0 += G * RG) {
+    if (r0 > 0) __syncthreads();
+    const int rows = min(members - r0, G * RG), groups = (rows + RG - 1) / RG;
+    hold_rows<XP>(lds, parts, rows, ld, chunks, blocks, wave, lane,
+                  [&](int r) { return 2 * Dp * __builtin_amdgcn_readfirstlane(lds.tok[r0 + r]); },
+                  [&] { sweep.begin(tile + wave, tiles, chunks, fetch); });
+    sweep.run(lds.rows, ld, groups, tiles, chunks, lane, fetch, [&](int t, const f32x4_t (&acc)[G][2]) {
+      const int n = 16 * t + l16;
+#pragma unroll
+      for (int i = 0; i < G; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int rr = 4 * quad + q, r = RG * i + rr;
+          if (rr >= RG || r >= rows) continue;
+          float h = 0.f;
+          with_act(g.act, [&](auto a) {
+            float d;
+            h = act_parts<decltype(a)::value>(acc[i][0][q], &d) * acc[i][1][q] * lds.wt[r0 + r];
+          });
+          uint16_t p[HP];
+          parts_of<HP>(n < g.I ? h : 0.f, p);  // the padding is 0 whatever x is
+#pragma unroll
+          for (int b = 0; b < HP; ++b) o.h[((int64_t)b * g.T * g.top_k + lds.row[r0 + r]) * Ip + operand_order(n)] = p[b];
+        }
     });
   }
 }
@@ -607,6 +769,51 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
   }
 }
 
+template <int HP, int G>
+__global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int Dz, int per) {
+  __shared__ HeldLds lds;
+  constexpr int RG = kHeldRows<HP>;
+  const int lane = threadIdx.x & 63, quad = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const MoeGroup m = group_of(o, (int)blockIdx.y, pairs != 0, g.T, g.top_k, lane);
+  if (m.e < 0) return;
+  const int chunks = mx4_chunks(g.I), blocks = mx4_blocks(g.I), members = __popcll(m.who), ld = 2 * Ip + 16;
+  const int tile = per * (int)blockIdx.x, tiles = min(tile + per, Dz / 32);
+  const int64_t strip_bytes = mx4_strip_bytes(g.I), at = (int64_t)m.e * mx4_weight_bytes(g.D, g.I);
+  auto fetch = [&](MoeChunk (&w)[2], int t, int c) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      load_chunk(w[i], t < tiles && 32 * t + 16 * i < g.D ? g.wd + at + (2 * t + i) * strip_bytes + (int64_t)kChunkBytes * c : nullptr,
+                 blocks - 16 * c, lane);
+  };
+  if (wave == 0 && m.place >= 0) {
+    const int r = __popcll(m.who & ((uint64_t(1) << lane) - 1));
+    lds.row[r] = lane * g.top_k + m.place;
+  }
+  __syncthreads();
+  buf_t parts[HP];
+  part_buffers<HP>(parts, o.h, g.T * g.top_k, Ip);
+  HeldSweep<HP, G> sweep;
+  for (int r0 = 0; r0 < members; r0 += G * RG) {
+    if (r0 > 0) __syncthreads();
+    const int rows = min(members - r0, G * RG), groups = (rows + RG - 1) / RG;
+    hold_rows<HP>(lds, parts, rows, ld, chunks, blocks, wave, lane,
+                  [&](int r) { return 2 * Ip * __builtin_amdgcn_readfirstlane(lds.row[r0 + r]); },
+                  [&] { sweep.begin(tile + wave, tiles, chunks, fetch); });
+    sweep.run(lds.rows, ld, groups, tiles, chunks, lane, fetch, [&](int t, const f32x4_t (&acc)[G][2]) {
+#pragma unroll
+      for (int i = 0; i < G; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int rr = 4 * quad + q, r = RG * i + rr;
+          if (rr >= RG || r >= rows) continue;
+          float* z = o.z + (int64_t)lds.row[r0 + r] * Dz + 32 * t + l16;
+          z[0] = acc[i][0][q], z[16] = acc[i][1][q];
+        }
+    });
+  }
+}
+
 // The same for up to 4 tokens and 64 choices whose h fits LDS: a workgroup has 16 columns of y whole, its 16 waves taking
 // chunks of all chosen experts in turn; nothing is left to add across workgroups.
 constexpr int kFewWaves = 16, kFewLds = 120 << 10;
@@ -747,6 +954,16 @@ MoePlan plan_moe(int T, int D, int I, int top_k, int x_dtype, int y_dtype) {
   return p;
 }
 
+// Groups of rows that a workgroup holds in LDS, 0: none.
+static int held_groups(bool more, int Kp, int tiles, int slots) {
+  const int groups = more ? 2 : 1;
+  return groups * 16 * (2 * Kp + 16) <= kHeldBytes && (int64_t)tiles * slots >= 256 * kHeldWaves ? groups : 0;
+}
+static int held_each(int tiles, int slots) {
+  const int wgs = slots < 256 ? 256 / slots : 1;
+  return (tiles + wgs - 1) / wgs;
+}
+
 template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
   // a workgroup for each expert, or for each place of the tokens' choices if these are fewer; of more tiles than
   // about 3 rounds of workgroups (2 on a CU) would be, a workgroup takes several in turn
@@ -762,15 +979,32 @@ template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePla
   } else {
     e = launch_kernel(moe_route_kernel<XP>, dim3((unsigned)((a.T + 3) / 4 + (xg < 256 ? xg : 256))), dim3(256), s, a, o, gd, p.Dp);
     if (e != hipSuccess) return e;
-    e = launch_kernel(a.T <= kRowGroup<XP> ? moe_up_kernel<XP, HP, 1> : moe_up_kernel<XP, HP, 2>,
-                      dim3((unsigned)((up + per_up - 1) / per_up), (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Dp, p.Ip,
-                      pairs, per_up);
+    const int held = held_groups(a.T > kHeldRows<XP>, p.Dp, up, slots);
+    if (held != 0) {
+      const int per = held_each(up, slots);
+      e = launch_kernel(held == 1 ? moe_up_held_kernel<XP, HP, 1> : moe_up_held_kernel<XP, HP, 2>,
+                        dim3((unsigned)((up + per - 1) / per), (unsigned)slots), dim3(64 * kHeldWaves), s, a, o, p.Dp, p.Ip,
+                        pairs, per);
+    } else {
+      e = launch_kernel(a.T <= kRowGroup<XP> ? moe_up_kernel<XP, HP, 1> : moe_up_kernel<XP, HP, 2>,
+                        dim3((unsigned)((up + per_up - 1) / per_up), (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Dp, p.Ip,
+                        pairs, per_up);
+    }
   }
   if (e != hipSuccess) return e;
   const int places = a.T * a.top_k;
   if (a.T <= 4 && places <= 64 && (int64_t)places * HP * (2 * p.Ip + 16) <= kFewLds)
     return launch_kernel(moe_down_few_kernel<HP>, dim3((unsigned)((a.D + 15) / 16)), dim3(64 * kFewWaves), s, a, o, p.Ip);
   const bool join = a.T <= 16;
+  const int held = join ? 0 : held_groups(true, p.Ip, down, slots);
+  if (held != 0) {
+    const int per = held_each(down, slots);
+    e = launch_kernel(moe_down_held_kernel<HP, 2>, dim3((unsigned)((down + per - 1) / per), (unsigned)slots), dim3(64 * kHeldWaves),
+                      s, a, o, p.Ip, pairs, p.Dz, per);
+    if (e != hipSuccess) return e;
+    const int columns = (a.D + 255) / 256;
+    return launch_kernel(moe_join_kernel, dim3((unsigned)(a.T * columns)), dim3(256), s, a, o, p.Dz, columns);
+  }
   e = launch_kernel(!join ? moe_down_kernel<HP, 2, false>
                           : a.T <= kRowGroup<HP> ? moe_down_kernel<HP, 1, true> : moe_down_kernel<HP, 2, true>,
                     dim3((unsigned)gd, (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs, p.Dz, per_down);

@@ -287,6 +287,46 @@ def test_moe(T, D, I, E, k, x, out, act, norm):
     m4.assert_close(y, ref, bound, f"moe {T} {D} {I} {E} {k}")
 
 
+# tiles enough for workgroups that hold an expert's rows: in the first half, the second, both; more of an expert's
+# tokens than are held at once; a place for each workgroup
+MANY = [(17, 600, 784, 64, 4), (24, 1600, 200, 64, 3), (64, 1570, 800, 66, 2), (40, 1540, 790, 64, 32), (12, 4000, 784, 64, 2),
+        (3, 4001, 784, 64, 2), (6, 300, 1100, 60, 8)]
+
+
+@pytest.mark.parametrize("T,D,I,E,k", MANY)
+@pytest.mark.parametrize("x,out", [("bf16", "fp16"), ("fp16", "fp32"), ("fp32", "bf16"), ("fp32", "fp32")])
+def test_moe_of_many_tiles(T, D, I, E, k, x, out):
+    packed, values = experts(E, D, I, T + D)
+    v = m4.tokens(T, D, seed=I, dtype=TYPES[x])
+    lg = torch.randn((T, E), generator=torch.Generator().manual_seed(k)) * 2
+    y = qmm.mx4_moe(v.cuda(), *packed, I, logits=lg.cuda(), top_k=k, out_dtype=TYPES[out])
+    ref, bound = m4.moe_ref("silu", v, *values, *m4.route_ref(lg, k, True), TYPES[out])
+    m4.assert_close(y, ref, bound, f"moe {T} {D} {I} {E} {k}")
+
+
+# up to 4 tokens: rows of whole 16 bytes and others, h that fits a workgroup's LDS and one that does not, more than 64 places
+FEW = [(1, 8, 40, 4, 4), (2, 520, 520, 9, 3), (3, 1032, 77, 128, 8), (4, 2064, 300, 16, 16), (4, 72, 96, 40, 17), (4, 40, 2600, 20, 5),
+       (4, 64, 96, 300, 32), (1, 512, 8200, 2, 2), (2, 4104, 64, 3, 1)]
+
+
+@pytest.mark.parametrize("T,D,I,E,k", FEW)
+@pytest.mark.parametrize("x,out,norm", [("bf16", "bf16", True), ("fp16", "fp32", True), ("fp32", "fp16", False), ("fp32", "fp32", True)])
+def test_moe_few_tokens(T, D, I, E, k, x, out, norm):
+    packed, values = experts(E, D, I, T + D)
+    v = m4.tokens(T, D, seed=I, dtype=TYPES[x])
+    lg = torch.randn((T, E), generator=torch.Generator().manual_seed(k)) * 2
+    y = qmm.mx4_moe(v.cuda(), *packed, I, logits=lg.cuda(), top_k=k, renormalize=norm, out_dtype=TYPES[out])
+    ref, bound = m4.moe_ref("silu", v, *values, *m4.route_ref(lg, k, norm), TYPES[out])
+    m4.assert_close(y, ref, bound, f"moe {T} {D} {I} {E} {k}")
+    # experts given, the first of them twice
+    ids = torch.randint(0, E, (T, k), generator=torch.Generator().manual_seed(D), dtype=torch.int32)
+    ids[:, -1] = ids[:, 0]
+    w = torch.randn((T, k), generator=torch.Generator().manual_seed(I))
+    y = qmm.mx4_moe(v.cuda(), *packed, I, ids=ids.cuda(), weights=w.cuda(), out_dtype=TYPES[out])
+    ref, bound = m4.moe_ref("silu", v, *values, ids, w, TYPES[out])
+    m4.assert_close(y, ref, bound, f"given {T} {D} {I} {E} {k}")
+
+
 @pytest.mark.parametrize("T", [1, 4, 20, 64])
 @pytest.mark.parametrize("itype", [torch.int32, torch.int64])
 def test_moe_given_experts(T, itype):
