@@ -10,6 +10,8 @@
 // in the weights' shadow that costs nothing.  Rows of the product are an expert's tokens.
 //
 // Three launches: the tokens' choices, and x as parts; the first half; the second.
+#include <math.h>
+
 #include "mx4_device.h"
 
 namespace qmm {
@@ -954,14 +956,23 @@ MoePlan plan_moe(int T, int D, int I, int top_k, int x_dtype, int y_dtype) {
   return p;
 }
 
-// Groups of rows that a workgroup holds in LDS, 0: none.
-static int held_groups(bool more, int Kp, int tiles, int slots) {
-  const int groups = more ? 2 : 1;
-  return groups * 16 * (2 * Kp + 16) <= kHeldBytes && (int64_t)tiles * slots >= 256 * kHeldWaves ? groups : 0;
-}
-static int held_each(int tiles, int slots) {
-  const int wgs = slots < 256 ? 256 / slots : 1;
-  return (tiles + wgs - 1) / wgs;
+// Whether workgroups, one on each CU, hold an expert's rows, and of how many row groups: 0 not.  RG: tokens of a group;
+// Kp: values of a row.  Taken for what tokens that choose evenly would choose.
+struct HeldPlan {
+  int groups, per;  // per: tiles of a workgroup
+};
+static HeldPlan plan_held(const MoeArgs& a, int RG, int Kp, int tiles, int least) {
+  float none = 1.f;
+  for (int t = 0; t < a.T; ++t) none *= 1.f - (float)a.top_k / (float)a.E;
+  const float chosen = (float)a.E * (1.f - none), mean = (float)(a.T * a.top_k) / chosen;
+  const int bytes = 16 * (2 * Kp + 16);
+  HeldPlan p{};
+  if (a.T <= RG || mean + 2.f * sqrtf(mean) <= (float)RG) p.groups = bytes <= kHeldBytes;
+  if (a.T > RG && 2 * bytes <= kHeldBytes) p.groups = 2;
+  const int wgs = chosen < 256.f ? (int)(256.f / chosen) : 1;
+  p.per = (tiles + wgs - 1) / wgs;
+  if (p.per < least) p.groups = 0;
+  return p;
 }
 
 template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
@@ -979,12 +990,12 @@ template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePla
   } else {
     e = launch_kernel(moe_route_kernel<XP>, dim3((unsigned)((a.T + 3) / 4 + (xg < 256 ? xg : 256))), dim3(256), s, a, o, gd, p.Dp);
     if (e != hipSuccess) return e;
-    const int held = held_groups(a.T > kHeldRows<XP>, p.Dp, up, slots);
-    if (held != 0) {
-      const int per = held_each(up, slots);
-      e = launch_kernel(held == 1 ? moe_up_held_kernel<XP, HP, 1> : moe_up_held_kernel<XP, HP, 2>,
-                        dim3((unsigned)((up + per - 1) / per), (unsigned)slots), dim3(64 * kHeldWaves), s, a, o, p.Dp, p.Ip,
-                        pairs, per);
+    // (held in LDS or not, 18 tiles a workgroup: 45 and 39 us; 22 tiles: 41 and 48)
+    const HeldPlan held = plan_held(a, kHeldRows<XP>, p.Dp, up, 20);
+    if (held.groups != 0) {
+      e = launch_kernel(held.groups == 1 ? moe_up_held_kernel<XP, HP, 1> : moe_up_held_kernel<XP, HP, 2>,
+                        dim3((unsigned)((up + held.per - 1) / held.per), (unsigned)slots), dim3(64 * kHeldWaves), s, a, o, p.Dp,
+                        p.Ip, pairs, held.per);
     } else {
       e = launch_kernel(a.T <= kRowGroup<XP> ? moe_up_kernel<XP, HP, 1> : moe_up_kernel<XP, HP, 2>,
                         dim3((unsigned)((up + per_up - 1) / per_up), (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Dp, p.Ip,
@@ -995,19 +1006,17 @@ template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePla
   const int places = a.T * a.top_k;
   if (a.T <= 4 && places <= 64 && (int64_t)places * HP * (2 * p.Ip + 16) <= kFewLds)
     return launch_kernel(moe_down_few_kernel<HP>, dim3((unsigned)((a.D + 15) / 16)), dim3(64 * kFewWaves), s, a, o, p.Ip);
-  const bool join = a.T <= 16;
-  const int held = join ? 0 : held_groups(true, p.Ip, down, slots);
-  if (held != 0) {
-    const int per = held_each(down, slots);
-    e = launch_kernel(moe_down_held_kernel<HP, 2>, dim3((unsigned)((down + per - 1) / per), (unsigned)slots), dim3(64 * kHeldWaves),
-                      s, a, o, p.Ip, pairs, p.Dz, per);
-    if (e != hipSuccess) return e;
-    const int columns = (a.D + 255) / 256;
-    return launch_kernel(moe_join_kernel, dim3((unsigned)(a.T * columns)), dim3(256), s, a, o, p.Dz, columns);
-  }
-  e = launch_kernel(!join ? moe_down_kernel<HP, 2, false>
-                          : a.T <= kRowGroup<HP> ? moe_down_kernel<HP, 1, true> : moe_down_kernel<HP, 2, true>,
-                    dim3((unsigned)gd, (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs, p.Dz, per_down);
+  // (10 tiles a workgroup: 23 us and 5 of additions, else 23; 16 tiles: 27 and 5, else 36 and 5; 22 tiles: 28 and 5, else 49)
+  const HeldPlan held = plan_held(a, kHeldRows<HP>, p.Ip, down, 14);
+  const bool join = held.groups == 0 && a.T <= 16;
+  if (held.groups != 0)
+    e = launch_kernel(held.groups == 1 ? moe_down_held_kernel<HP, 1> : moe_down_held_kernel<HP, 2>,
+                      dim3((unsigned)((down + held.per - 1) / held.per), (unsigned)slots), dim3(64 * kHeldWaves), s, a, o, p.Ip,
+                      pairs, p.Dz, held.per);
+  else
+    e = launch_kernel(!join ? moe_down_kernel<HP, 2, false>
+                            : a.T <= kRowGroup<HP> ? moe_down_kernel<HP, 1, true> : moe_down_kernel<HP, 2, true>,
+                      dim3((unsigned)gd, (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs, p.Dz, per_down);
   if (e != hipSuccess || join) return e;
   const int columns = (a.D + 255) / 256;
   return launch_kernel(moe_join_kernel, dim3((unsigned)(a.T * columns)), dim3(256), s, a, o, p.Dz, columns);

@@ -287,21 +287,30 @@ def test_moe(T, D, I, E, k, x, out, act, norm):
     m4.assert_close(y, ref, bound, f"moe {T} {D} {I} {E} {k}")
 
 
-# tiles enough for workgroups that hold an expert's rows: in the first half, the second, both; more of an expert's
-# tokens than are held at once; a place for each workgroup
-MANY = [(17, 600, 784, 64, 4), (24, 1600, 200, 64, 3), (64, 1570, 800, 66, 2), (40, 1540, 790, 64, 32), (12, 4000, 784, 64, 2),
-        (3, 4001, 784, 64, 2), (6, 300, 1100, 60, 8)]
+# (T, D, I, E, top_k, n): tiles enough, of E experts' weights, for workgroups that hold an expert's rows: in the first half,
+# the second, both; n experts alone are chosen, so that more of one's tokens come than are held at once; a group of rows and two
+MANY = [(64, 130, 330, 300, 8, 60), (64, 460, 40, 300, 8, 60), (64, 460, 330, 260, 8, 9), (16, 460, 330, 256, 32, 33),
+        (8, 460, 330, 256, 32, 40), (4, 897, 650, 128, 32, 34), (64, 2100, 330, 260, 8, 16), (64, 460, 2100, 260, 8, 16),
+        (20, 4000, 330, 300, 32, 40)]
 
 
-@pytest.mark.parametrize("T,D,I,E,k", MANY)
+@pytest.mark.parametrize("T,D,I,E,k,n", MANY)
 @pytest.mark.parametrize("x,out", [("bf16", "fp16"), ("fp16", "fp32"), ("fp32", "bf16"), ("fp32", "fp32")])
-def test_moe_of_many_tiles(T, D, I, E, k, x, out):
-    packed, values = experts(E, D, I, T + D)
+def test_moe_of_many_tiles(T, D, I, E, k, n, x, out):
+    some, values = experts(n, D, I, T + D)
+    g = torch.Generator().manual_seed(k)
+    of = torch.sort(torch.randperm(E, generator=g)[:n]).values
+    packed = []
+    for w in some:
+        packed.append(torch.zeros((E,) + tuple(w.shape[1:]), dtype=torch.uint8, device="cuda"))
+        packed[-1][of.cuda()] = w
     v = m4.tokens(T, D, seed=I, dtype=TYPES[x])
-    lg = torch.randn((T, E), generator=torch.Generator().manual_seed(k)) * 2
-    y = qmm.mx4_moe(v.cuda(), *packed, I, logits=lg.cuda(), top_k=k, out_dtype=TYPES[out])
+    lg = torch.randn((T, n), generator=g) * 2
+    full = torch.full((T, E), -math.inf)
+    full[:, of] = lg
+    y = qmm.mx4_moe(v.cuda(), *packed, I, logits=full.cuda(), top_k=k, out_dtype=TYPES[out])
     ref, bound = m4.moe_ref("silu", v, *values, *m4.route_ref(lg, k, True), TYPES[out])
-    m4.assert_close(y, ref, bound, f"moe {T} {D} {I} {E} {k}")
+    m4.assert_close(y, ref, bound, f"moe {T} {D} {I} {E} {k} {n}")
 
 
 # up to 4 tokens: rows of whole 16 bytes and others, h that fits a workgroup's LDS and one that does not, more than 64 places
