@@ -45,14 +45,15 @@ _lib.qmm_mx4_moe.argtypes = [_P, _I, _L, _P, _P, _P, _P, _I, _L, _I, _I, _I, _I,
 EXPORTS_MX4 = ("qmm_mx4_quantize", "qmm_mx4_dequantize", "qmm_mx4_packed_bytes", "qmm_mx4_pack",
                "qmm_mx4_workspace_bytes", "qmm_mx4_gemm", "qmm_mx4_moe_workspace_bytes", "qmm_mx4_moe")
 
-# the current stream's handle without the object around it (a microsecond less for each call)
+# the current GPU, and its current stream's handle without the object around it (a microsecond less for each call)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _run(index, call):
     """call(stream) with the GPU current, on its current stream."""
-    if index == torch.cuda.current_device():
+    if index == _device():
         _check(call(_raw_stream(index)))
     else:
         with torch.cuda.device(index):
@@ -98,12 +99,12 @@ def mx4_quantize(x):
     index = _one_gpu(fn, x)
     M, K = x.shape
     B = _blocks(K)
-    q = torch.empty((M, 16 * B), dtype=torch.uint8, device=x.device)
+    q = x.new_empty((M, 16 * B), dtype=torch.uint8)
     lds = max(4, -(-B // 4) * 4)
-    s = torch.empty((M, lds), dtype=torch.uint8, device=x.device)
+    s = x.new_empty((M, lds), dtype=torch.uint8)
     _run(index, lambda st: _lib.qmm_mx4_quantize(px, code, ldx, q.data_ptr(), max(16 * B, 16), s.data_ptr(), lds,
                                                  M, K, st))
-    return q, s[:, :B]
+    return q, s if lds == B else s[:, :B]
 
 
 def mx4_dequantize(codes, scales, K=None, out=None, out_dtype=torch.float32):
@@ -174,7 +175,7 @@ def mx4_gemm(x, W, N, sx=None, out=None, out_dtype=torch.float32):
     pw = _packed(fn, "W", W, mx4_packed_bytes(N, K))
     index = _one_gpu(fn, x, sx, W, out)
     y, ycode, py, ldy = _output(fn, "out", out, out_dtype, (M, N), x.device)
-    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    ws = x.new_empty(need, dtype=torch.uint8) if need else None
     _run(index, lambda st: _lib.qmm_mx4_gemm(px, code, ldx, ps, lds, pw, py, ycode, ldy, M, N, K,
                                              ws.data_ptr() if need else None, need, st))
     return y
@@ -224,7 +225,7 @@ def mx4_moe(x, Wg, Wu, Wd, I, logits=None, top_k=None, renormalize=True, ids=Non
     index = _one_gpu(fn, x, Wg, Wu, Wd, logits, ids, weights, out)
     y, ycode, py, ldy = _output(fn, "out", out, out_dtype, (T, D), x.device)
     need = _lib.qmm_mx4_moe_workspace_bytes(T, D, I, E, k, xcode, ycode)
-    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    ws = x.new_empty(need, dtype=torch.uint8) if need else None
     _run(index, lambda st: _lib.qmm_mx4_moe(px, xcode, ldx, pg, pu, pd, py, ycode, ldy, T, D, I, E, k, a, pl, lcode,
                                             ldl, int(bool(renormalize)), pi, isize, pw, wcode,
                                             ws.data_ptr() if need else None, need, st))
