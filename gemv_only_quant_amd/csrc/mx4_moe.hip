@@ -35,6 +35,8 @@ template <int N> __device__ __forceinline__ void parts_of(float v, uint16_t (&p)
   }
 }
 
+template <int XP> constexpr int kTypeOfParts = XP == 1 ? XBF16 : XP == 2 ? XF16 : YF32;  // of x
+
 // ---- routing, and the activations as parts ------------------------------------
 __device__ __forceinline__ float as_f32(const void* p, int64_t i, int dtype) {
   if (dtype == YF32) return static_cast<const float*>(p)[i];
@@ -144,13 +146,15 @@ __global__ __launch_bounds__(256) void moe_route_kernel(MoeArgs g, MoeBufs o, in
     if (t < g.T) choose(g, t, lane, o.ids, o.w);
     return;
   }
+  constexpr int XT = kTypeOfParts<XP>;
   const int units = Dp / 8;
   for (int u = tid - 256 * groups; u < g.T * units; u += ((int)gridDim.x - groups) * 256) {
     const int r = u / units, i = 8 * (u - r * units);
+    float f[8];
+    floats8<XT>(take8<XT, false>(static_cast<const typename Elem<XT>::type*>(g.x) + (int64_t)r * g.ldx + i, g.D - i), f);
     uint16_t p[8][XP];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      parts_of<XP>(i + j < g.D ? as_f32(g.x, (int64_t)r * g.ldx + i + j, g.x_dtype) : 0.f, p[j]);
+    for (int j = 0; j < 8; ++j) parts_of<XP>(f[j], p[j]);
 #pragma unroll
     for (int q = 0; q < XP; ++q) {
       u32x4_t v;
@@ -984,7 +988,7 @@ template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePla
   const int xg = (a.T * (p.Dp / 8) + 255) / 256, gd = (down + per_down - 1) / per_down;
   hipError_t e = hipSuccess;
   if (a.T <= 4 && vec8_ok(a.x, a.ldx, a.D, a.x_dtype == YF32 ? 4 : 2) && a.D % 8 == 0) {
-    constexpr int XT = XP == 1 ? XBF16 : XP == 2 ? XF16 : YF32;
+    constexpr int XT = kTypeOfParts<XP>;
     e = launch_kernel(moe_up_few_kernel<XT, XP, HP>, dim3((unsigned)((up + per_up - 1) / per_up), (unsigned)slots),
                       dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs, per_up, gd);
   } else {

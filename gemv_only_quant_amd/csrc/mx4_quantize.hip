@@ -4,27 +4,6 @@
 
 namespace qmm {
 
-// 8 consecutive values of a row (zeros from `n` on), fp32.
-template <int XDT, bool VEC>
-__device__ __forceinline__ Raw8<XDT> take8(const typename Elem<XDT>::type* p, int n) {
-  Raw8<XDT> r = {};
-  if constexpr (VEC) {
-    if (n > 0) {
-      const u32x4_t* v = reinterpret_cast<const u32x4_t*>(p);
-      r.w[0] = v[0];
-      if constexpr (XDT == YF32) r.w[1] = v[1];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j >= n) break;
-      if constexpr (XDT == YF32) r.w[j / 4][j % 4] = __builtin_bit_cast(uint32_t, p[j]);
-      else r.w[0][j / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[j]) << (16 * (j % 2));
-    }
-  }
-  return r;
-}
-
 // Largest over the 4 lanes of a quad, in each of them.
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false);
@@ -120,12 +99,13 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(
   v[4] = d[0], v[5] = d[1], v[6] = f[0], v[7] = f[1];
   Y* o = y + (int64_t)m * ldy + 8 * i;
   const int n = K - 8 * i;
-  if (VEC && n >= 8) {
+  if (n >= 8) {
     typedef Y Y8 __attribute__((ext_vector_type(8)));
     Y8 q;
 #pragma unroll
     for (int j = 0; j < 8; ++j) q[j] = (Y)v[j];
-    *reinterpret_cast<Y8*>(o) = q;
+    if constexpr (VEC) *reinterpret_cast<Y8*>(o) = q;
+    else __builtin_memcpy(o, &q, sizeof(q));
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
