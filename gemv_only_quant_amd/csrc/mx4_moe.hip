@@ -402,6 +402,8 @@ template <int P> __device__ __forceinline__ float met(const MoeLds& lds, int p, 
 // Where an expert's rows fit LDS whole and there are tiles enough, a wave has whole tiles instead: nothing is left to
 // add across waves, and no barrier stands between a wave and its next weights.
 constexpr int kHeldWaves = 12, kHeldBytes = 32 * (4096 + 16);
+constexpr int held_chunks(int groups) { return (kHeldBytes / (16 * groups) - 16) / 1024; }  // of a row
+constexpr int64_t kRangesBytes = 1 << 28;  // of z, if more than one range of chunks is held
 template <int P> constexpr int kHeldRows = P == 1 ? 16 : P == 2 ? 8 : 4;  // a product's rows, of each its P parts
 
 struct HeldLds {
@@ -411,20 +413,20 @@ struct HeldLds {
   float wt[kMoeTokens];
 };
 
-// `rows` rows of bf16 parts in operand order to LDS, a chunk a turn; first() is called when the first ones are requested.
+// Chunks c0 .. of `rows` rows of bf16 parts in operand order to LDS, a chunk a turn; first() is called when the first ones are requested.
 template <int P, class Offset, class First>
-__device__ __forceinline__ void hold_rows(HeldLds& lds, const buf_t (&parts)[P], int rows, int ld, int chunks, int blocks, int wave,
+__device__ __forceinline__ void hold_rows(HeldLds& lds, const buf_t (&parts)[P], int rows, int ld, int c0, int chunks, int blocks, int wave,
                                           int lane, Offset&& offset, First&& first) {
   constexpr int RG = kHeldRows<P>, AHEAD = 4;
   const int turns = rows * P * chunks;
   u32x4_t v[AHEAD];
   auto get = [&](int t) {
     const int m = t / (P * chunks), q = (t / chunks) % P, c = t % chunks;
-    const bool ok = t < turns && 4 * (lane & 3) + (lane >> 4) < blocks - 16 * c;
+    const bool ok = t < turns && 4 * (lane & 3) + (lane >> 4) < blocks - 16 * (c0 + c);
     u32x4_t x = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < P; ++i)
-      if (i == q) x = __builtin_amdgcn_raw_buffer_load_b128(parts[i], ok ? 1024 * c + 16 * lane : kNowhere, t < turns ? offset(m) : 0, 0);
+      if (i == q) x = __builtin_amdgcn_raw_buffer_load_b128(parts[i], ok ? 1024 * (c0 + c) + 16 * lane : kNowhere, t < turns ? offset(m) : 0, 0);
     return x;
   };
   auto put = [&](int t, const u32x4_t& x) {
@@ -599,7 +601,7 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_up_held_kernel(MoeArgs g,
   for (int r0 = 0; r0 < members; r0 += G * RG) {
     if (r0 > 0) __syncthreads();
     const int rows = min(members - r0, G * RG), groups = (rows + RG - 1) / RG;
-    hold_rows<XP>(lds, parts, rows, ld, chunks, blocks, wave, lane,
+    hold_rows<XP>(lds, parts, rows, ld, 0, chunks, blocks, wave, lane,
                   [&](int r) { return 2 * Dp * __builtin_amdgcn_readfirstlane(lds.tok[r0 + r]); },
                   [&] { sweep.begin(tile + wave, tiles, chunks, fetch); });
     sweep.run(lds.rows, ld, groups, tiles, chunks, lane, fetch, [&](int t, const f32x4_t (&acc)[G][2]) {
@@ -684,18 +686,19 @@ __device__ __forceinline__ bool first_place(const int* ids, int p, int k) {
   return first;
 }
 
-// Column n of a token's rows, those of places p0 .. + k - 1 that exist, added in this order.
+// Column n of a token's rows, those of places p0 .. + k - 1 that exist (valid), of each range of `stride` rows; added in
+// this order.
 template <bool COHERENT, class Valid>
-__device__ __forceinline__ float token_sum(buf_t z, int p0, int k, int Dz, int n, Valid&& valid) {
+__device__ __forceinline__ float token_sum(buf_t z, int p0, int k, int Dz, int n, int ranges, int stride, Valid&& valid) {
   float v = 0.f;
-  for (int j0 = 0; j0 < k; j0 += 8) {  // 8 loads at once
+  for (int j0 = 0; j0 < k * ranges; j0 += 8) {  // 8 loads at once
     float r[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int p = p0 + j0 + j;
-      const bool ok = j0 + j < k && valid(p);
-      r[j] = __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(z, ok ? 4 * (p * Dz + n) : kNowhere, 0,
-                                                                                      COHERENT ? kCoherent : 0));
+      const int range = (j0 + j) / k, p = j0 + j - range * k;
+      r[j] = __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+                                           z, range < ranges && valid(p) ? 4 * ((range * stride + p0 + p) * Dz + n) : kNowhere, 0,
+                                           COHERENT ? kCoherent : 0));
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) v += r[j];
@@ -767,7 +770,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
   const int n0 = 32 * tile, cols = min(32 * tiles, g.D) - n0;
   for (int i = threadIdx.x; i < cols * g.T; i += 64 * kMoeWaves) {
     const int t = i / cols, n = n0 + i % cols;
-    const float v = token_sum<true>(zb, t * k, k, Dz, n, [&](int p) { return valid[p]; });
+    const float v = token_sum<true>(zb, t * k, k, Dz, n, 1, 0, [&](int p) { return valid[t * k + p]; });
     with_y(g.y, g.y_dtype, [&](auto* yt) {
       typedef typename std::remove_pointer<decltype(yt)>::type Y;
       yt[(int64_t)t * g.ldy + n] = (Y)v;
@@ -776,21 +779,22 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
 }
 
 template <int HP, int G>
-__global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int Dz, int per) {
+__global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int Dz, int per, int range) {
   __shared__ HeldLds lds;
   constexpr int RG = kHeldRows<HP>;
   const int lane = threadIdx.x & 63, quad = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const MoeGroup m = group_of(o, (int)blockIdx.y, pairs != 0, g.T, g.top_k, lane);
   if (m.e < 0) return;
-  const int chunks = mx4_chunks(g.I), blocks = mx4_blocks(g.I), members = __popcll(m.who), ld = 2 * Ip + 16;
+  const int c0 = range * (int)blockIdx.z, chunks = min(range, mx4_chunks(g.I) - c0), ld = 1024 * range + 16;
+  const int blocks = mx4_blocks(g.I), members = __popcll(m.who);
   const int tile = per * (int)blockIdx.x, tiles = min(tile + per, Dz / 32);
   const int64_t strip_bytes = mx4_strip_bytes(g.I), at = (int64_t)m.e * mx4_weight_bytes(g.D, g.I);
   auto fetch = [&](MoeChunk (&w)[2], int t, int c) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      load_chunk(w[i], t < tiles && 32 * t + 16 * i < g.D ? g.wd + at + (2 * t + i) * strip_bytes + (int64_t)kChunkBytes * c : nullptr,
-                 blocks - 16 * c, lane);
+      load_chunk(w[i], t < tiles && 32 * t + 16 * i < g.D ? g.wd + at + (2 * t + i) * strip_bytes + (int64_t)kChunkBytes * (c0 + c) : nullptr,
+                 blocks - 16 * (c0 + c), lane);
   };
   if (wave == 0 && m.place >= 0) {
     const int r = __popcll(m.who & ((uint64_t(1) << lane) - 1));
@@ -803,7 +807,7 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs 
   for (int r0 = 0; r0 < members; r0 += G * RG) {
     if (r0 > 0) __syncthreads();
     const int rows = min(members - r0, G * RG), groups = (rows + RG - 1) / RG;
-    hold_rows<HP>(lds, parts, rows, ld, chunks, blocks, wave, lane,
+    hold_rows<HP>(lds, parts, rows, ld, c0, chunks, blocks, wave, lane,
                   [&](int r) { return 2 * Ip * __builtin_amdgcn_readfirstlane(lds.row[r0 + r]); },
                   [&] { sweep.begin(tile + wave, tiles, chunks, fetch); });
     sweep.run(lds.rows, ld, groups, tiles, chunks, lane, fetch, [&](int t, const f32x4_t (&acc)[G][2]) {
@@ -813,7 +817,7 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs 
         for (int q = 0; q < 4; ++q) {
           const int rr = 4 * quad + q, r = RG * i + rr;
           if (rr >= RG || r >= rows) continue;
-          float* z = o.z + (int64_t)lds.row[r0 + r] * Dz + 32 * t + l16;
+          float* z = o.z + ((int64_t)blockIdx.z * g.T * g.top_k + lds.row[r0 + r]) * Dz + 32 * t + l16;
           z[0] = acc[i][0][q], z[16] = acc[i][1][q];
         }
     });
@@ -925,11 +929,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g,
 }
 
 // The same sums by a launch of its own, a workgroup for 256 columns of a token.
-__global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs g, MoeBufs o, int Dz, int blocks) {
+__global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs g, MoeBufs o, int Dz, int blocks, int ranges) {
   const int t = (int)blockIdx.x / blocks, n = ((int)blockIdx.x % blocks) * 256 + (int)threadIdx.x, k = g.top_k;
+  const buf_t zb = make_buf(o.z, 4u * (uint32_t)(g.T * k) * (uint32_t)Dz * (uint32_t)ranges);
+  // the places whose expert no earlier one has
+  const int lane = threadIdx.x & 63, id = lane < k ? o.ids[t * k + lane] : -1;
+  bool first = id >= 0;
+  for (int p = 0; p + 1 < k; ++p) first = first && !(p < lane && __builtin_amdgcn_readlane(id, p) == id);
+  const uint32_t firsts = (uint32_t)__ballot(first);
   if (n >= g.D) return;
-  const buf_t zb = make_buf(o.z, 4u * (uint32_t)(g.T * k) * (uint32_t)Dz);
-  const float v = token_sum<false>(zb, t * k, k, Dz, n, [&](int p) { return first_place(o.ids, p, k); });
+  const float v = token_sum<false>(zb, t * k, k, Dz, n, ranges, g.T * k, [&](int p) { return (firsts >> p) & 1; });
   with_y(g.y, g.y_dtype, [&](auto* yt) {
     typedef typename std::remove_pointer<decltype(yt)>::type Y;
     yt[(int64_t)t * g.ldy + n] = (Y)v;
@@ -937,13 +946,40 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs g, MoeBufs o, int
 }
 
 // ---------------------------------------------------------------- host side
-MoePlan plan_moe(int T, int D, int I, int top_k, int x_dtype, int y_dtype) {
+// Whether workgroups, one on each CU, hold an expert's rows, and of how many row groups: 0 not.  RG: tokens of a group;
+// `split`: whether they may hold a range of a row's chunks; `least`: tiles that each has, else not.  Taken for what tokens
+// that choose evenly would choose.
+static HeldPlan plan_held(int T, int top_k, int E, int RG, int chunks, bool split, int tiles, int least) {
+  float none = 1.f;
+  for (int t = 0; t < T; ++t) none *= 1.f - (float)top_k / (float)E;
+  const float chosen = (float)E * (1.f - none), mean = (float)(T * top_k) / chosen;
+  HeldPlan p{};
+  const bool one = T <= RG || mean + 2.f * sqrtf(mean) <= (float)RG;
+  p.groups = one && (T <= RG || chunks > held_chunks(2)) ? 1 : 2;
+  p.ranges = (chunks + held_chunks(p.groups) - 1) / held_chunks(p.groups);
+  if (p.ranges > 1 && !split) return HeldPlan{};
+  p.range = (chunks + p.ranges - 1) / p.ranges;
+  p.ranges = (chunks + p.range - 1) / p.range;
+  const float parts = chosen * (float)p.ranges;
+  const int wgs = parts < 256.f ? (int)(256.f / parts) : 1;
+  p.per = (tiles + wgs - 1) / wgs;
+  return p.per < least ? HeldPlan{} : p;
+}
+
+MoePlan plan_moe(int T, int D, int I, int E, int top_k, int x_dtype, int y_dtype) {
   MoePlan p{};
   p.xparts = x_dtype == YF32 ? 3 : x_dtype == XF16 ? 2 : 1;
   p.hparts = y_dtype == YF32 ? 3 : 2;
   p.Dp = (int)round_up(D, 512);
   p.Ip = (int)round_up(I, 512);
   p.Dz = (int)round_up(D, 32);
+  auto rows = [](int parts) { return parts == 1 ? kHeldRows<1> : parts == 2 ? kHeldRows<2> : kHeldRows<3>; };
+  // (held in LDS or not, 18 tiles a workgroup: 45 and 39 us; 22 tiles: 41 and 48)
+  p.up = plan_held(T, top_k, E, rows(p.xparts), mx4_chunks(D), false, 2 * mx4_blocks(I), 20);
+  // (10 tiles a workgroup: 23 us and 5 of additions, else 23; 16 tiles: 27 and 5, else 36 and 5; 22 tiles: 28 and 5, else 49)
+  p.down = plan_held(T, top_k, E, rows(p.hparts), mx4_chunks(I), true, p.Dz / 32, 14);
+  const int64_t z = (int64_t)T * top_k * p.Dz * 4;
+  if (p.down.ranges > 1 && z * p.down.ranges > kRangesBytes) p.down = HeldPlan{};
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -955,27 +991,8 @@ MoePlan plan_moe(int T, int D, int I, int top_k, int x_dtype, int y_dtype) {
   p.done = take((size_t)p.Dz / 32 * 4);
   p.x = take((size_t)p.xparts * T * p.Dp * 2);
   p.h = take((size_t)p.hparts * T * top_k * p.Ip * 2);
-  p.z = take((size_t)T * top_k * p.Dz * 4);
+  p.z = take((size_t)z * (p.down.ranges > 1 ? p.down.ranges : 1));
   p.bytes = at;
-  return p;
-}
-
-// Whether workgroups, one on each CU, hold an expert's rows, and of how many row groups: 0 not.  RG: tokens of a group;
-// Kp: values of a row.  Taken for what tokens that choose evenly would choose.
-struct HeldPlan {
-  int groups, per;  // per: tiles of a workgroup
-};
-static HeldPlan plan_held(const MoeArgs& a, int RG, int Kp, int tiles, int least) {
-  float none = 1.f;
-  for (int t = 0; t < a.T; ++t) none *= 1.f - (float)a.top_k / (float)a.E;
-  const float chosen = (float)a.E * (1.f - none), mean = (float)(a.T * a.top_k) / chosen;
-  const int bytes = 16 * (2 * Kp + 16);
-  HeldPlan p{};
-  if (a.T <= RG || mean + 2.f * sqrtf(mean) <= (float)RG) p.groups = bytes <= kHeldBytes;
-  if (a.T > RG && 2 * bytes <= kHeldBytes) p.groups = 2;
-  const int wgs = chosen < 256.f ? (int)(256.f / chosen) : 1;
-  p.per = (tiles + wgs - 1) / wgs;
-  if (p.per < least) p.groups = 0;
   return p;
 }
 
@@ -994,8 +1011,7 @@ template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePla
   } else {
     e = launch_kernel(moe_route_kernel<XP>, dim3((unsigned)((a.T + 3) / 4 + (xg < 256 ? xg : 256))), dim3(256), s, a, o, gd, p.Dp);
     if (e != hipSuccess) return e;
-    // (held in LDS or not, 18 tiles a workgroup: 45 and 39 us; 22 tiles: 41 and 48)
-    const HeldPlan held = plan_held(a, kHeldRows<XP>, p.Dp, up, 20);
+    const HeldPlan& held = p.up;
     if (held.groups != 0) {
       e = launch_kernel(held.groups == 1 ? moe_up_held_kernel<XP, HP, 1> : moe_up_held_kernel<XP, HP, 2>,
                         dim3((unsigned)((up + held.per - 1) / held.per), (unsigned)slots), dim3(64 * kHeldWaves), s, a, o, p.Dp,
@@ -1010,20 +1026,20 @@ template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePla
   const int places = a.T * a.top_k;
   if (a.T <= 4 && places <= 64 && (int64_t)places * HP * (2 * p.Ip + 16) <= kFewLds)
     return launch_kernel(moe_down_few_kernel<HP>, dim3((unsigned)((a.D + 15) / 16)), dim3(64 * kFewWaves), s, a, o, p.Ip);
-  // (10 tiles a workgroup: 23 us and 5 of additions, else 23; 16 tiles: 27 and 5, else 36 and 5; 22 tiles: 28 and 5, else 49)
-  const HeldPlan held = plan_held(a, kHeldRows<HP>, p.Ip, down, 14);
+  const HeldPlan& held = p.down;
   const bool join = held.groups == 0 && a.T <= 16;
   if (held.groups != 0)
     e = launch_kernel(held.groups == 1 ? moe_down_held_kernel<HP, 1> : moe_down_held_kernel<HP, 2>,
-                      dim3((unsigned)((down + held.per - 1) / held.per), (unsigned)slots), dim3(64 * kHeldWaves), s, a, o, p.Ip,
-                      pairs, p.Dz, held.per);
+                      dim3((unsigned)((down + held.per - 1) / held.per), (unsigned)slots, (unsigned)held.ranges), dim3(64 * kHeldWaves), s, a,
+                      o, p.Ip, pairs, p.Dz, held.per, held.range);
   else
     e = launch_kernel(!join ? moe_down_kernel<HP, 2, false>
                             : a.T <= kRowGroup<HP> ? moe_down_kernel<HP, 1, true> : moe_down_kernel<HP, 2, true>,
                       dim3((unsigned)gd, (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs, p.Dz, per_down);
   if (e != hipSuccess || join) return e;
   const int columns = (a.D + 255) / 256;
-  return launch_kernel(moe_join_kernel, dim3((unsigned)(a.T * columns)), dim3(256), s, a, o, p.Dz, columns);
+  return launch_kernel(moe_join_kernel, dim3((unsigned)(a.T * columns)), dim3(256), s, a, o, p.Dz, columns,
+                       held.groups != 0 ? held.ranges : 1);
 }
 
 template <int XP> static hipError_t moe_h(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {

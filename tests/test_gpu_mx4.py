@@ -288,10 +288,10 @@ def test_moe(T, D, I, E, k, x, out, act, norm):
 
 
 # (T, D, I, E, top_k, n): tiles enough, of E experts' weights, for workgroups that hold an expert's rows: in the first half,
-# the second, both; n experts alone are chosen, so that more of one's tokens come than are held at once; a group of rows and two
+# the second, both, the second in ranges; n experts alone are chosen, so that more of one's tokens come than are held at once
 MANY = [(64, 130, 330, 300, 8, 60), (64, 460, 40, 300, 8, 60), (64, 460, 330, 260, 8, 9), (16, 460, 330, 256, 32, 33),
         (8, 460, 330, 256, 32, 40), (4, 897, 650, 128, 32, 34), (64, 2100, 330, 260, 8, 16), (64, 460, 2100, 260, 8, 16),
-        (20, 4000, 330, 300, 32, 40)]
+        (20, 4000, 330, 300, 32, 40), (16, 900, 9000, 40, 8, 4)]
 
 
 @pytest.mark.parametrize("T,D,I,E,k,n", MANY)
