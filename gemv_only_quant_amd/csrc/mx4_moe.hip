@@ -848,27 +848,21 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs 
 constexpr int kFewWaves = 16, kFewLds = 120 << 10;
 
 template <int HP>
-__global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g, MoeBufs o, int Ip) {
-  __shared__ __align__(16) char hs[kFewLds];  // h's rows, of each its parts, 16 bytes apart
+__global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g, MoeBufs o, uint32_t inverse, int step_x, int step_c) {
+  __shared__ __align__(16) char hs[kFewLds];  // h's rows, of each its parts, chunks kRowBytes apart
   __shared__ float sums[kFewWaves][16][17];
   const int lane = threadIdx.x & 63, k = g.top_k, places = g.T * k;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   static_assert(HP <= 4, "a row's parts are rows of the product");
   const int l16 = lane & 15, quad = lane >> 4, strip = (int)blockIdx.x;
-  const int chunks = mx4_chunks(g.I), blocks = mx4_blocks(g.I), row_bytes = 2 * Ip + 16;
+  const int chunks = mx4_chunks(g.I), blocks = mx4_blocks(g.I);
   const int id = lane < places ? o.ids[lane] : -1;
   // h to LDS, a chunk of a row's part a turn
   constexpr int HELD = 4;
   const int turns = places * HP * chunks;
   u32x4_t v[HELD];
-  auto get = [&](int t) {
-    const int r = t / chunks, q = r / places, c = t - r * chunks;  // r: part q's row r - q places
-    return *reinterpret_cast<const u32x4_t*>(o.h + ((int64_t)q * places + (r - q * places)) * Ip + 512 * c + 8 * lane);
-  };
-  auto put = [&](int t, const u32x4_t& x) {
-    const int r = t / chunks, c = t - r * chunks;
-    *reinterpret_cast<u32x4_t*>(hs + r * row_bytes + 1024 * c + 16 * lane) = x;
-  };
+  auto get = [&](int t) { return *reinterpret_cast<const u32x4_t*>(o.h + (int64_t)512 * t + 8 * lane); };
+  auto put = [&](int t, const u32x4_t& x) { *reinterpret_cast<u32x4_t*>(hs + t * kRowBytes + 16 * lane) = x; };
   int t = wave;
 #pragma unroll
   for (int i = 0; i < HELD; ++i)
@@ -878,24 +872,33 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g,
   bool first = id >= 0;
   for (int p = 0; p + 1 < places; ++p) first = first && !(p < lane && __builtin_amdgcn_readlane(id, p) == id);
   const uint64_t firsts = __ballot(first);
-  const int rank = __popcll(firsts & ((uint64_t(1) << lane) - 1)), items = __popcll(firsts) * chunks;
-  auto expert = [&](int n) {
-    const uint64_t m = __ballot(first && rank == n / chunks);
-    return __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(m | (uint64_t(1) << 63)));
+  const int rank = __popcll(firsts & ((uint64_t(1) << lane) - 1)), experts = __popcll(firsts);
+  // A wave's units: chunk c of the x-th chosen expert, the kFewWaves-th next one each time.  (Without divisions: step_x and
+  // step_c are kFewWaves over chunks, and its remainder.)
+  struct Unit {
+    int x, c;
   };
-  auto request = [&](MoeChunk& w, int n) {
+  auto after = [&](const Unit& u) {
+    Unit n = {u.x + step_x, u.c + step_c};
+    if (n.c >= chunks) n.c -= chunks, ++n.x;
+    return n;
+  };
+  auto expert = [&](const Unit& u) {
+    return __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(__ballot(first && rank == u.x) | (uint64_t(1) << 63)));
+  };
+  auto request = [&](MoeChunk& w, const Unit& u) {
     const uint8_t* p = nullptr;
-    int nb = 0;
-    if (n < items) {
-      const int c = n % chunks;
-      p = g.wd + (int64_t)expert(n) * mx4_weight_bytes(g.D, g.I) + (int64_t)strip * mx4_strip_bytes(g.I) + (int64_t)kChunkBytes * c;
-      nb = blocks - 16 * c;
-    }
-    load_chunk(w, p, nb, lane);
+    if (u.x < experts)
+      p = g.wd + (int64_t)expert(u) * mx4_weight_bytes(g.D, g.I) + (int64_t)strip * mx4_strip_bytes(g.I) +
+          (int64_t)kChunkBytes * u.c;
+    load_chunk(w, p, blocks - 16 * u.c, lane);
   };
   MoeChunk w[2];
-  request(w[0], wave);
-  request(w[1], wave + kFewWaves);
+  Unit u0, u1;
+  u0.x = (int)((uint32_t)wave * inverse >> 16), u0.c = wave - u0.x * chunks;
+  u1 = after(u0);
+  request(w[0], u0);
+  request(w[1], u1);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int i = 0; i < HELD; ++i)
@@ -904,13 +907,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g,
   __syncthreads();
 
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  auto use = [&](const MoeChunk& m, int n) {
-    const int c = n % chunks, e = expert(n);
+  auto use = [&](const MoeChunk& m, const Unit& u) {
+    const int c = u.c, e = expert(u);
     // row l16 is part l16 / 4 of token l16 % 4, its first place with this expert
     const uint64_t same = __ballot(id == e);
     const int token = l16 % 4, part = l16 / 4;
     const uint32_t own = token < g.T && part < HP ? (uint32_t)(same >> (token * k)) & (uint32_t)((uint64_t(1) << k) - 1) : 0u;
-    const char* from = own == 0 ? hs : hs + (part * places + token * k + __builtin_ctz(own)) * row_bytes + 1024 * c + 16 * quad;
+    const char* from = own == 0 ? hs : hs + ((part * places + token * k + __builtin_ctz(own)) * chunks + c) * kRowBytes + 16 * quad;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const bool ok = own != 0 && 4 * quad + j < blocks - 16 * c;
@@ -924,12 +927,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g,
       }
     }
   };
-  for (int n = wave; n < items; n += 2 * kFewWaves) {
-    use(w[0], n);
-    request(w[0], n + 2 * kFewWaves);
-    if (n + kFewWaves >= items) break;
-    use(w[1], n + kFewWaves);
-    request(w[1], n + 3 * kFewWaves);
+  while (u0.x < experts) {
+    use(w[0], u0);
+    u0 = after(u1);
+    request(w[0], u0);
+    if (u1.x >= experts) break;
+    use(w[1], u1);
+    u1 = after(u0);
+    request(w[1], u1);
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) sums[wave][4 * quad + r][l16] = acc[r];
@@ -1043,8 +1048,10 @@ template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePla
   }
   if (e != hipSuccess) return e;
   const int places = a.T * a.top_k;
-  if (a.T <= 4 && places <= 64 && (int64_t)places * HP * (2 * p.Ip + 16) <= kFewLds)
-    return launch_kernel(moe_down_few_kernel<HP>, dim3((unsigned)((a.D + 15) / 16)), dim3(64 * kFewWaves), s, a, o, p.Ip);
+  const int chunks = mx4_chunks(a.I);
+  if (a.T <= 4 && places <= 64 && (int64_t)places * HP * chunks * kRowBytes <= kFewLds)
+    return launch_kernel(moe_down_few_kernel<HP>, dim3((unsigned)((a.D + 15) / 16)), dim3(64 * kFewWaves), s, a, o,
+                         (uint32_t)((65536 + chunks - 1) / chunks), kFewWaves / chunks, kFewWaves % chunks);
   const HeldPlan& held = p.down;
   const bool join = held.groups == 0 && a.T <= 16;
   if (held.groups != 0)
