@@ -438,9 +438,12 @@ __device__ __forceinline__ void hold_rows(HeldLds& lds, const buf_t (&parts)[P],
                                           int lane, Offset&& offset, First&& first) {
   constexpr int RG = kHeldRows<P>, AHEAD = 4;
   const int turns = rows * P * chunks;
+  // t / chunks, exact for the 32 rows of 8 chunks that there may be
+  const uint32_t inverse = 65535u / (uint32_t)chunks + 1;
+  auto row_of = [&](int t) { return (int)((uint32_t)t * inverse >> 16); };
   u32x4_t v[AHEAD];
   auto get = [&](int t) {
-    const int m = t / (P * chunks), q = (t / chunks) % P, c = t % chunks;
+    const int r = row_of(t), m = r / P, q = r % P, c = t - r * chunks;
     const bool ok = t < turns && 4 * (lane & 3) + (lane >> 4) < blocks - 16 * (c0 + c);
     u32x4_t x = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -449,7 +452,7 @@ __device__ __forceinline__ void hold_rows(HeldLds& lds, const buf_t (&parts)[P],
     return x;
   };
   auto put = [&](int t, const u32x4_t& x) {
-    const int m = t / (P * chunks), q = (t / chunks) % P, c = t % chunks;
+    const int r = row_of(t), m = r / P, q = r % P, c = t - r * chunks;
     if (t < turns) *reinterpret_cast<u32x4_t*>(lds.rows + (16 * (m / RG) + RG * q + m % RG) * ld + 1024 * c + 16 * lane) = x;
   };
   for (int t = wave; t == wave || t < turns; t += AHEAD * kHeldWaves) {
