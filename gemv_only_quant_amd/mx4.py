@@ -81,6 +81,15 @@ def _coded(fn, codes, scales):
     return pc, ldc, ps, lds, cols // 16
 
 
+def _result(fn, like, out, out_dtype, shape):
+    """As _output, a new tensor from another of its GPU (half a microsecond less)."""
+    if out is not None:
+        return _output(fn, "out", out, out_dtype, shape, like.device)
+    code = _float_type(fn, "out_dtype", out_dtype)
+    out = like.new_empty(shape, dtype=out_dtype)
+    return out, code, out.data_ptr(), max(shape[1], 1)
+
+
 def _packed(fn, name, W, need):
     """Pointer of a packed weight of `need` bytes."""
     if not isinstance(W, torch.Tensor) or W.dtype != torch.uint8:
@@ -117,7 +126,7 @@ def mx4_dequantize(codes, scales, K=None, out=None, out_dtype=torch.float32):
         _refuse(fn, f"K={K} does not have {B} blocks of 32")
     index = _one_gpu(fn, codes, scales, out)
     M = codes.shape[0]
-    y, code, py, ldy = _output(fn, "out", out, out_dtype, (M, K), codes.device)
+    y, code, py, ldy = _result(fn, codes, out, out_dtype, (M, K))
     _run(index, lambda st: _lib.qmm_mx4_dequantize(pc, ldc, ps, lds, py, code, ldy, M, K, st))
     return y
 
@@ -174,7 +183,7 @@ def mx4_gemm(x, W, N, sx=None, out=None, out_dtype=torch.float32):
     need = _lib.qmm_mx4_workspace_bytes(M, K, code)
     pw = _packed(fn, "W", W, mx4_packed_bytes(N, K))
     index = _one_gpu(fn, x, sx, W, out)
-    y, ycode, py, ldy = _output(fn, "out", out, out_dtype, (M, N), x.device)
+    y, ycode, py, ldy = _result(fn, x, out, out_dtype, (M, N))
     ws = x.new_empty(need, dtype=torch.uint8) if need else None
     _run(index, lambda st: _lib.qmm_mx4_gemm(px, code, ldx, ps, lds, pw, py, ycode, ldy, M, N, K,
                                              ws.data_ptr() if need else None, need, st))
@@ -223,7 +232,7 @@ def mx4_moe(x, Wg, Wu, Wd, I, logits=None, top_k=None, renormalize=True, ids=Non
         pi, isize, pw, wcode = ids.data_ptr(), ids.element_size(), weights.data_ptr(), \
             _float_type(fn, "weights", weights.dtype)
     index = _one_gpu(fn, x, Wg, Wu, Wd, logits, ids, weights, out)
-    y, ycode, py, ldy = _output(fn, "out", out, out_dtype, (T, D), x.device)
+    y, ycode, py, ldy = _result(fn, x, out, out_dtype, (T, D))
     need = _lib.qmm_mx4_moe_workspace_bytes(T, D, I, E, k, xcode, ycode)
     ws = x.new_empty(need, dtype=torch.uint8) if need else None
     _run(index, lambda st: _lib.qmm_mx4_moe(px, xcode, ldx, pg, pu, pd, py, ycode, ldy, T, D, I, E, k, a, pl, lcode,
