@@ -313,9 +313,10 @@ def test_moe_of_many_tiles(T, D, I, E, k, n, x, out):
     m4.assert_close(y, ref, bound, f"moe {T} {D} {I} {E} {k} {n}")
 
 
-# up to 4 tokens: rows of whole 16 bytes and others, h that fits a workgroup's LDS and one that does not, more than 64 places
+# few tokens: rows of whole 16 bytes and others, h that fits a workgroup's LDS and one that does not, more than 64 places
 FEW = [(1, 8, 40, 4, 4), (2, 520, 520, 9, 3), (3, 1032, 77, 128, 8), (4, 2064, 300, 16, 16), (4, 72, 96, 40, 17), (4, 40, 2600, 20, 5),
-       (4, 64, 96, 300, 32), (1, 512, 8200, 2, 2), (2, 4104, 64, 3, 1)]
+       (4, 64, 96, 300, 32), (1, 512, 8200, 2, 2), (2, 4104, 64, 3, 1), (8, 72, 96, 300, 32), (5, 1001, 77, 16, 4), (7, 33, 50, 40, 17),
+       (8, 2600, 40, 100, 9)]
 
 
 @pytest.mark.parametrize("T,D,I,E,k", FEW)
