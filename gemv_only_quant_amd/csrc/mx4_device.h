@@ -13,19 +13,6 @@ __device__ __forceinline__ float scale_f32(uint32_t e) {
   return __builtin_bit_cast(float, e == 0 ? 0x00400000u : e == 255 ? 0x7FC00000u : b);
 }
 
-// c += A B^t over 128 values of 16 rows each, both operands mx4: lane L holds
-// block L / 16 (32 codes, 16 bytes) of row L % 16, and in the low byte of its
-// scale word that block's scale; the matrix cores apply the scales (255 gives
-// NaN, 0 is 2^-127).  Products within a block are summed exactly; block sums and
-// accumulator are aligned to the largest of them, and what falls below its last
-// bits is dropped.
-__device__ __forceinline__ f32x4_t mfma_mx4(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c,
-                                            uint32_t sa, uint32_t sb) {
-  const i32x8_t x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-  const i32x8_t y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, (int)sa, 0, (int)sb);
-}
-
 // 8 codes times their scale as bf16, pairs in order: exact wherever bf16 has
 // the value (code times power of two: all but the ends of its range).
 __device__ __forceinline__ u32x4_t bf16_of_codes(uint32_t c, float scale) {

@@ -3,13 +3,21 @@
 //
 //   h[t][j] = w[t][j] act(Wg_e x[t]) * (Wu_e x[t]),  y[t] = sum_j Wd_e h[t][j]
 //
-// Bound by reading the weights of the experts that some token chose, once.  The
-// products run on the 16-bit matrix cores: a code times its scale is exact in
-// bf16, whose exponents reach as far as the scales', and an activation of more
-// bits is a sum of bf16 parts (fp16: 2, fp32: 3, exact), each multiplied in turn;
-// in the weights' shadow that costs nothing.  Rows of the product are an expert's tokens.
+// Bound by reading the weights of the experts that some token chose, once.  The products run on the 16-bit matrix cores: a
+// code times its scale is exact in bf16, whose exponents reach as far as the scales', and an activation of more bits is a
+// sum of bf16 parts (fp16: 2, fp32: 3, exact; h: 2, or 3 for fp32 y), rows of the product beside each other, whose sums are
+// added in fp32.  The other rows are an expert's further tokens, so most of the time parts cost nothing.
 //
-// Three launches: the tokens' choices, and x as parts; the first half; the second.
+// Launches: the tokens' choices, and x as parts; the first half, h; the second, rows of y of each choice; their sum.  What
+// differs is how rows and weights come to a wave (us from one launch to the next, bf16 if not said):
+//
+//  few     up to 4 tokens: each workgroup of the first half makes the choices itself, one of the second has its columns of y
+//          whole.  Two launches, bound by their latencies: one token, 8 of 128 experts of 2048 x 768, 13.5 (17.4 by three
+//          launches, each part a product of its own)
+//  held    many columns for each CU: a workgroup holds an expert's rows in LDS, a wave has whole tiles and no barrier between
+//          them.  64 tokens, 64 experts of 2048 x 1408, 6 each, fp16: 80 (4.0 TB/s of weights; by the next form 101); 16
+//          tokens, 8 experts of 4096 x 14336, 2 each: 137 (5.5 TB/s; 152)
+//  other   K over a workgroup's waves, rows through each wave's own LDS: 5 tokens, 16 experts of 1001 x 777, 4 each, fp32: 18
 #include <math.h>
 
 #include "mx4_device.h"
@@ -432,10 +440,11 @@ struct HeldLds {
   float wt[kMoeTokens];
 };
 
-// Chunks c0 .. of `rows` rows of bf16 parts in operand order to LDS, a chunk a turn; first() is called when the first ones are requested.
+// Chunks c0 .. of `rows` rows of bf16 parts in operand order to LDS, a chunk a turn; first() is called when the first ones
+// are requested.
 template <int P, class Offset, class First>
-__device__ __forceinline__ void hold_rows(HeldLds& lds, const buf_t (&parts)[P], int rows, int ld, int c0, int chunks, int blocks, int wave,
-                                          int lane, Offset&& offset, First&& first) {
+__device__ __forceinline__ void hold_rows(HeldLds& lds, const buf_t (&parts)[P], int rows, int ld, int c0, int chunks,
+                                          int blocks, int wave, int lane, Offset&& offset, First&& first) {
   constexpr int RG = kHeldRows<P>, AHEAD = 4;
   const int turns = rows * P * chunks;
   // t / chunks, exact for the 32 rows of 8 chunks that there may be
@@ -445,15 +454,17 @@ __device__ __forceinline__ void hold_rows(HeldLds& lds, const buf_t (&parts)[P],
   auto get = [&](int t) {
     const int r = row_of(t), m = r / P, q = r % P, c = t - r * chunks;
     const bool ok = t < turns && 4 * (lane & 3) + (lane >> 4) < blocks - 16 * (c0 + c);
+    const int at = ok ? 1024 * (c0 + c) + 16 * lane : kNowhere, row = t < turns ? offset(m) : 0;
     u32x4_t x = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < P; ++i)
-      if (i == q) x = __builtin_amdgcn_raw_buffer_load_b128(parts[i], ok ? 1024 * (c0 + c) + 16 * lane : kNowhere, t < turns ? offset(m) : 0, 0);
+      if (i == q) x = __builtin_amdgcn_raw_buffer_load_b128(parts[i], at, row, 0);
     return x;
   };
   auto put = [&](int t, const u32x4_t& x) {
     const int r = row_of(t), m = r / P, q = r % P, c = t - r * chunks;
-    if (t < turns) *reinterpret_cast<u32x4_t*>(lds.rows + (16 * (m / RG) + RG * q + m % RG) * ld + 1024 * c + 16 * lane) = x;
+    const int to = (16 * (m / RG) + RG * q + m % RG) * ld + 1024 * c + 16 * lane;
+    if (t < turns) *reinterpret_cast<u32x4_t*>(lds.rows + to) = x;
   };
   for (int t = wave; t == wave || t < turns; t += AHEAD * kHeldWaves) {
 #pragma unroll
@@ -465,7 +476,7 @@ __device__ __forceinline__ void hold_rows(HeldLds& lds, const buf_t (&parts)[P],
   __syncthreads();
 }
 
-// The tiles tile, tile + 16 .. of a wave, their weights in two sets of registers in turn; put(tile, sums of rows).
+// The tiles tile, tile + kHeldWaves .. of a wave, their weights in two sets of registers in turn; put(tile, sums of rows).
 template <int P, int G> struct HeldSweep {
   MoeChunk w[2][2];
   int t, c, tn, cn;  // the unit whose weights come first, and the one requested last
@@ -479,7 +490,8 @@ template <int P, int G> struct HeldSweep {
     if (++c == chunks) c = 0, t += kHeldWaves;
   }
   template <class Fetch, class Put>
-  __device__ __forceinline__ void run(const char* rows, int ld, int groups, int tiles, int chunks, int lane, Fetch&& fetch, Put&& put) {
+  __device__ __forceinline__ void run(const char* rows, int ld, int groups, int tiles, int chunks, int lane, Fetch&& fetch,
+                                      Put&& put) {
     f32x4_t acc[G][2] = {};
     const char* from0 = rows + (lane & 15) * ld + 16 * (lane >> 4);
     auto use = [&](const MoeChunk (&m)[2]) {
@@ -494,7 +506,8 @@ template <int P, int G> struct HeldSweep {
 #pragma unroll
           for (int g = 0; g < G; ++g) {
             if (g > 0 && g >= groups) break;
-            const bf16x8_t a = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t*>(from + 16 * g * ld + 256 * j + 64 * i));
+            const char* at = from + 16 * g * ld + 256 * j + 64 * i;
+            const bf16x8_t a = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t*>(at));
             acc[g][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b0, acc[g][0], 0, 0, 0);
             acc[g][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b1, acc[g][1], 0, 0, 0);
           }
@@ -534,8 +547,8 @@ template <int P, int G> struct HeldSweep {
 // ---- first half ----------------------------------------------------------------
 // Column threadIdx.x % 16 of strip t of h, from the waves' sums of row rr, for `place` of token `tok`.
 template <int XP, int HP>
-__device__ __forceinline__ void put_hidden(const MoeArgs& g, const MoeBufs& o, const MoeLds& lds, int rr, int t, int tok, int place,
-                                           float wt, int Ip) {
+__device__ __forceinline__ void put_hidden(const MoeArgs& g, const MoeBufs& o, const MoeLds& lds, int rr, int t, int tok,
+                                           int place, float wt, int Ip) {
   const int col = threadIdx.x % 16;
   const float gv = met<XP>(lds, 0, rr, col), uv = met<XP>(lds, 1, rr, col);
   float h = 0.f;
@@ -545,8 +558,9 @@ __device__ __forceinline__ void put_hidden(const MoeArgs& g, const MoeBufs& o, c
   });
   uint16_t p[HP];
   parts_of<HP>(16 * t + col < g.I ? h : 0.f, p);  // the padding is 0 whatever x is
+  const int row = tok * g.top_k + place, at = operand_order(16 * t + col);
 #pragma unroll
-  for (int q = 0; q < HP; ++q) o.h[((int64_t)q * g.T * g.top_k + tok * g.top_k + place) * Ip + operand_order(16 * t + col)] = p[q];
+  for (int q = 0; q < HP; ++q) o.h[((int64_t)q * g.T * g.top_k + row) * Ip + at] = p[q];
 }
 
 // A workgroup: `per` strips of 16 columns of h of one expert.
@@ -582,7 +596,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs g, Mo
     rows.offs = r0 + lane < members ? 2 * tok[r0 + lane] * Dp : 0;
     rows.members = members - r0, rows.blocks = blocks, rows.lane = lane, rows.lds = lds.rows[wave];
     if (wave < chunks) rows.request(0, wave);
-    sweep<XP, G>(rows, members - r0, wave, tile, tiles, chunks, lds.rows[wave], lane, fetch, [&](int t, const f32x4_t (&acc)[G][2]) {
+    auto put = [&](int t, const f32x4_t (&acc)[G][2]) {
 #pragma unroll
       for (int i = 0; i < G; ++i) {
         if (r0 + RG * i >= members) break;
@@ -590,12 +604,14 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs g, Mo
         const int rr = threadIdx.x / 16, r = r0 + RG * i + rr;
         if (rr < RG && r < members) put_hidden<XP, HP>(g, o, lds, rr, t, tok[r], place[r], wt[r], Ip);
       }
-    });
+    };
+    sweep<XP, G>(rows, members - r0, wave, tile, tiles, chunks, lds.rows[wave], lane, fetch, put);
   }
 }
 
 template <int XP, int HP, int G>
-__global__ __launch_bounds__(64 * kHeldWaves) void moe_up_held_kernel(MoeArgs g, MoeBufs o, int Dp, int Ip, int pairs, int per) {
+__global__ __launch_bounds__(64 * kHeldWaves) void moe_up_held_kernel(MoeArgs g, MoeBufs o, int Dp, int Ip, int pairs,
+                                                                      int per) {
   __shared__ HeldLds lds;
   constexpr int RG = kHeldRows<XP>;
   const int lane = threadIdx.x & 63, quad = lane >> 4, l16 = lane & 15;
@@ -648,10 +664,12 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_up_held_kernel(MoeArgs g,
   }
 }
 
-// The same for up to 4 tokens, with their choices made by every workgroup itself (a launch less), rows of the product
+// The same for up to 4 tokens, with their choices made by every workgroup itself (a launch less: one token, 8 of 128 experts
+// of 2048 x 768, 7.3 us for 4 and 7 by two), rows of the product
 // the tokens in their order.  The first workgroup leaves the choices for the second half.
 template <int XT, int XP, int HP>
-__global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_few_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int per, int strips_y) {
+__global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_few_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int per,
+                                                                       int strips_y) {
   __shared__ MoeLds lds;
   __shared__ int ids[4 * kMoeTopK];
   __shared__ float ws[4 * kMoeTopK];
@@ -697,9 +715,6 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_few_kernel(MoeArgs g
 }
 
 // ---- second half ---------------------------------------------------------------
-// A workgroup: `per` times 32 columns of one expert's rows of y.  A token's rows are added in the order of its
-// choices: for a few tokens (JOIN) by the last of those columns' workgroups to come, else by another launch (64
-// tokens, 64 experts of 2048 x 1408: few workgroups would be left with 23 us of additions).
 // Whether place p of all tokens' choices has rows: that of an expert which no earlier place of its token has.
 __device__ __forceinline__ bool first_place(const int* ids, int p, int k) {
   const int e = ids[p];
@@ -718,9 +733,8 @@ __device__ __forceinline__ float token_sum(buf_t z, int p0, int k, int Dz, int n
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int range = (j0 + j) / k, p = j0 + j - range * k;
-      r[j] = __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-                                           z, range < ranges && valid(p) ? 4 * ((range * stride + p0 + p) * Dz + n) : kNowhere, 0,
-                                           COHERENT ? kCoherent : 0));
+      const int at = range < ranges && valid(p) ? 4 * ((range * stride + p0 + p) * Dz + n) : kNowhere;
+      r[j] = __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(z, at, 0, COHERENT ? kCoherent : 0));
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) v += r[j];
@@ -728,6 +742,9 @@ __device__ __forceinline__ float token_sum(buf_t z, int p0, int k, int Dz, int n
   return v;
 }
 
+// A workgroup: `per` times 32 columns of one expert's rows of y.  A token's rows are added in the order of its places: for
+// a few tokens (JOIN) by the last of those columns' workgroups to come, else by another launch (64 tokens, 64 experts of
+// 2048 x 1408: few workgroups would be left with 23 us of additions, the launch takes 5).
 template <int HP, int G, bool JOIN>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int Dz, int per) {
   __shared__ MoeLds lds;
@@ -764,7 +781,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
       rows.offs = r0 + lane < members ? 2 * (tok[r0 + lane] * k + place[r0 + lane]) * Ip : 0;
       rows.members = members - r0, rows.blocks = blocks, rows.lane = lane, rows.lds = lds.rows[wave];
       if (wave < chunks) rows.request(0, wave);
-      sweep<HP, G>(rows, members - r0, wave, tile, tiles, chunks, lds.rows[wave], lane, fetch, [&](int t, const f32x4_t (&acc)[G][2]) {
+      auto put = [&](int t, const f32x4_t (&acc)[G][2]) {
 #pragma unroll
         for (int i = 0; i < G; ++i) {
           if (r0 + RG * i >= members) break;
@@ -776,7 +793,8 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
           __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), zb,
                                                 4 * ((tok[r] * k + place[r]) * Dz + 32 * t + col), 0, JOIN ? kCoherent : 0);
         }
-      });
+      };
+      sweep<HP, G>(rows, members - r0, wave, tile, tiles, chunks, lds.rows[wave], lane, fetch, put);
     }
   }
   if (!JOIN) return;
@@ -801,7 +819,8 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
 }
 
 template <int HP, int G>
-__global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int Dz, int per, int range) {
+__global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int Dz, int per,
+                                                                        int range) {
   __shared__ HeldLds lds;
   constexpr int RG = kHeldRows<HP>;
   const int lane = threadIdx.x & 63, quad = lane >> 4, l16 = lane & 15;
@@ -814,9 +833,10 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs 
   const int64_t strip_bytes = mx4_strip_bytes(g.I), at = (int64_t)m.e * mx4_weight_bytes(g.D, g.I);
   auto fetch = [&](MoeChunk (&w)[2], int t, int c) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      load_chunk(w[i], t < tiles && 32 * t + 16 * i < g.D ? g.wd + at + (2 * t + i) * strip_bytes + (int64_t)kChunkBytes * (c0 + c) : nullptr,
-                 blocks - 16 * (c0 + c), lane);
+    for (int i = 0; i < 2; ++i) {
+      const int64_t to = at + (2 * t + i) * strip_bytes + (int64_t)kChunkBytes * (c0 + c);
+      load_chunk(w[i], t < tiles && 32 * t + 16 * i < g.D ? g.wd + to : nullptr, blocks - 16 * (c0 + c), lane);
+    }
   };
   if (wave == 0 && m.place >= 0) {
     const int r = __popcll(m.who & ((uint64_t(1) << lane) - 1));
@@ -847,11 +867,13 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs 
 }
 
 // The same for up to 4 tokens and 64 choices whose h fits LDS: a workgroup has 16 columns of y whole, its 16 waves taking
-// chunks of all chosen experts in turn; nothing is left to add across workgroups.
+// chunks of all chosen experts in turn; nothing is left to add across workgroups (one token, 8 of 128 experts of 2048 x 768:
+// 6.8 us, by the next kernel 9.3).
 constexpr int kFewWaves = 16, kFewLds = 120 << 10;
 
 template <int HP>
-__global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g, MoeBufs o, uint32_t inverse, int step_x, int step_c) {
+__global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g, MoeBufs o, uint32_t inverse, int step_x,
+                                                                      int step_c) {
   __shared__ __align__(16) char hs[kFewLds];  // h's rows, of each its parts, chunks kRowBytes apart
   __shared__ float sums[kFewWaves][16][17];
   const int lane = threadIdx.x & 63, k = g.top_k, places = g.T * k;
@@ -916,7 +938,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g,
     const uint64_t same = __ballot(id == e);
     const int token = l16 % 4, part = l16 / 4;
     const uint32_t own = token < g.T && part < HP ? (uint32_t)(same >> (token * k)) & (uint32_t)((uint64_t(1) << k) - 1) : 0u;
-    const char* from = own == 0 ? hs : hs + ((part * places + token * k + __builtin_ctz(own)) * chunks + c) * kRowBytes + 16 * quad;
+    const int row = own == 0 ? 0 : part * places + token * k + __builtin_ctz(own);
+    const char* from = own == 0 ? hs : hs + (row * chunks + c) * kRowBytes + 16 * quad;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const bool ok = own != 0 && 4 * quad + j < blocks - 16 * c;
@@ -955,7 +978,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g,
   });
 }
 
-// The same sums by a launch of its own, a workgroup for 256 columns of a token.
+// A token's sums by a launch of its own, a workgroup for 256 columns.
 __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs g, MoeBufs o, int Dz, int blocks, int ranges) {
   const int t = (int)blockIdx.x / blocks, n = ((int)blockIdx.x % blocks) * 256 + (int)threadIdx.x, k = g.top_k;
   const buf_t zb = make_buf(o.z, 4u * (uint32_t)(g.T * k) * (uint32_t)Dz * (uint32_t)ranges);
@@ -977,8 +1000,8 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs g, MoeBufs o, int
 // `split`: whether they may hold a range of a row's chunks; `least`: tiles that each has, else not.  Taken for what tokens
 // that choose evenly would choose.
 static HeldPlan plan_held(int T, int top_k, int E, int RG, int chunks, bool split, int tiles, int least) {
-  float none = 1.f;
-  for (int t = 0; t < T; ++t) none *= 1.f - (float)top_k / (float)E;
+  float none = 1.f;  // (given experts may be more than there are)
+  for (int t = 0; t < T; ++t) none *= 1.f - (float)(top_k < E ? top_k : E) / (float)E;
   const float chosen = (float)E * (1.f - none), mean = (float)(T * top_k) / chosen;
   HeldPlan p{};
   const bool one = T <= RG || mean + 2.f * sqrtf(mean) <= (float)RG;

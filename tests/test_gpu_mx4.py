@@ -362,6 +362,18 @@ def test_moe_given_experts(T, itype):
             assert (y[1:3] == 0).all()
 
 
+@pytest.mark.parametrize("T,E,k", [(64, 1, 32), (3, 1, 5), (64, 2, 17), (4, 2, 16)])
+def test_moe_more_places_than_experts(T, E, k):
+    D, I = 72, 40
+    packed, values = experts(E, D, I, 4)
+    g = torch.Generator().manual_seed(T)
+    ids, w = torch.randint(-1, E + 1, (T, k), generator=g), torch.randn((T, k), generator=g)
+    v = m4.tokens(T, D, seed=1, dtype=torch.bfloat16)
+    y = qmm.mx4_moe(v.cuda(), *packed, I, ids=ids.cuda(), weights=w.cuda())
+    ref, bound = m4.moe_ref("silu", v, *values, ids, w, torch.float32)
+    m4.assert_close(y, ref, bound, f"places {T} {E} {k}")
+
+
 @pytest.mark.parametrize("lt", TYPES)
 def test_moe_equal_logits_take_the_lowest(lt):
     T, D, I, E, k = 20, 64, 48, 150, 5

@@ -114,6 +114,18 @@ def raises(fn, text, status=ARG):
     assert text in str(e.value) and e.value.status == status, str(e.value)
 
 
+@pytest.mark.parametrize("E", [1, 2, 3, 40, 1024])
+def test_mixture_workspace_for_any_choice(E):
+    """Given experts may be more for each token than there are."""
+    need = L.qmm_mx4_moe_workspace_bytes
+    for T in (1, 2, 3, 16, 63, 64):
+        for k in (1, 2, 3, 8, 31, 32):
+            for D, I in ((1, 1), (64, 64), (4096, 14336), (14336, 4096)):
+                if T * k * max(D, I) < 1 << 27:
+                    for x in (0, 1, 2):
+                        assert need(T, D, I, E, k, x, x) >= 4 * T * k * (D + I)
+
+
 def test_binding_checks():
     u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
     x, W = torch.zeros(4, 64), u8(qmm.mx4_packed_bytes(32, 64))
