@@ -190,7 +190,7 @@ qmm_status qmm_mx4_gemm(const void* x, int x_dtype, int64_t ldx, const uint8_t* 
   a.a = packed;
   hipError_t e = coded ? qmm::launch_mx4_pack(static_cast<const uint8_t*>(x), ldx, sx, ldsx, packed, 1, M, K, s)
                        : qmm::launch_mx4_quantize_packed(x, x_dtype, ldx, packed, M, K, s);
-  if (e == hipSuccess) e = qmm::mx4_skinny_fits(M) ? qmm::launch_mx4_skinny(a, s) : qmm::launch_mx4_large(a, s);
+  if (e == hipSuccess) e = qmm::mx4_skinny_fits(M, N) ? qmm::launch_mx4_skinny(a, s) : qmm::launch_mx4_large(a, s);
   return device_status(fn, e);
 }
 

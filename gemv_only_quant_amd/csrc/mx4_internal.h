@@ -47,8 +47,8 @@ struct Mx4Args {
 // Few values (mx4_skinny.hip): quantized within the launch; a.a counts for nothing.
 bool mx4_rows_fits(int M, int K);
 hipError_t launch_mx4_rows(const Mx4Args& a, const void* x, int x_dtype, int64_t ldx, hipStream_t s);
-// Up to 64 rows, and more (mx4_large.hip).
-bool mx4_skinny_fits(int M);
+// Up to 64 rows or some more, and many (mx4_large.hip).
+bool mx4_skinny_fits(int M, int N);
 hipError_t launch_mx4_skinny(const Mx4Args& a, hipStream_t s);
 hipError_t launch_mx4_large(const Mx4Args& a, hipStream_t s);
 

@@ -1,4 +1,4 @@
-// mx4_skinny.hip -- products of microscaled 4-bit codes for up to 64 rows, y = x^ W^t:
+// mx4_skinny.hip -- products of microscaled 4-bit codes for few rows, y = x^ W^t:
 // bound by reading the weights once.  The packed strip is the matrix cores' operand:
 // waves stream chunks of 512 values from memory straight to registers and multiply
 // them by v_mfma_scale_f32_16x16x128_f8f6f4, a few instructions for each KiB; what the
@@ -6,9 +6,11 @@
 //
 //  rows    (few values) x is quantized by every workgroup itself, into LDS in the
 //          operand's order, while its first weights are on their way: one launch;
-//  packed  x comes packed as weights are, and is read as they are.
+//  packed  x comes packed as weights are, and is read as they are, in blocks of up to 64 rows.
 //
 // The waves of a workgroup split K (chunks in turn) and add their sums in LDS in a fixed order.
+// us from one launch to the next, bf16: 1 x 4096 x 4096 3.7 (2.4 TB/s); 64 x 4096 x 14336 13.4 with x packed (2.5 TB/s), of
+// which the product is 10.9: 224 workgroups read 140 KB of weights and as much of x each, all of it requested at once.
 #include <type_traits>
 
 #include "mx4_device.h"
@@ -182,16 +184,18 @@ __global__ __launch_bounds__(64 * KW) void mx4_rows_kernel(const uint8_t* __rest
 }
 
 // ---- packed ----------------------------------------------------------------------
-// A workgroup: all rows (MT strips of the packed x) and PS strips of columns.
+// A workgroup: 16 MT rows (MT strips of the packed x) and PS strips of columns.
 template <int MT, int PS, int KW, class Y>
 __global__ __launch_bounds__(64 * KW, 1) void mx4_packed_kernel(Mx4Args g) {
+  const int m0 = 16 * MT * (int)blockIdx.y;
   __shared__ float sums[KW][PS][16 * MT][17];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
   const int chunks = mx4_chunks(g.K), s0 = PS * (int)blockIdx.x;
-  const int strips = (g.N + 15) / 16, mt = (g.M + 15) / 16;
+  const int strips = (g.N + 15) / 16, mt = (g.M - m0 + 15) / 16;
   const int64_t strip_bytes = mx4_strip_bytes(g.K);
+  const uint8_t* rows = g.a + m0 / 16 * strip_bytes;
   struct Stage {
     Chunk a[MT], b[PS];
   };
@@ -201,7 +205,7 @@ __global__ __launch_bounds__(64 * KW, 1) void mx4_packed_kernel(Mx4Args g) {
     for (int p = 0; p < PS; ++p)
       load_chunk<kStream>(s.b[p], c < chunks && s0 + p < strips ? g.w + (s0 + p) * strip_bytes + at : nullptr, lane);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) load_chunk<0>(s.a[i], c < chunks && i < mt ? g.a + i * strip_bytes + at : nullptr, lane);
+    for (int i = 0; i < MT; ++i) load_chunk<0>(s.a[i], c < chunks && i < mt ? rows + i * strip_bytes + at : nullptr, lane);
   };
   f32x4_t acc[MT][PS];
 #pragma unroll
@@ -237,11 +241,11 @@ __global__ __launch_bounds__(64 * KW, 1) void mx4_packed_kernel(Mx4Args g) {
   __syncthreads();
   for (int i = threadIdx.x; i < 16 * MT * 16 * PS; i += 64 * KW) {
     const int m = i / (16 * PS), col = i % (16 * PS), n = 16 * s0 + col;
-    if (m >= g.M || n >= g.N) continue;
+    if (m0 + m >= g.M || n >= g.N) continue;
     float v = 0.f;
 #pragma unroll
     for (int q = 0; q < KW; ++q) v += sums[q][col / 16][m][col % 16];
-    static_cast<Y*>(g.y)[(int64_t)m * g.ldy + n] = (Y)v;
+    static_cast<Y*>(g.y)[(int64_t)(m0 + m) * g.ldy + n] = (Y)v;
   }
 }
 
@@ -252,7 +256,14 @@ static int rows_lds(int M, int K, int waves) { return rows_x_bytes(M, mx4_chunks
 // Where strips are too few to occupy the chip, more waves share each.
 static int rows_waves(int M, int N, int K) { return (N + 15) / 16 <= 128 && rows_lds(M, K, 16) <= kRowsLds ? 16 : 8; }
 
-bool mx4_skinny_fits(int M) { return M <= 64; }
+// Workgroups of 64 rows and PS strips, where these are all on the chip at once.
+static int64_t row_blocks(int M, int N, int PS) { return (((int64_t)N + 16 * PS - 1) / (16 * PS)) * (((int64_t)M + 63) / 64); }
+static bool at_once(int M, int N, int PS) { return row_blocks(M, N, PS) <= 256; }
+
+// More rows too, if blocks of 64 with 4 strips are all on the chip at once: waves that split K end sooner than a few tiles of
+// 128 x 128 that have all of it (K = 4096, us from codes: 128 x 4096 10.6, tiles 20.2; 256 x 4096 13.9, tiles 20.3; with 2
+// rounds of blocks, 192 x 11008, 34, tiles 21).
+bool mx4_skinny_fits(int M, int N) { return M <= 64 || at_once(M, N, 4); }
 
 // Every workgroup quantizes all of x: up to 32 Ki values this costs less than a launch (4096 x 4096, us: 1 row
 // 3.8, 4 5.0, 8 6.2, 16 9.1; packed first 7.8 to 8.5).
@@ -294,7 +305,8 @@ template <int MT, int PS, int KW> static hipError_t packed_y(const Mx4Args& a, h
     g.w += f * mx4_strip_bytes(a.K);
     g.y = static_cast<char*>(a.y) + 16 * f * (a.y_dtype == YF32 ? 4 : 2);
     g.N = (int)(a.N - 16 * f < 16 * most ? a.N - 16 * f : 16 * most);
-    const dim3 grid((unsigned)((((int64_t)g.N + 15) / 16 + PS - 1) / PS)), block(64 * KW);
+    const dim3 grid((unsigned)((((int64_t)g.N + 15) / 16 + PS - 1) / PS), (unsigned)((g.M + 16 * MT - 1) / (16 * MT)));
+    const dim3 block(64 * KW);
     switch (a.y_dtype) {
       case XF16: e = launch_kernel(mx4_packed_kernel<MT, PS, KW, _Float16>, grid, block, s, g); break;
       case XBF16: e = launch_kernel(mx4_packed_kernel<MT, PS, KW, __bf16>, grid, block, s, g); break;
@@ -303,6 +315,9 @@ template <int MT, int PS, int KW> static hipError_t packed_y(const Mx4Args& a, h
   }
   return e;
 }
+// Strips of a workgroup: 4, or 2, as long as most CUs have one; x is read again for each.  (K = 4096, us, 1, 2 and 4 strips:
+// 16 x 4096 8.5, 9.1, 9.4; 16 x 6144 11.9, 9.4, 9.7; 16 x 12288 16.0, 13.9, 10.7; 64 x 4096 11.3, 10.1, 13.0; 64 x 6144 17.5,
+// 10.8, 13.4; 64 x 12288 24.4, 16.8, 14.6.)
 template <int MT> static hipError_t packed_m(const Mx4Args& a, hipStream_t s) {
   const int strips = (a.N + 15) / 16;
   if (strips >= 4 * 192) return packed_y<MT, 4, 4>(a, s);
@@ -310,7 +325,9 @@ template <int MT> static hipError_t packed_m(const Mx4Args& a, hipStream_t s) {
   return packed_y<MT, 1, MT == 1 ? 16 : 8>(a, s);
 }
 hipError_t launch_mx4_skinny(const Mx4Args& a, hipStream_t s) {
-  return a.M <= 16 ? packed_m<1>(a, s) : a.M <= 32 ? packed_m<2>(a, s) : packed_m<4>(a, s);
+  if (a.M <= 16) return packed_m<1>(a, s);
+  if (a.M <= 32) return packed_m<2>(a, s);
+  return at_once(a.M, a.N, 2) ? packed_y<4, 2, 4>(a, s) : packed_y<4, 4, 4>(a, s);
 }
 
 }  // namespace qmm

@@ -140,7 +140,10 @@ SIZES = [(1, 1, 1), (1, 17, 33), (1, 300, 1024), (2, 64, 4096), (3, 64, 64), (4,
          (8, 96, 528), (15, 48, 3000), (16, 130, 1000), (17, 33, 128), (33, 515, 260), (64, 256, 512),
          (65, 129, 300), (100, 1024, 96), (200, 70, 96), (257, 260, 784), (300, 520, 1040), (513, 700, 2064),
          (2100, 2100, 300), (2300, 1900, 145), (4090, 1030, 1024), (2950, 2900, 145), (1500, 2900, 200),
-         (4, 48, 16384), (1, 40, 65536), (2, 20, 40000), (16, 36, 16400), (40, 36, 20000), (16, 4100, 512)]
+         (4, 48, 16384), (1, 40, 65536), (2, 20, 40000), (16, 36, 16400), (40, 36, 20000), (16, 4100, 512),
+         # blocks of 64 rows: 2 and 4 strips a workgroup; tiles of 128 and 256 that are not whole
+         (70, 4000, 300), (257, 1400, 784), (600, 1200, 260), (16000, 20, 96), (900, 1200, 270), (1111, 1000, 1040),
+         (1300, 2000, 96), (3500, 3600, 150), (3330, 4000, 600)]
 
 
 def weights(n, k, seed):
@@ -164,12 +167,15 @@ def test_gemm(m, n, k, kind, out):
     m4.assert_close(y, xv @ wv.t(), m4.gemm_bound(xv, wv, TYPES[out]), f"gemm {m} {n} {k}")
 
 
-@pytest.mark.parametrize("m", [1, 3, 16, 50, 130, 300])
+# rows (few, up to 64, blocks of 64, tiles of 128 and of 256) and columns
+SHAPES = [(1, 50), (3, 50), (16, 50), (50, 50), (130, 50), (300, 50), (1000, 1100), (3500, 3500)]
+
+
+@pytest.mark.parametrize("m,n", SHAPES)
 @pytest.mark.parametrize("k", [128, 160, 512, 900, 2048])
-def test_whole_sums_are_exact(m, k):
+def test_whole_sums_are_exact(m, n, k):
     """Scales of 1: every sum is a whole multiple of a quarter below 2^24 quarters; each block in its place
     (the codes of a block depend on it)."""
-    n = 50
     g = torch.Generator().manual_seed(m + k)
     B = m4.blocks(k)
     c = torch.randint(0, 16, (m, 32 * B), generator=g, dtype=torch.uint8)
@@ -180,13 +186,13 @@ def test_whole_sums_are_exact(m, k):
     assert torch.equal(y, m4.VALUES[c.long()] @ m4.VALUES[d.long()].t())
 
 
-@pytest.mark.parametrize("m", [1, 7, 40, 150])
-def test_one_block_at_a_time(m):
+@pytest.mark.parametrize("m,n", [(1, 37), (7, 37), (40, 37), (150, 37), (1000, 1100), (3500, 3500)])
+def test_one_block_at_a_time(m, n):
     """One block of x and one of W are not zero, each with a scale of its own: the product of the pair, exactly,
     wherever they meet, for every place of a row."""
-    k, n = 1184, 37
+    k = 1184
     B = m4.blocks(k)
-    for b in range(B):
+    for b in range(B) if m < 1000 else (0, 7, 15, 16, 30, 36):
         c = torch.zeros((m, 32 * B), dtype=torch.uint8)
         d = torch.zeros((n, 32 * B), dtype=torch.uint8)
         g = torch.Generator().manual_seed(b)
@@ -200,9 +206,9 @@ def test_one_block_at_a_time(m):
         assert torch.equal(y, want), b
 
 
-@pytest.mark.parametrize("m", [1, 6, 40, 90, 300])
-def test_gemm_strided(m):
-    n, k = 70, 200
+@pytest.mark.parametrize("m,n", [(1, 70), (6, 70), (40, 70), (90, 70), (300, 70), (1000, 1100), (3500, 3500)])
+def test_gemm_strided(m, n):
+    k = 200
     W, wv = weights(n, k, 3)
     q, s = m4.coded(2 * m, k, 5, 120, 130)
     big = torch.full((2 * m, q.shape[1] + 48), 255, dtype=torch.uint8).cuda()
@@ -225,9 +231,9 @@ def test_gemm_strided(m):
         m4.assert_close(qmm.mx4_gemm(v, W, n), xq @ wv.t(), m4.gemm_bound(xq, wv, torch.float32), "strided x")
 
 
-@pytest.mark.parametrize("m", [1, 5, 20, 100, 300])
-def test_rows_that_are_not_finite_touch_no_other(m):
-    n, k = 50, 300
+@pytest.mark.parametrize("m,n", [(1, 50), (5, 50), (20, 50), (100, 50), (300, 50), (1000, 1100), (3500, 3500)])
+def test_rows_that_are_not_finite_touch_no_other(m, n):
+    k = 300
     W, _ = weights(n, k, 2)
     x = m4.tokens(m, k, seed=1, dtype=torch.bfloat16)
     clean = qmm.mx4_gemm(x.cuda(), W, n).cpu()
@@ -518,7 +524,7 @@ def test_other_stream_and_run_to_run():
         assert torch.equal(g, want)
 
 
-@pytest.mark.parametrize("m", [3, 20, 70, 300])
+@pytest.mark.parametrize("m", [3, 20, 70, 300, 6000])
 def test_a_row_does_not_depend_on_its_neighbours(m):
     n, k = 200, 1000
     W, _ = weights(n, k, 1)
@@ -538,3 +544,15 @@ def test_warns_where_gradients_end():
         qmm.mx4_quantize(x)
     with torch.no_grad():
         qmm.mx4_quantize(x)
+
+
+def test_example_runs():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "mx4_experts.py")
+    spec = importlib.util.spec_from_file_location("mx4_experts", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    for tokens in ("1", "6", "40"):
+        assert all(mod.main(["--width", "512", "--hidden", "160", "--experts", "12", "--top-k", "3", "--vocab", "1000",
+                             "--tokens", tokens], log=lambda *_: None))
