@@ -23,7 +23,7 @@ import ctypes
 import torch
 
 from . import _check, _lib
-from .int8 import _act, _float_type, _matrix, _one_gpu, _output, _refuse
+from .int8 import _INT_MAX, _act, _float_type, _matrix, _one_gpu, _output, _refuse
 
 QMM_MX4 = 4  # x_dtype of activations that are codes already
 QMM_MX4_MAX_TOKENS, QMM_MX4_MAX_TOP_K, QMM_MX4_MAX_EXPERTS = 64, 32, 1024
@@ -58,6 +58,12 @@ def _run(index, call):
     else:
         with torch.cuda.device(index):
             _check(call(_raw_stream(index)))
+
+
+def _size(fn, name, v):
+    """A size that is no tensor's: an int that the library's would not cut off."""
+    if not isinstance(v, int) or not 0 <= v <= _INT_MAX:
+        _refuse(fn, f"{name} must be a size below 2^31, got {v!r}")
 
 
 def _blocks(K):
@@ -122,7 +128,8 @@ def mx4_dequantize(codes, scales, K=None, out=None, out_dtype=torch.float32):
     fn = "qmm_mx4_dequantize"
     pc, ldc, ps, lds, B = _coded(fn, codes, scales)
     K = 32 * B if K is None else K
-    if _blocks(K) != B or K < 0:
+    _size(fn, "K", K)
+    if _blocks(K) != B:
         _refuse(fn, f"K={K} does not have {B} blocks of 32")
     index = _one_gpu(fn, codes, scales, out)
     M = codes.shape[0]
@@ -132,7 +139,9 @@ def mx4_dequantize(codes, scales, K=None, out=None, out_dtype=torch.float32):
 
 
 def mx4_packed_bytes(N, K):
-    """Bytes of a packed weight (N, K)."""
+    """Bytes of a packed weight (N, K); 0 for sizes that there cannot be."""
+    if not (0 <= N <= _INT_MAX and 0 <= K <= _INT_MAX):
+        return 0
     return _lib.qmm_mx4_packed_bytes(N, K)
 
 
@@ -167,6 +176,7 @@ def mx4_gemm(x, W, N, sx=None, out=None, out_dtype=torch.float32):
     B), or (M, K) float values that the call quantizes as mx4_quantize does.  y is `out`, else a new tensor of
     out_dtype (float32, float16, bfloat16)."""
     fn = "qmm_mx4_gemm"
+    _size(fn, "N", N)
     ps, lds = None, 0
     if isinstance(x, torch.Tensor) and x.dtype == torch.uint8:
         if sx is None:
@@ -198,6 +208,7 @@ def mx4_moe(x, Wg, Wu, Wd, I, logits=None, top_k=None, renormalize=True, ids=Non
     all; or ids (T, k) int32 / int64 with weights (T, k): an id outside [0, E) counts for nothing.  Activations
     are not quantized.  y is `out`, else a new tensor of out_dtype."""
     fn = "qmm_mx4_moe"
+    _size(fn, "I", I)
     a = _act(fn, act)
     px, ldx = _matrix(fn, "x", x)
     xcode = _float_type(fn, "x", x.dtype)
@@ -213,6 +224,7 @@ def mx4_moe(x, Wg, Wu, Wd, I, logits=None, top_k=None, renormalize=True, ids=Non
             _refuse(fn, "logits, or ids and weights, not both")
         if top_k is None:
             _refuse(fn, "logits need top_k")
+        _size(fn, "top_k", top_k)
         pl, ldl = _matrix(fn, "logits", logits, (T, E))
         lcode = _float_type(fn, "logits", logits.dtype)
         k = top_k

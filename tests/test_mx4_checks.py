@@ -172,6 +172,20 @@ def test_binding_checks():
     raises(lambda: go(logits=lg, top_k=2, x=x.double()), "x must be one of")
 
 
+@pytest.mark.parametrize("v", [1 << 32 | 32, 1 << 31, -1, 32.0, None, "32"])
+def test_binding_refuses_sizes_that_would_be_cut_off(v):
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
+    x, W = torch.zeros(4, 64), u8(qmm.mx4_packed_bytes(32, 64))
+    up, down = u8(8, qmm.mx4_packed_bytes(32, 64)), u8(8, qmm.mx4_packed_bytes(64, 32))
+    raises(lambda: qmm.mx4_gemm(x, W, v), "N must be a size")
+    raises(lambda: qmm.mx4_moe(x, up, up, down, v, logits=torch.zeros(4, 8), top_k=2), "I must be a size")
+    if v is not None:
+        raises(lambda: qmm.mx4_moe(x, up, up, down, 32, logits=torch.zeros(4, 8), top_k=v), "top_k must be a size")
+        raises(lambda: qmm.mx4_dequantize(u8(4, 32), u8(4, 2), v), "K must be a size")
+    if isinstance(v, int):
+        assert qmm.mx4_packed_bytes(v, 64) == qmm.mx4_packed_bytes(64, v) == 0
+
+
 def test_quantizer_reference_worked_example():
     """Largest 6: floor(log2 6) - 2 = 0, scale byte 127 and codes the values themselves, rounded; halves to even."""
     x = torch.zeros(2, 33)
