@@ -1,5 +1,7 @@
 // mx4_device.h -- device helpers of the microscaled 4-bit kernels (gfx950).
 #pragma once
+#include <type_traits>
+
 #include "mx4_internal.h"
 #include "w8a8_device.h"
 
@@ -42,32 +44,54 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
   return e == 255 ? 255u : (e < 2 ? 0u : e - 2);
 }
 
-// 8 consecutive values of a row (zeros from `n` on).  Whole ones are loaded at once where they lie: global memory takes
-// any alignment (value by value, 333 x 1001 fp32 to packed codes took 6.3 us, so 4.1; VEC: on 16 bytes, rows of whole 8).
+// Values k .. k + 7 of a row of K (zeros from K on).  VEC: on 16 bytes, K a multiple of 8.  Else they are loaded at once where
+// they lie, global memory takes any alignment; the last ones of a row with those before them, which settle8 shifts out when
+// all of a wave's loads are under way (value by value, 333 x 1001 fp32 to packed codes took 6.3 us, so 4.7).
 template <int XDT, bool VEC>
-__device__ __forceinline__ Raw8<XDT> take8(const typename Elem<XDT>::type* p, int n) {
+__device__ __forceinline__ Raw8<XDT> take8(const typename Elem<XDT>::type* row, int k, int K) {
   Raw8<XDT> r = {};
+  const int n = K - k;
   if constexpr (VEC) {
     if (n > 0) {
-      const u32x4_t* v = reinterpret_cast<const u32x4_t*>(p);
+      const u32x4_t* v = reinterpret_cast<const u32x4_t*>(row + k);
       r.w[0] = v[0];
       if constexpr (XDT == YF32) r.w[1] = v[1];
     }
-  } else if (n >= 8) {
+  } else if (n > 0 && K >= 8) {
     typedef u32x4_t words_t __attribute__((aligned(4)));
     typedef u32x4_t halves_t __attribute__((aligned(2)));
-    const auto* v = reinterpret_cast<const typename std::conditional<XDT == YF32, words_t, halves_t>::type*>(p);
+    const int back = n >= 8 ? 0 : 8 - n;
+    const auto* v = reinterpret_cast<const typename std::conditional<XDT == YF32, words_t, halves_t>::type*>(row + k - back);
     r.w[0] = v[0];
     if constexpr (XDT == YF32) r.w[1] = v[1];
-  } else {
+  } else if (n > 0) {
 #pragma unroll
     for (int j = 0; j < 7; ++j) {
       if (j >= n) break;
-      if constexpr (XDT == YF32) r.w[j / 4][j % 4] = __builtin_bit_cast(uint32_t, p[j]);
-      else r.w[0][j / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[j]) << (16 * (j % 2));
+      if constexpr (XDT == YF32) r.w[j / 4][j % 4] = __builtin_bit_cast(uint32_t, row[k + j]);
+      else r.w[0][j / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, row[k + j]) << (16 * (j % 2));
     }
   }
   return r;
+}
+
+template <int XDT, bool VEC> __device__ __forceinline__ void settle8(Raw8<XDT>& r, int k, int K) {
+  const int back = K < 8 || K - k <= 0 || K - k >= 8 ? 0 : 8 - (K - k);
+  if (VEC || back == 0) return;
+  constexpr int WORDS = XDT == YF32 ? 8 : 4;
+  uint32_t w[WORDS];
+#pragma unroll
+  for (int j = 0; j < WORDS; ++j) w[j] = r.w[j / 4][j % 4];
+  const int words = XDT == YF32 ? back : back / 2;
+#pragma unroll
+  for (int s = WORDS / 2; s > 0; s /= 2)
+#pragma unroll
+    for (int j = 0; j < WORDS; ++j) w[j] = (words & s) == 0 ? w[j] : j + s < WORDS ? w[j + s] : 0;
+  if constexpr (XDT != YF32)
+#pragma unroll
+    for (int j = 0; j < WORDS; ++j) w[j] = (back & 1) == 0 ? w[j] : (w[j] >> 16) | (j + 1 < WORDS ? w[j + 1] << 16 : 0);
+#pragma unroll
+  for (int j = 0; j < WORDS; ++j) r.w[j / 4][j % 4] = w[j];
 }
 
 }  // namespace qmm

@@ -178,7 +178,9 @@ __global__ __launch_bounds__(256) void moe_route_kernel(MoeArgs g, MoeBufs o, in
   for (int u = tid - 256 * groups; u < g.T * units; u += ((int)gridDim.x - groups) * 256) {
     const int r = u / units, i = 8 * (u - r * units);
     float f[8];
-    floats8<XT>(take8<XT, false>(static_cast<const typename Elem<XT>::type*>(g.x) + (int64_t)r * g.ldx + i, g.D - i), f);
+    Raw8<XT> raw = take8<XT, false>(static_cast<const typename Elem<XT>::type*>(g.x) + (int64_t)r * g.ldx, i, g.D);
+    settle8<XT, false>(raw, i, g.D);
+    floats8<XT>(raw, f);
     uint16_t p[8][XP];
 #pragma unroll
     for (int j = 0; j < 8; ++j) parts_of<XP>(f[j], p[j]);

@@ -22,7 +22,8 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(
   if (u >= total) return;  // whole quads: units are multiples of 4
   const uint32_t m = u / (uint32_t)units;
   const int i = (int)(u - m * (uint32_t)units);
-  const Raw8<XDT> raw = take8<XDT, VEC>(x + (int64_t)m * ldx + 8 * i, K - 8 * i);
+  Raw8<XDT> raw = take8<XDT, VEC>(x + (int64_t)m * ldx, 8 * i, K);
+  settle8<XDT, VEC>(raw, 8 * i, K);
   const uint32_t e = scale_byte(quad_max(top_f32<XDT>(top8<XDT>(raw, 0u))));
   float v[8];
   floats8<XDT>(raw, v);
@@ -55,13 +56,14 @@ __global__ __launch_bounds__(256) void mx4_quantize_packed_kernel(
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int m = 16 * (int)strip + 4 * (int)(u % 4) + i, k = 512 * c + 8 * lane;
-    raw[i] = take8<XDT, VEC>(x + (int64_t)(m < M ? m : 0) * ldx + k, m < M ? K - k : 0);
+    raw[i] = take8<XDT, VEC>(x + (int64_t)(m < M ? m : 0) * ldx, m < M ? k : K, K);
   }
   // lane: quarter lane % 4 of block lane / 4 = 4 q + j
   const int q = lane >> 4, j = (lane >> 2) & 3;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 4 * (int)(u % 4) + i;
+    if (16 * (int)strip + r < M) settle8<XDT, VEC>(raw[i], 512 * c + 8 * lane, K);
     const uint32_t e = scale_byte(quad_max(top_f32<XDT>(top8<XDT>(raw[i], 0u))));
     float v[8];
     floats8<XDT>(raw[i], v);

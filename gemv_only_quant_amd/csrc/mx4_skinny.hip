@@ -76,29 +76,13 @@ __global__ __launch_bounds__(64 * KW) void mx4_rows_kernel(const uint8_t* __rest
   const int turns = M * chunks;
   auto get = [&](int t) {
     const int r = t / chunks, k = 512 * (t - r * chunks) + 8 * lane;
-    const T* p = static_cast<const T*>(x) + (int64_t)r * ldx + k;
-    const int n = K - k;
-    Raw8<XT> v = {};
-    if constexpr (VEC) {
-      if (n > 0) {
-        const u32x4_t* q = reinterpret_cast<const u32x4_t*>(p);
-        v.w[0] = q[0];
-        if constexpr (XT == YF32) v.w[1] = q[1];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j >= n) break;
-        if constexpr (XT == YF32) v.w[j / 4][j % 4] = __builtin_bit_cast(uint32_t, p[j]);
-        else v.w[0][j / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[j]) << (16 * (j % 2));
-      }
-    }
-    return v;
+    return take8<XT, VEC>(static_cast<const T*>(x) + (int64_t)r * ldx, k, K);
   };
   // lane: quarter lane % 4 of block lane / 4 = 4 q + j
   const int pq = lane >> 4, pj = (lane >> 2) & 3;
-  auto put = [&](int t, const Raw8<XT>& v) {
+  auto put = [&](int t, Raw8<XT>& v) {
     const int r = t / chunks, c = t - r * chunks;
+    settle8<XT, VEC>(v, 512 * c + 8 * lane, K);
     uint32_t top = top_f32<XT>(top8<XT>(v, 0u));
     uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, false);
     top = o > top ? o : top;
