@@ -509,6 +509,37 @@ def test_graph_replays_between_eager_calls(T):
         assert torch.equal(y, want) and torch.equal(y2, want)
 
 
+@pytest.mark.parametrize("T,D,I,E,k,n", [(64, 460, 330, 260, 8, 13), (16, 900, 9000, 40, 8, 4), (5, 72, 96, 300, 32, 3),
+                                         (3, 77, 2600, 40, 20, 4)])
+def test_forms_replayed_and_on_two_streams_at_once(T, D, I, E, k, n):
+    """Held rows, ranges of them, rows through LDS, few tokens: n experts' weights, E / n times."""
+    packed = [w.repeat(E // n, 1) for w in experts(n, D, I, 5)[0]]
+    x, lg = torch.zeros((T, D), device="cuda", dtype=torch.float16), torch.zeros((T, E), device="cuda")
+    call = lambda: qmm.mx4_moe(x, *packed, I, logits=lg, top_k=k, renormalize=False, act="gelu")  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = call()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in range(4):
+        g = torch.Generator().manual_seed(i)
+        x.copy_(m4.tokens(T, D, i, torch.float16))
+        lg.copy_(torch.randn((T, E), generator=g))
+        want = call()
+        graph.replay()
+        call()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        got = []
+        for _ in range(3):
+            for s in streams:
+                with torch.cuda.stream(s):
+                    got.append(call())
+        torch.cuda.synchronize()
+        assert all(torch.equal(v, want) for v in got)
+
+
 def test_other_stream_and_run_to_run():
     T, D, I, E, k, n = 33, 700, 300, 8, 3, 500
     packed, _ = experts(E, D, I, 2)
