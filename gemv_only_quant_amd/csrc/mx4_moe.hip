@@ -871,7 +871,7 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs 
 // The same for up to 4 tokens and 64 choices whose h fits LDS: a workgroup has 16 columns of y whole, its 16 waves taking
 // chunks of all chosen experts in turn; nothing is left to add across workgroups (one token, 8 of 128 experts of 2048 x 768:
 // 6.8 us, by the next kernel 9.3).
-constexpr int kFewWaves = 16, kFewLds = 120 << 10;
+constexpr int kFewWaves = 16, kFewLds = 140 << 10;
 
 template <int HP>
 __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g, MoeBufs o, uint32_t inverse, int step_x,
@@ -1055,11 +1055,14 @@ template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePla
   auto each = [&](int tiles) { return (int)(((int64_t)tiles * slots + 1535) / 1536); };
   const int up = 2 * mx4_blocks(a.I), down = p.Dz / 32, per_up = each(up), per_down = each(down);
   const int xg = (a.T * (p.Dp / 8) + 255) / 256, gd = (down + per_down - 1) / per_down;
+  // where every workgroup makes the choices, all are on the chip at once (4 tokens, 8 of 128 experts of 2048 x 768: 30.4 us, in
+  // three rounds 35.9)
+  const int per_few = (int)(((int64_t)up * slots + 511) / 512);
   hipError_t e = hipSuccess;
   if (a.T <= 4 && vec8_ok(a.x, a.ldx, a.D, a.x_dtype == YF32 ? 4 : 2) && a.D % 8 == 0) {
     constexpr int XT = kTypeOfParts<XP>;
-    e = launch_kernel(moe_up_few_kernel<XT, XP, HP>, dim3((unsigned)((up + per_up - 1) / per_up), (unsigned)slots),
-                      dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs, per_up, gd);
+    e = launch_kernel(moe_up_few_kernel<XT, XP, HP>, dim3((unsigned)((up + per_few - 1) / per_few), (unsigned)slots),
+                      dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs, per_few, gd);
   } else {
     e = launch_kernel(moe_route_kernel<XP>, dim3((unsigned)((a.T + 3) / 4 + (xg < 256 ? xg : 256))), dim3(256), s, a, o, gd, p.Dp);
     if (e != hipSuccess) return e;
