@@ -308,25 +308,30 @@ template <int P> struct Parts {
     }
   }
 };
-// x itself, up to 4 tokens whose rows are whole 16 bytes: 8 values a lane, made parts on the way to LDS.
-template <int XT, int P> struct Values {
+// x itself, up to 4 tokens: 8 values a lane, made parts on the way to LDS.  VEC: rows of whole 16 bytes.
+template <int XT, int P, bool VEC> struct Values {
   static constexpr int RG = kRowGroup<P>, SIZE = XT == YF32 ? 4 : 2;
   static_assert(RG >= 4, "rows");
+  typedef typename Elem<XT>::type T;
+  const T* x;
+  int64_t ldx;
   buf_t rows[4];
-  int members, lane;
+  int members, lane, K, k;  // k: this lane's first value of those requested
   char* lds;
   Raw8<XT> v[4];
-  __device__ __forceinline__ Values(const MoeArgs& g, int lane, char* lds) : members(g.T), lane(lane), lds(lds) {
+  __device__ __forceinline__ Values(const MoeArgs& g, int lane, char* lds)
+      : x(static_cast<const T*>(g.x)), ldx(g.ldx), members(g.T), lane(lane), K(g.D), lds(lds) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      rows[r] = make_buf(static_cast<const char*>(g.x) + (int64_t)(r < g.T ? r : 0) * g.ldx * SIZE,
-                         r < g.T ? (uint32_t)(g.D * SIZE) : 0u);
+      rows[r] = make_buf(x + (r < g.T ? r : 0) * ldx, r < g.T ? (uint32_t)(K * SIZE) : 0u);
   }
   __device__ __forceinline__ void request(int, int c) {
+    k = 512 * c + 8 * lane;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       if (r >= members) break;
-      v[r] = load8<XT, true>(rows[r], 512 * c + 8 * lane);
+      if constexpr (VEC) v[r] = load8<XT, true>(rows[r], k);
+      else v[r] = take8<XT, false>(x + r * ldx, k, K);
     }
   }
   __device__ __forceinline__ void leave(int) {
@@ -335,6 +340,7 @@ template <int XT, int P> struct Values {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       if (r >= members) break;
+      settle8<XT, VEC>(v[r], k, K);
       if constexpr (P == 1) {
         *reinterpret_cast<u32x4_t*>(to + r * kRowBytes) = v[r].w[0];
       } else {
@@ -669,7 +675,7 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_up_held_kernel(MoeArgs g,
 // The same for up to 4 tokens, with their choices made by every workgroup itself (a launch less: one token, 8 of 128 experts
 // of 2048 x 768, 7.3 us for 4 and 7 by two), rows of the product
 // the tokens in their order.  The first workgroup leaves the choices for the second half.
-template <int XT, int XP, int HP>
+template <int XT, int XP, int HP, bool VEC>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_few_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int per,
                                                                        int strips_y) {
   __shared__ MoeLds lds;
@@ -678,7 +684,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_few_kernel(MoeArgs g
   const int lane = threadIdx.x & 63, k = g.top_k, slot = (int)blockIdx.y;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int chunks = mx4_chunks(g.D), blocks = mx4_blocks(g.D);
-  Values<XT, XP> rows(g, lane, lds.rows[wave]);
+  Values<XT, XP, VEC> rows(g, lane, lds.rows[wave]);
   if (wave < chunks) rows.request(0, wave);
   if (wave < g.T) choose(g, wave, lane, ids, ws);
   __syncthreads();
@@ -1059,9 +1065,10 @@ template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePla
   // three rounds 35.9)
   const int per_few = (int)(((int64_t)up * slots + 511) / 512);
   hipError_t e = hipSuccess;
-  if (a.T <= 4 && vec8_ok(a.x, a.ldx, a.D, a.x_dtype == YF32 ? 4 : 2) && a.D % 8 == 0) {
+  if (a.T <= 4) {
     constexpr int XT = kTypeOfParts<XP>;
-    e = launch_kernel(moe_up_few_kernel<XT, XP, HP>, dim3((unsigned)((up + per_few - 1) / per_few), (unsigned)slots),
+    const bool vec = vec8_ok(a.x, a.ldx, a.D, a.x_dtype == YF32 ? 4 : 2) && a.D % 8 == 0;
+    e = launch_kernel(vec ? moe_up_few_kernel<XT, XP, HP, true> : moe_up_few_kernel<XT, XP, HP, false>, dim3((unsigned)((up + per_few - 1) / per_few), (unsigned)slots),
                       dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs, per_few, gd);
   } else {
     e = launch_kernel(moe_route_kernel<XP>, dim3((unsigned)((a.T + 3) / 4 + (xg < 256 ? xg : 256))), dim3(256), s, a, o, gd, p.Dp);
