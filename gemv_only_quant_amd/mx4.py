@@ -51,13 +51,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _run(index, call):
-    """call(stream) with the GPU current, on its current stream."""
+def _run(index, call, *args):
+    """call(*args, stream) with the GPU current, on its current stream."""
     if index == _device():
-        _check(call(_raw_stream(index)))
+        _check(call(*args, _raw_stream(index)))
     else:
         with torch.cuda.device(index):
-            _check(call(_raw_stream(index)))
+            _check(call(*args, _raw_stream(index)))
 
 
 def _size(fn, name, v):
@@ -117,8 +117,8 @@ def mx4_quantize(x):
     q = x.new_empty((M, 16 * B), dtype=torch.uint8)
     lds = max(4, -(-B // 4) * 4)
     s = x.new_empty((M, lds), dtype=torch.uint8)
-    _run(index, lambda st: _lib.qmm_mx4_quantize(px, code, ldx, q.data_ptr(), max(16 * B, 16), s.data_ptr(), lds,
-                                                 M, K, st))
+    _run(index, _lib.qmm_mx4_quantize, px, code, ldx, q.data_ptr(), max(16 * B, 16), s.data_ptr(), lds,
+         M, K)
     return q, s if lds == B else s[:, :B]
 
 
@@ -134,7 +134,7 @@ def mx4_dequantize(codes, scales, K=None, out=None, out_dtype=torch.float32):
     index = _one_gpu(fn, codes, scales, out)
     M = codes.shape[0]
     y, code, py, ldy = _result(fn, codes, out, out_dtype, (M, K))
-    _run(index, lambda st: _lib.qmm_mx4_dequantize(pc, ldc, ps, lds, py, code, ldy, M, K, st))
+    _run(index, _lib.qmm_mx4_dequantize, pc, ldc, ps, lds, py, code, ldy, M, K)
     return y
 
 
@@ -167,7 +167,7 @@ def mx4_pack(codes, scales):
     index = _one_gpu(fn, codes, scales)
     E = batch[0] if batch else 1
     W = torch.empty((*batch, mx4_packed_bytes(N, 32 * B)), dtype=torch.uint8, device=codes.device)
-    _run(index, lambda st: _lib.qmm_mx4_pack(pc, ldc, ps, lds, W.data_ptr(), E, N, 32 * B, st))
+    _run(index, _lib.qmm_mx4_pack, pc, ldc, ps, lds, W.data_ptr(), E, N, 32 * B)
     return W
 
 
@@ -195,8 +195,8 @@ def mx4_gemm(x, W, N, sx=None, out=None, out_dtype=torch.float32):
     index = _one_gpu(fn, x, sx, W, out)
     y, ycode, py, ldy = _result(fn, x, out, out_dtype, (M, N))
     ws = x.new_empty(need, dtype=torch.uint8) if need else None
-    _run(index, lambda st: _lib.qmm_mx4_gemm(px, code, ldx, ps, lds, pw, py, ycode, ldy, M, N, K,
-                                             ws.data_ptr() if need else None, need, st))
+    _run(index, _lib.qmm_mx4_gemm, px, code, ldx, ps, lds, pw, py, ycode, ldy, M, N, K,
+         ws.data_ptr() if need else None, need)
     return y
 
 
@@ -247,7 +247,6 @@ def mx4_moe(x, Wg, Wu, Wd, I, logits=None, top_k=None, renormalize=True, ids=Non
     y, ycode, py, ldy = _result(fn, x, out, out_dtype, (T, D))
     need = _lib.qmm_mx4_moe_workspace_bytes(T, D, I, E, k, xcode, ycode)
     ws = x.new_empty(need, dtype=torch.uint8) if need else None
-    _run(index, lambda st: _lib.qmm_mx4_moe(px, xcode, ldx, pg, pu, pd, py, ycode, ldy, T, D, I, E, k, a, pl, lcode,
-                                            ldl, int(bool(renormalize)), pi, isize, pw, wcode,
-                                            ws.data_ptr() if need else None, need, st))
+    _run(index, _lib.qmm_mx4_moe, px, xcode, ldx, pg, pu, pd, py, ycode, ldy, T, D, I, E, k, a, pl, lcode, ldl,
+         int(bool(renormalize)), pi, isize, pw, wcode, ws.data_ptr() if need else None, need)
     return y
