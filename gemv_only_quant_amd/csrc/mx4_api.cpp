@@ -197,7 +197,7 @@ qmm_status qmm_mx4_gemm(const void* x, int x_dtype, int64_t ldx, const uint8_t* 
 size_t qmm_mx4_moe_workspace_bytes(int T, int D, int I, int E, int top_k, int x_dtype, int y_dtype) {
   if (!moe_sizes_ok(T, D, I, E, top_k) || !value_type(x_dtype) || !value_type(y_dtype)) return 0;
   if (T == 0 || D == 0 || I == 0 || E == 0 || top_k == 0) return 0;
-  return qmm::plan_moe(T, D, I, E, top_k, x_dtype, y_dtype).bytes;
+  return qmm::plan_moe(T, D, I, E, top_k, x_dtype).bytes;
 }
 
 qmm_status qmm_mx4_moe(const void* x, int x_dtype, int64_t ldx, const void* Wg, const void* Wu,
@@ -246,7 +246,7 @@ qmm_status qmm_mx4_moe(const void* x, int x_dtype, int64_t ldx, const void* Wg, 
     if (!aligned(ids, (uintptr_t)ids_size) || !aligned(weights, (uintptr_t)type_size(weights_dtype)))
       QMM_REFUSE(QMM_ERR_ARG, "%s: ids and weights must be aligned to their elements", fn);
   }
-  const qmm::MoePlan p = qmm::plan_moe(T, D, I, E, top_k, x_dtype, y_dtype);
+  const qmm::MoePlan p = qmm::plan_moe(T, D, I, E, top_k, x_dtype);
   QMM_CHECK(check_workspace(fn, p.bytes, workspace, workspace_bytes, 256));
   qmm::MoeArgs a{};
   a.x = x, a.x_dtype = x_dtype, a.ldx = ldx;

@@ -79,12 +79,12 @@ struct HeldPlan {
   int groups, range, ranges, per;  // row groups in LDS (0: none), chunks of a row there, ranges of these; tiles of a workgroup
 };
 struct MoePlan {
-  int xparts, hparts;
+  int xparts;
   HeldPlan up, down;
   int Dp, Ip, Dz;
   size_t ids, w, done, x, h, z, bytes;
 };
-MoePlan plan_moe(int T, int D, int I, int E, int top_k, int x_dtype, int y_dtype);
+MoePlan plan_moe(int T, int D, int I, int E, int top_k, int x_dtype);
 hipError_t launch_mx4_moe(const MoeArgs& a, const MoePlan& p, hipStream_t s);
 
 }  // namespace qmm

@@ -5,7 +5,7 @@
 //
 // Bound by reading the weights of the experts that some token chose, once.  The products run on the 16-bit matrix cores: a
 // code times its scale is exact in bf16, whose exponents reach as far as the scales', and an activation of more bits is a
-// sum of bf16 parts (fp16: 2, fp32: 3, exact; h: 2, or 3 for fp32 y), rows of the product beside each other, whose sums are
+// sum of bf16 parts (fp16: 2, fp32 and h: 3, exact), rows of the product beside each other, whose sums are
 // added in fp32.  The other rows are an expert's further tokens, so most of the time parts cost nothing.
 //
 // Launches: the tokens' choices, and x as parts; the first half, h; the second, rows of y of each choice; their sum.  What
@@ -43,6 +43,9 @@ template <int N> __device__ __forceinline__ void parts_of(float v, uint16_t (&p)
   }
 }
 
+// Of h, whatever y's type: the fp32 values as they are.  (2 parts are 16 bits: where nearly equal values of h meet with
+// opposite signs, what is left would be off by up to 2^-16 of them, which a 16-bit y shows.)
+constexpr int kHParts = 3;
 template <int XP> constexpr int kTypeOfParts = XP == 1 ? XBF16 : XP == 2 ? XF16 : YF32;  // of x
 
 // ---- routing, and the activations as parts ------------------------------------
@@ -554,7 +557,7 @@ template <int P, int G> struct HeldSweep {
 
 // ---- first half ----------------------------------------------------------------
 // Column threadIdx.x % 16 of strip t of h, from the waves' sums of row rr, for `place` of token `tok`.
-template <int XP, int HP>
+template <int XP>
 __device__ __forceinline__ void put_hidden(const MoeArgs& g, const MoeBufs& o, const MoeLds& lds, int rr, int t, int tok,
                                            int place, float wt, int Ip) {
   const int col = threadIdx.x % 16;
@@ -564,15 +567,15 @@ __device__ __forceinline__ void put_hidden(const MoeArgs& g, const MoeBufs& o, c
     float d;
     h = act_parts<decltype(a)::value>(gv, &d) * uv * wt;
   });
-  uint16_t p[HP];
-  parts_of<HP>(16 * t + col < g.I ? h : 0.f, p);  // the padding is 0 whatever x is
+  uint16_t p[kHParts];
+  parts_of<kHParts>(16 * t + col < g.I ? h : 0.f, p);  // the padding is 0 whatever x is
   const int row = tok * g.top_k + place, at = operand_order(16 * t + col);
 #pragma unroll
-  for (int q = 0; q < HP; ++q) o.h[((int64_t)q * g.T * g.top_k + row) * Ip + at] = p[q];
+  for (int q = 0; q < kHParts; ++q) o.h[((int64_t)q * g.T * g.top_k + row) * Ip + at] = p[q];
 }
 
 // A workgroup: `per` strips of 16 columns of h of one expert.
-template <int XP, int HP, int G>
+template <int XP, int G>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs g, MoeBufs o, int Dp, int Ip, int pairs, int per) {
   __shared__ MoeLds lds;
   __shared__ int tok[kMoeTokens], place[kMoeTokens];
@@ -610,14 +613,14 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs g, Mo
         if (r0 + RG * i >= members) break;
         meet<G>(lds, acc, i, wave, lane);
         const int rr = threadIdx.x / 16, r = r0 + RG * i + rr;
-        if (rr < RG && r < members) put_hidden<XP, HP>(g, o, lds, rr, t, tok[r], place[r], wt[r], Ip);
+        if (rr < RG && r < members) put_hidden<XP>(g, o, lds, rr, t, tok[r], place[r], wt[r], Ip);
       }
     };
     sweep<XP, G>(rows, members - r0, wave, tile, tiles, chunks, lds.rows[wave], lane, fetch, put);
   }
 }
 
-template <int XP, int HP, int G>
+template <int XP, int G>
 __global__ __launch_bounds__(64 * kHeldWaves) void moe_up_held_kernel(MoeArgs g, MoeBufs o, int Dp, int Ip, int pairs,
                                                                       int per) {
   __shared__ HeldLds lds;
@@ -663,10 +666,10 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_up_held_kernel(MoeArgs g,
             float d;
             h = act_parts<decltype(a)::value>(acc[i][0][q], &d) * acc[i][1][q] * lds.wt[r0 + r];
           });
-          uint16_t p[HP];
-          parts_of<HP>(n < g.I ? h : 0.f, p);  // the padding is 0 whatever x is
+          uint16_t p[kHParts];
+          parts_of<kHParts>(n < g.I ? h : 0.f, p);  // the padding is 0 whatever x is
 #pragma unroll
-          for (int b = 0; b < HP; ++b) o.h[((int64_t)b * g.T * g.top_k + lds.row[r0 + r]) * Ip + operand_order(n)] = p[b];
+          for (int b = 0; b < kHParts; ++b) o.h[((int64_t)b * g.T * g.top_k + lds.row[r0 + r]) * Ip + operand_order(n)] = p[b];
         }
     });
   }
@@ -675,7 +678,7 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_up_held_kernel(MoeArgs g,
 // The same for up to 4 tokens, with their choices made by every workgroup itself (a launch less: one token, 8 of 128 experts
 // of 2048 x 768, 7.3 us for 4 and 7 by two), rows of the product
 // the tokens in their order.  The first workgroup leaves the choices for the second half.
-template <int XT, int XP, int HP, bool VEC>
+template <int XT, int XP, bool VEC>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_few_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int per,
                                                                        int strips_y) {
   __shared__ MoeLds lds;
@@ -718,7 +721,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_few_kernel(MoeArgs g
     const int place = (int)__builtin_ctzll(own);
     float wt = 0.f;
     for (; own != 0; own &= own - 1) wt += ws[p + (int)__builtin_ctzll(own)];
-    put_hidden<XP, HP>(g, o, lds, r, t, r, place, wt, Ip);
+    put_hidden<XP>(g, o, lds, r, t, r, place, wt, Ip);
   });
 }
 
@@ -753,7 +756,7 @@ __device__ __forceinline__ float token_sum(buf_t z, int p0, int k, int Dz, int n
 // A workgroup: `per` times 32 columns of one expert's rows of y.  A token's rows are added in the order of its places: for
 // a few tokens (JOIN) by the last of those columns' workgroups to come, else by another launch (64 tokens, 64 experts of
 // 2048 x 1408: few workgroups would be left with 23 us of additions, the launch takes 5).
-template <int HP, int G, bool JOIN>
+template <int G, bool JOIN>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int Dz, int per) {
   __shared__ MoeLds lds;
   __shared__ int tok[kMoeTokens], place[kMoeTokens];
@@ -781,11 +784,11 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
       tok[r] = lane, place[r] = m.place;
     }
     __syncthreads();
-    constexpr int RG = kRowGroup<HP>;
+    constexpr int RG = kRowGroup<kHParts>;
     static_assert(RG <= 8, "rows that the workgroup's threads take at once");
     for (int r0 = 0; r0 < members; r0 += G * RG) {
-      Parts<HP> rows;
-      part_buffers<HP>(rows.parts, o.h, g.T * k, Ip);
+      Parts<kHParts> rows;
+      part_buffers<kHParts>(rows.parts, o.h, g.T * k, Ip);
       rows.offs = r0 + lane < members ? 2 * (tok[r0 + lane] * k + place[r0 + lane]) * Ip : 0;
       rows.members = members - r0, rows.blocks = blocks, rows.lane = lane, rows.lds = lds.rows[wave];
       if (wave < chunks) rows.request(0, wave);
@@ -796,13 +799,13 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
           meet<G>(lds, acc, i, wave, lane);
           const int rr = threadIdx.x / 32, r = r0 + RG * i + rr, col = threadIdx.x % 32;
           if (rr >= RG || r >= members) continue;
-          const float v = met<HP>(lds, col / 16, rr, col % 16);
+          const float v = met<kHParts>(lds, col / 16, rr, col % 16);
           // past this XCD's L2: another XCD's workgroup may read it
           __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), zb,
                                                 4 * ((tok[r] * k + place[r]) * Dz + 32 * t + col), 0, JOIN ? kCoherent : 0);
         }
       };
-      sweep<HP, G>(rows, members - r0, wave, tile, tiles, chunks, lds.rows[wave], lane, fetch, put);
+      sweep<kHParts, G>(rows, members - r0, wave, tile, tiles, chunks, lds.rows[wave], lane, fetch, put);
     }
   }
   if (!JOIN) return;
@@ -826,11 +829,11 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs g, 
   }
 }
 
-template <int HP, int G>
+template <int G>
 __global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs g, MoeBufs o, int Ip, int pairs, int Dz, int per,
                                                                         int range) {
   __shared__ HeldLds lds;
-  constexpr int RG = kHeldRows<HP>;
+  constexpr int RG = kHeldRows<kHParts>;
   const int lane = threadIdx.x & 63, quad = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const MoeGroup m = group_of(o, (int)blockIdx.y, pairs != 0, g.T, g.top_k, lane);
@@ -851,13 +854,13 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs 
     lds.row[r] = lane * g.top_k + m.place;
   }
   __syncthreads();
-  buf_t parts[HP];
-  part_buffers<HP>(parts, o.h, g.T * g.top_k, Ip);
-  HeldSweep<HP, G> sweep;
+  buf_t parts[kHParts];
+  part_buffers<kHParts>(parts, o.h, g.T * g.top_k, Ip);
+  HeldSweep<kHParts, G> sweep;
   for (int r0 = 0; r0 < members; r0 += G * RG) {
     if (r0 > 0) __syncthreads();
     const int rows = min(members - r0, G * RG), groups = (rows + RG - 1) / RG;
-    hold_rows<HP>(lds, parts, rows, ld, c0, chunks, blocks, wave, lane,
+    hold_rows<kHParts>(lds, parts, rows, ld, c0, chunks, blocks, wave, lane,
                   [&](int r) { return 2 * Ip * __builtin_amdgcn_readfirstlane(lds.row[r0 + r]); },
                   [&] { sweep.begin(tile + wave, tiles, chunks, fetch); });
     sweep.run(lds.rows, ld, groups, tiles, chunks, lane, fetch, [&](int t, const f32x4_t (&acc)[G][2]) {
@@ -879,20 +882,19 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs 
 // 6.8 us, by the next kernel 9.3).
 constexpr int kFewWaves = 16, kFewLds = 140 << 10;
 
-template <int HP>
 __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g, MoeBufs o, uint32_t inverse, int step_x,
                                                                       int step_c) {
   __shared__ __align__(16) char hs[kFewLds];  // h's rows, of each its parts, chunks kRowBytes apart
   __shared__ float sums[kFewWaves][16][17];
   const int lane = threadIdx.x & 63, k = g.top_k, places = g.T * k;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  static_assert(HP <= 4, "a row's parts are rows of the product");
+  static_assert(kHParts <= 4, "a row's parts are rows of the product");
   const int l16 = lane & 15, quad = lane >> 4, strip = (int)blockIdx.x;
   const int chunks = mx4_chunks(g.I), blocks = mx4_blocks(g.I);
   const int id = lane < places ? o.ids[lane] : -1;
   // h to LDS, a chunk of a row's part a turn
   constexpr int HELD = 4;
-  const int turns = places * HP * chunks;
+  const int turns = places * kHParts * chunks;
   u32x4_t v[HELD];
   auto get = [&](int t) { return *reinterpret_cast<const u32x4_t*>(o.h + (int64_t)512 * t + 8 * lane); };
   auto put = [&](int t, const u32x4_t& x) { *reinterpret_cast<u32x4_t*>(hs + t * kRowBytes + 16 * lane) = x; };
@@ -945,7 +947,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g,
     // row l16 is part l16 / 4 of token l16 % 4, its first place with this expert
     const uint64_t same = __ballot(id == e);
     const int token = l16 % 4, part = l16 / 4;
-    const uint32_t own = token < g.T && part < HP ? (uint32_t)(same >> (token * k)) & (uint32_t)((uint64_t(1) << k) - 1) : 0u;
+    const uint32_t own = token < g.T && part < kHParts ? (uint32_t)(same >> (token * k)) & (uint32_t)((uint64_t(1) << k) - 1) : 0u;
     const int row = own == 0 ? 0 : part * places + token * k + __builtin_ctz(own);
     const char* from = own == 0 ? hs : hs + (row * chunks + c) * kRowBytes + 16 * quad;
 #pragma unroll
@@ -977,7 +979,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g,
   if (m >= g.T || n >= g.D) return;
   float y = 0.f;
 #pragma unroll
-  for (int i = HP; i-- > 0;)
+  for (int i = kHParts; i-- > 0;)
 #pragma unroll
     for (int q = 0; q < kFewWaves; ++q) y += sums[q][4 * i + m][threadIdx.x % 16];
   with_y(g.y, g.y_dtype, [&](auto* yt) {
@@ -1024,10 +1026,9 @@ static HeldPlan plan_held(int T, int top_k, int E, int RG, int chunks, bool spli
   return p.per < least ? HeldPlan{} : p;
 }
 
-MoePlan plan_moe(int T, int D, int I, int E, int top_k, int x_dtype, int y_dtype) {
+MoePlan plan_moe(int T, int D, int I, int E, int top_k, int x_dtype) {
   MoePlan p{};
   p.xparts = x_dtype == YF32 ? 3 : x_dtype == XF16 ? 2 : 1;
-  p.hparts = y_dtype == YF32 ? 3 : 2;
   p.Dp = (int)round_up(D, 512);
   p.Ip = (int)round_up(I, 512);
   p.Dz = (int)round_up(D, 32);
@@ -1035,7 +1036,7 @@ MoePlan plan_moe(int T, int D, int I, int E, int top_k, int x_dtype, int y_dtype
   // (held in LDS or not, 18 tiles a workgroup: 45 and 39 us; 22 tiles: 41 and 48)
   p.up = plan_held(T, top_k, E, rows(p.xparts), mx4_chunks(D), false, 2 * mx4_blocks(I), 20);
   // (10 tiles a workgroup: 23 us and 5 of additions, else 23; 16 tiles: 27 and 5, else 36 and 5; 22 tiles: 28 and 5, else 49)
-  p.down = plan_held(T, top_k, E, rows(p.hparts), mx4_chunks(I), true, p.Dz / 32, 14);
+  p.down = plan_held(T, top_k, E, rows(kHParts), mx4_chunks(I), true, p.Dz / 32, 14);
   const int64_t z = (int64_t)T * top_k * p.Dz * 4;
   if (p.down.ranges > 1 && z * p.down.ranges > kRangesBytes) p.down = HeldPlan{};
   size_t at = 0;
@@ -1048,13 +1049,13 @@ MoePlan plan_moe(int T, int D, int I, int E, int top_k, int x_dtype, int y_dtype
   p.w = take((size_t)T * top_k * 4);
   p.done = take((size_t)p.Dz / 32 * 4);
   p.x = take((size_t)p.xparts * T * p.Dp * 2);
-  p.h = take((size_t)p.hparts * T * top_k * p.Ip * 2);
+  p.h = take((size_t)kHParts * T * top_k * p.Ip * 2);
   p.z = take((size_t)z * (p.down.ranges > 1 ? p.down.ranges : 1));
   p.bytes = at;
   return p;
 }
 
-template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
+template <int XP> static hipError_t moe_t(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
   // a workgroup for each expert, or for each place of the tokens' choices if these are fewer; of more tiles than
   // about 3 rounds of workgroups (2 on a CU) would be, a workgroup takes several in turn
   const int pairs = a.T * a.top_k < a.E, slots = pairs ? a.T * a.top_k : a.E;
@@ -1068,18 +1069,18 @@ template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePla
   if (a.T <= 4) {
     constexpr int XT = kTypeOfParts<XP>;
     const bool vec = vec8_ok(a.x, a.ldx, a.D, a.x_dtype == YF32 ? 4 : 2) && a.D % 8 == 0;
-    e = launch_kernel(vec ? moe_up_few_kernel<XT, XP, HP, true> : moe_up_few_kernel<XT, XP, HP, false>, dim3((unsigned)((up + per_few - 1) / per_few), (unsigned)slots),
+    e = launch_kernel(vec ? moe_up_few_kernel<XT, XP, true> : moe_up_few_kernel<XT, XP, false>, dim3((unsigned)((up + per_few - 1) / per_few), (unsigned)slots),
                       dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs, per_few, gd);
   } else {
     e = launch_kernel(moe_route_kernel<XP>, dim3((unsigned)((a.T + 3) / 4 + (xg < 256 ? xg : 256))), dim3(256), s, a, o, gd, p.Dp);
     if (e != hipSuccess) return e;
     const HeldPlan& held = p.up;
     if (held.groups != 0) {
-      e = launch_kernel(held.groups == 1 ? moe_up_held_kernel<XP, HP, 1> : moe_up_held_kernel<XP, HP, 2>,
+      e = launch_kernel(held.groups == 1 ? moe_up_held_kernel<XP, 1> : moe_up_held_kernel<XP, 2>,
                         dim3((unsigned)((up + held.per - 1) / held.per), (unsigned)slots), dim3(64 * kHeldWaves), s, a, o, p.Dp,
                         p.Ip, pairs, held.per);
     } else {
-      e = launch_kernel(a.T <= kRowGroup<XP> ? moe_up_kernel<XP, HP, 1> : moe_up_kernel<XP, HP, 2>,
+      e = launch_kernel(a.T <= kRowGroup<XP> ? moe_up_kernel<XP, 1> : moe_up_kernel<XP, 2>,
                         dim3((unsigned)((up + per_up - 1) / per_up), (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Dp, p.Ip,
                         pairs, per_up);
     }
@@ -1087,18 +1088,18 @@ template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePla
   if (e != hipSuccess) return e;
   const int places = a.T * a.top_k;
   const int chunks = mx4_chunks(a.I);
-  if (a.T <= 4 && places <= 64 && (int64_t)places * HP * chunks * kRowBytes <= kFewLds)
-    return launch_kernel(moe_down_few_kernel<HP>, dim3((unsigned)((a.D + 15) / 16)), dim3(64 * kFewWaves), s, a, o,
+  if (a.T <= 4 && places <= 64 && (int64_t)places * kHParts * chunks * kRowBytes <= kFewLds)
+    return launch_kernel(moe_down_few_kernel, dim3((unsigned)((a.D + 15) / 16)), dim3(64 * kFewWaves), s, a, o,
                          (uint32_t)((65536 + chunks - 1) / chunks), kFewWaves / chunks, kFewWaves % chunks);
   const HeldPlan& held = p.down;
   const bool join = held.groups == 0 && a.T <= 16;
   if (held.groups != 0)
-    e = launch_kernel(held.groups == 1 ? moe_down_held_kernel<HP, 1> : moe_down_held_kernel<HP, 2>,
+    e = launch_kernel(held.groups == 1 ? moe_down_held_kernel<1> : moe_down_held_kernel<2>,
                       dim3((unsigned)((down + held.per - 1) / held.per), (unsigned)slots, (unsigned)held.ranges), dim3(64 * kHeldWaves), s, a,
                       o, p.Ip, pairs, p.Dz, held.per, held.range);
   else
-    e = launch_kernel(!join ? moe_down_kernel<HP, 2, false>
-                            : a.T <= kRowGroup<HP> ? moe_down_kernel<HP, 1, true> : moe_down_kernel<HP, 2, true>,
+    e = launch_kernel(!join ? moe_down_kernel<2, false>
+                            : a.T <= kRowGroup<kHParts> ? moe_down_kernel<1, true> : moe_down_kernel<2, true>,
                       dim3((unsigned)gd, (unsigned)slots), dim3(64 * kMoeWaves), s, a, o, p.Ip, pairs, p.Dz, per_down);
   if (e != hipSuccess || join) return e;
   const int columns = (a.D + 255) / 256;
@@ -1106,9 +1107,6 @@ template <int XP, int HP> static hipError_t moe_t(const MoeArgs& a, const MoePla
                        held.groups != 0 ? held.ranges : 1);
 }
 
-template <int XP> static hipError_t moe_h(const MoeArgs& a, const MoePlan& p, const MoeBufs& o, hipStream_t s) {
-  return p.hparts == 3 ? moe_t<XP, 3>(a, p, o, s) : moe_t<XP, 2>(a, p, o, s);
-}
 
 hipError_t launch_mx4_moe(const MoeArgs& a, const MoePlan& p, hipStream_t s) {
   char* ws = static_cast<char*>(a.ws);
@@ -1120,10 +1118,10 @@ hipError_t launch_mx4_moe(const MoeArgs& a, const MoePlan& p, hipStream_t s) {
   o.h = reinterpret_cast<uint16_t*>(ws + p.h);
   o.z = reinterpret_cast<float*>(ws + p.z);
   switch (p.xparts) {
-    case 1: return moe_h<1>(a, p, o, s);
-    case 2: return moe_h<2>(a, p, o, s);
+    case 1: return moe_t<1>(a, p, o, s);
+    case 2: return moe_t<2>(a, p, o, s);
   }
-  return moe_h<3>(a, p, o, s);
+  return moe_t<3>(a, p, o, s);
 }
 
 }  // namespace qmm

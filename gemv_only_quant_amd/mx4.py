@@ -206,7 +206,7 @@ def mx4_moe(x, Wg, Wu, Wd, I, logits=None, top_k=None, renormalize=True, ids=Non
     Wg and Wu are E packed weights (I, D), Wd E packed weights (D, I), each (E, bytes) as mx4_pack makes it.
     The experts are the top_k largest of logits (T, E), weighted by the softmax over them (renormalize) or over
     all; or ids (T, k) int32 / int64 with weights (T, k): an id outside [0, E) counts for nothing.  Activations
-    are not quantized.  y is `out`, else a new tensor of out_dtype."""
+    are not quantized, and what lies between the halves is fp32.  y is `out`, else a new tensor of out_dtype."""
     fn = "qmm_mx4_moe"
     _size(fn, "I", I)
     a = _act(fn, act)

@@ -109,8 +109,8 @@ QMM_API size_t qmm_mx4_moe_workspace_bytes(int T, int D, int I, int E, int top_k
  * qmm_mx4_moe: y (T, D) of y_dtype for T <= QMM_MX4_MAX_TOKENS tokens x (T, D)
  * of x_dtype (QMM_F32, QMM_F16, QMM_BF16).  Wg and Wu are E packed weights (I, D)
  * one after the other, Wd E packed weights (D, I).  The activations are not
- * quantized: products are of x's own values and the weights', h's of fp32 values
- * rounded to 24 bits (fp32 y) or 16 bits (others); sums are fp32.
+ * quantized: products are of x's own values and the weights', then of h's in fp32, whatever
+ * y's type; sums are fp32.
  *   logits (T, E) of logits_dtype, not NULL: each token's top_k largest (the
  *     lower index of equal ones; NaN above everything), weighted by the softmax
  *     over them (renormalize 1) or over all (0).  A logit of minus infinity is
