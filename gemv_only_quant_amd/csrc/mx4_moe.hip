@@ -439,10 +439,21 @@ template <int P> __device__ __forceinline__ float met(const MoeLds& lds, int p, 
 
 // Where an expert's rows fit LDS whole and there are tiles enough, a wave has whole tiles instead: nothing is left to
 // add across waves, and no barrier stands between a wave and its next weights.
-constexpr int kHeldWaves = 12, kHeldBytes = 32 * (4096 + 16);
-constexpr int held_chunks(int groups) { return (kHeldBytes / (16 * groups) - 16) / 1024; }  // of a row
+constexpr int kHeldWaves = 12, kHeldBytes = 30 * (5 * 1024 + 16);
 constexpr int64_t kRangesBytes = 1 << 28;  // of z, if more than one range of chunks is held
-template <int P> constexpr int kHeldRows = P == 1 ? 16 : P == 2 ? 8 : 4;  // a product's rows, of each its P parts
+// A product's rows, of each its P parts, and how many such groups there may be.
+template <int P> constexpr int kHeldRows = P == 1 ? 16 : P == 2 ? 8 : 5;
+template <int P> constexpr int kHeldGroups = P == 3 ? 3 : 2;
+template <int P> constexpr int held_chunks(int groups) { return (kHeldBytes / (P * kHeldRows<P> * groups) - 16) / 1024; }  // of a row
+// Part q of row r of a group is this row of the product.  Lanes of a quad have rows 4 quad .. + 3 of the sums: 3 parts of rows
+// 0 to 3 lie in as many quads, those of row 4 in the last quad beside each other.
+template <int P> __device__ __forceinline__ int held_slot(int r, int q) {
+  return P == 3 ? (r == 4 ? 12 + q : 4 * q + r) : kHeldRows<P> * q + r;
+}
+// The row whose whole sum a lane has at place i of its four; kHeldRows or more: none.
+template <int P> __device__ __forceinline__ int held_row(int quad, int i) {
+  return P == 3 ? (quad == 0 ? i : quad == 3 && i == 0 ? 4 : kHeldRows<P>) : 4 * quad + i;
+}
 
 struct HeldLds {
   char rows[kHeldBytes];
@@ -458,7 +469,7 @@ __device__ __forceinline__ void hold_rows(HeldLds& lds, const buf_t (&parts)[P],
                                           int blocks, int wave, int lane, Offset&& offset, First&& first) {
   constexpr int RG = kHeldRows<P>, AHEAD = 4;
   const int turns = rows * P * chunks;
-  // t / chunks, exact for the 32 rows of 8 chunks that there may be
+  // t / chunks, exact for what fits LDS (fewer than 2^16 / chunks turns)
   const uint32_t inverse = 65535u / (uint32_t)chunks + 1;
   auto row_of = [&](int t) { return (int)((uint32_t)t * inverse >> 16); };
   u32x4_t v[AHEAD];
@@ -474,7 +485,7 @@ __device__ __forceinline__ void hold_rows(HeldLds& lds, const buf_t (&parts)[P],
   };
   auto put = [&](int t, const u32x4_t& x) {
     const int r = row_of(t), m = r / P, q = r % P, c = t - r * chunks;
-    const int to = (16 * (m / RG) + RG * q + m % RG) * ld + 1024 * c + 16 * lane;
+    const int to = (P * RG * (m / RG) + held_slot<P>(m % RG, q)) * ld + 1024 * c + 16 * lane;
     if (t < turns) *reinterpret_cast<u32x4_t*>(lds.rows + to) = x;
   };
   for (int t = wave; t == wave || t < turns; t += AHEAD * kHeldWaves) {
@@ -504,7 +515,8 @@ template <int P, int G> struct HeldSweep {
   __device__ __forceinline__ void run(const char* rows, int ld, int groups, int tiles, int chunks, int lane, Fetch&& fetch,
                                       Put&& put) {
     f32x4_t acc[G][2] = {};
-    const char* from0 = rows + (lane & 15) * ld + 16 * (lane >> 4);
+    constexpr int ROWS = P * kHeldRows<P>;
+    const char* from0 = rows + min(lane & 15, ROWS - 1) * ld + 16 * (lane >> 4);
     auto use = [&](const MoeChunk (&m)[2]) {
       const char* from = from0 + 1024 * c;
 #pragma unroll
@@ -517,7 +529,7 @@ template <int P, int G> struct HeldSweep {
 #pragma unroll
           for (int g = 0; g < G; ++g) {
             if (g > 0 && g >= groups) break;
-            const char* at = from + 16 * g * ld + 256 * j + 64 * i;
+            const char* at = from + ROWS * g * ld + 256 * j + 64 * i;
             const bf16x8_t a = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t*>(at));
             acc[g][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b0, acc[g][0], 0, 0, 0);
             acc[g][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b1, acc[g][1], 0, 0, 0);
@@ -529,13 +541,16 @@ template <int P, int G> struct HeldSweep {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
 #pragma unroll
-          for (int p = 0; p < 2; ++p)
+          for (int p = 0; p < 2; ++p) {
+            const float last = acc[g][p][0] + (acc[g][p][1] + acc[g][p][2]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float v = acc[g][p][r];
               if (P == 2) acc[g][p][r] = v + __shfl_xor(v, 32, 64);
               if (P == 3) acc[g][p][r] = v + (__shfl(v, (lane & 15) + 16, 64) + __shfl(v, (lane & 15) + 32, 64));
             }
+            if (P == 3 && lane >= 48) acc[g][p][0] = last;
+          }
         }
         put(t, acc);
 #pragma unroll
@@ -659,7 +674,7 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_up_held_kernel(MoeArgs g,
       for (int i = 0; i < G; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int rr = 4 * quad + q, r = RG * i + rr;
+          const int rr = held_row<XP>(quad, q), r = RG * i + rr;
           if (rr >= RG || r >= rows) continue;
           float h = 0.f;
           with_act(g.act, [&](auto a) {
@@ -868,7 +883,7 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs 
       for (int i = 0; i < G; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int rr = 4 * quad + q, r = RG * i + rr;
+          const int rr = held_row<kHParts>(quad, q), r = RG * i + rr;
           if (rr >= RG || r >= rows) continue;
           float* z = o.z + ((int64_t)blockIdx.z * g.T * g.top_k + lds.row[r0 + r]) * Dz + 32 * t + l16;
           z[0] = acc[i][0][q], z[16] = acc[i][1][q];
@@ -1006,17 +1021,22 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs g, MoeBufs o, int
 }
 
 // ---------------------------------------------------------------- host side
-// Whether workgroups, one on each CU, hold an expert's rows, and of how many row groups: 0 not.  RG: tokens of a group;
-// `split`: whether they may hold a range of a row's chunks; `least`: tiles that each has, else not.  Taken for what tokens
-// that choose evenly would choose.
-static HeldPlan plan_held(int T, int top_k, int E, int RG, int chunks, bool split, int tiles, int least) {
+// Whether workgroups, one on each CU, hold an expert's rows, and of how many row groups: 0 not.  `split`: whether they may
+// hold a range of a row's chunks; `least`: tiles that each has, else not.  Taken for what tokens that choose evenly would
+// choose: groups for all but a few experts' rows, and more where they cost no further range (an expert with more rows has
+// its weights read again for each so many).
+template <int P> static HeldPlan plan_held(int T, int top_k, int E, int chunks, bool split, int tiles, int least) {
+  constexpr int RG = kHeldRows<P>, MOST = kHeldGroups<P>;
   float none = 1.f;  // (given experts may be more than there are)
   for (int t = 0; t < T; ++t) none *= 1.f - (float)(top_k < E ? top_k : E) / (float)E;
   const float chosen = (float)E * (1.f - none), mean = (float)(T * top_k) / chosen;
   HeldPlan p{};
-  const bool one = T <= RG || mean + 2.f * sqrtf(mean) <= (float)RG;
-  p.groups = one && (T <= RG || chunks > held_chunks(2)) ? 1 : 2;
-  p.ranges = (chunks + held_chunks(p.groups) - 1) / held_chunks(p.groups);
+  const float rows = fminf((float)T, mean + 2.f * sqrtf(mean));
+  p.groups = 1;
+  while (p.groups < MOST && rows > (float)(RG * p.groups)) ++p.groups;
+  while (p.groups < MOST && T > RG * p.groups && chunks <= held_chunks<P>(p.groups + 1)) ++p.groups;
+  const int most = held_chunks<P>(p.groups);
+  p.ranges = (chunks + most - 1) / most;
   if (p.ranges > 1 && !split) return HeldPlan{};
   p.range = (chunks + p.ranges - 1) / p.ranges;
   p.ranges = (chunks + p.range - 1) / p.range;
@@ -1032,11 +1052,11 @@ MoePlan plan_moe(int T, int D, int I, int E, int top_k, int x_dtype) {
   p.Dp = (int)round_up(D, 512);
   p.Ip = (int)round_up(I, 512);
   p.Dz = (int)round_up(D, 32);
-  auto rows = [](int parts) { return parts == 1 ? kHeldRows<1> : parts == 2 ? kHeldRows<2> : kHeldRows<3>; };
   // (held in LDS or not, 18 tiles a workgroup: 45 and 39 us; 22 tiles: 41 and 48)
-  p.up = plan_held(T, top_k, E, rows(p.xparts), mx4_chunks(D), false, 2 * mx4_blocks(I), 20);
+  const auto plan_up = p.xparts == 1 ? plan_held<1> : p.xparts == 2 ? plan_held<2> : plan_held<3>;
+  p.up = plan_up(T, top_k, E, mx4_chunks(D), false, 2 * mx4_blocks(I), 20);
   // (10 tiles a workgroup: 23 us and 5 of additions, else 23; 16 tiles: 27 and 5, else 36 and 5; 22 tiles: 28 and 5, else 49)
-  p.down = plan_held(T, top_k, E, rows(kHParts), mx4_chunks(I), true, p.Dz / 32, 14);
+  p.down = plan_held<kHParts>(T, top_k, E, mx4_chunks(I), true, p.Dz / 32, 14);
   const int64_t z = (int64_t)T * top_k * p.Dz * 4;
   if (p.down.ranges > 1 && z * p.down.ranges > kRangesBytes) p.down = HeldPlan{};
   size_t at = 0;
@@ -1076,7 +1096,7 @@ template <int XP> static hipError_t moe_t(const MoeArgs& a, const MoePlan& p, co
     if (e != hipSuccess) return e;
     const HeldPlan& held = p.up;
     if (held.groups != 0) {
-      e = launch_kernel(held.groups == 1 ? moe_up_held_kernel<XP, 1> : moe_up_held_kernel<XP, 2>,
+      e = launch_kernel(held.groups == 1 ? moe_up_held_kernel<XP, 1> : held.groups == 2 ? moe_up_held_kernel<XP, 2> : moe_up_held_kernel<XP, kHeldGroups<XP>>,
                         dim3((unsigned)((up + held.per - 1) / held.per), (unsigned)slots), dim3(64 * kHeldWaves), s, a, o, p.Dp,
                         p.Ip, pairs, held.per);
     } else {
@@ -1094,7 +1114,7 @@ template <int XP> static hipError_t moe_t(const MoeArgs& a, const MoePlan& p, co
   const HeldPlan& held = p.down;
   const bool join = held.groups == 0 && a.T <= 16;
   if (held.groups != 0)
-    e = launch_kernel(held.groups == 1 ? moe_down_held_kernel<1> : moe_down_held_kernel<2>,
+    e = launch_kernel(held.groups == 1 ? moe_down_held_kernel<1> : held.groups == 2 ? moe_down_held_kernel<2> : moe_down_held_kernel<kHeldGroups<kHParts>>,
                       dim3((unsigned)((down + held.per - 1) / held.per), (unsigned)slots, (unsigned)held.ranges), dim3(64 * kHeldWaves), s, a,
                       o, p.Ip, pairs, p.Dz, held.per, held.range);
   else

@@ -17,7 +17,9 @@ pytestmark = pytest.mark.gpu
 FORMS = [(1, 64, 64, 4, 2), (4, 72, 96, 40, 2), (4, 1032, 700, 40, 8), (4, 40, 2600, 20, 5), (5, 100, 77, 6, 3), (8, 700, 515, 5, 1),
          (16, 256, 128, 8, 2), (33, 96, 1040, 4, 4), (64, 130, 330, 300, 8), (64, 460, 40, 300, 8), (64, 460, 330, 260, 8),
          (16, 460, 330, 256, 32), (8, 460, 330, 256, 32), (5, 460, 330, 300, 32), (4, 897, 650, 128, 32),
-         (64, 2100, 330, 260, 8), (64, 460, 2100, 260, 8), (20, 4000, 330, 300, 32), (16, 900, 9000, 40, 8)]
+         (64, 2100, 330, 260, 8), (64, 460, 2100, 260, 8), (20, 4000, 330, 300, 32), (16, 900, 9000, 40, 8),
+         # few tokens whose h fits LDS in two turns, of as many chunks and of one less; three groups and ranges
+         (3, 520, 768, 40, 8), (1, 72, 14336, 4, 2), (1, 72, 13500, 4, 2), (32, 900, 5000, 24, 8)]
 
 
 def run(t, out):
