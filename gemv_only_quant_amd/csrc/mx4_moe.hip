@@ -892,13 +892,15 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs 
   }
 }
 
-// The same for up to 4 tokens and 64 choices whose h fits LDS: a workgroup has 16 columns of y whole, its 16 waves taking
+// The same for up to 4 tokens and 64 choices whose h fits LDS, at once or in two turns: a workgroup has 16 columns of y whole, its 16 waves taking
 // chunks of all chosen experts in turn; nothing is left to add across workgroups (one token, 8 of 128 experts of 2048 x 768:
 // 6.8 us, by the next kernel 9.3).
 constexpr int kFewWaves = 16, kFewLds = 140 << 10;
 
-__global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g, MoeBufs o, uint32_t inverse, int step_x,
-                                                                      int step_c) {
+// `range` chunks of a row are in LDS at once: all, or (TWICE) half of them.
+template <bool TWICE>
+__global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g, MoeBufs o, int range, uint32_t inverse,
+                                                                      int step_x, int step_c) {
   __shared__ __align__(16) char hs[kFewLds];  // h's rows, of each its parts, chunks kRowBytes apart
   __shared__ float sums[kFewWaves][16][17];
   const int lane = threadIdx.x & 63, k = g.top_k, places = g.T * k;
@@ -907,30 +909,39 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g,
   const int l16 = lane & 15, quad = lane >> 4, strip = (int)blockIdx.x;
   const int chunks = mx4_chunks(g.I), blocks = mx4_blocks(g.I);
   const int id = lane < places ? o.ids[lane] : -1;
-  // h to LDS, a chunk of a row's part a turn
+  // h to LDS, a chunk of a row's part a turn (what lies past a row's last chunk counts for nothing)
   constexpr int HELD = 4;
-  const int turns = places * kHParts * chunks;
+  const int turns = places * kHParts * range;
   u32x4_t v[HELD];
-  auto get = [&](int t) { return *reinterpret_cast<const u32x4_t*>(o.h + (int64_t)512 * t + 8 * lane); };
+  auto get = [&](int t, int c0) {
+    int at = t;
+    if (TWICE) {
+      const int row = (int)((uint32_t)t * inverse >> 16);
+      at = row * chunks + min(c0 + t - row * range, chunks - 1);
+    }
+    return *reinterpret_cast<const u32x4_t*>(o.h + (int64_t)512 * at + 8 * lane);
+  };
   auto put = [&](int t, const u32x4_t& x) { *reinterpret_cast<u32x4_t*>(hs + t * kRowBytes + 16 * lane) = x; };
-  int t = wave;
+  auto first_turns = [&](int c0) {
 #pragma unroll
-  for (int i = 0; i < HELD; ++i)
-    if (t + i * kFewWaves < turns) v[i] = get(t + i * kFewWaves);
+    for (int i = 0; i < HELD; ++i)
+      if (wave + i * kFewWaves < turns) v[i] = get(wave + i * kFewWaves, c0);
+  };
+  first_turns(0);
   __builtin_amdgcn_sched_barrier(0);
   // the places whose expert no earlier one has
   bool first = id >= 0;
   for (int p = 0; p + 1 < places; ++p) first = first && !(p < lane && __builtin_amdgcn_readlane(id, p) == id);
   const uint64_t firsts = __ballot(first);
   const int rank = __popcll(firsts & ((uint64_t(1) << lane) - 1)), experts = __popcll(firsts);
-  // A wave's units: chunk c of the x-th chosen expert, the kFewWaves-th next one each time.  (Without divisions: step_x and
-  // step_c are kFewWaves over chunks, and its remainder.)
+  // A wave's units: chunk c0 + c of the x-th chosen expert, the kFewWaves-th next one each time, of the chunks from c0 on that are
+  // in LDS.  (Without divisions: step_x and step_c are kFewWaves over range, and its remainder.)
   struct Unit {
-    int x, c;
+    int x, c, c0;
   };
   auto after = [&](const Unit& u) {
-    Unit n = {u.x + step_x, u.c + step_c};
-    if (n.c >= chunks) n.c -= chunks, ++n.x;
+    Unit n = {u.x + step_x, u.c + step_c, u.c0};
+    if (n.c >= range) n.c -= range, ++n.x;
     return n;
   };
   auto expert = [&](const Unit& u) {
@@ -938,36 +949,39 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g,
   };
   auto request = [&](MoeChunk& w, const Unit& u) {
     const uint8_t* p = nullptr;
-    if (u.x < experts)
+    if (u.x < experts && (!TWICE || u.c0 + u.c < chunks))
       p = g.wd + (int64_t)expert(u) * mx4_weight_bytes(g.D, g.I) + (int64_t)strip * mx4_strip_bytes(g.I) +
-          (int64_t)kChunkBytes * u.c;
-    load_chunk(w, p, blocks - 16 * u.c, lane);
+          (int64_t)kChunkBytes * (u.c0 + u.c);
+    load_chunk(w, p, blocks - 16 * (u.c0 + u.c), lane);
   };
   MoeChunk w[2];
-  Unit u0, u1;
-  u0.x = (int)((uint32_t)wave * inverse >> 16), u0.c = wave - u0.x * chunks;
-  u1 = after(u0);
+  Unit begin, u0, u1;
+  begin.x = (int)((uint32_t)wave * inverse >> 16), begin.c = wave - begin.x * range, begin.c0 = 0;
+  u0 = begin, u1 = after(u0);
   request(w[0], u0);
   request(w[1], u1);
   __builtin_amdgcn_sched_barrier(0);
+  auto rest = [&](int c0) {
 #pragma unroll
-  for (int i = 0; i < HELD; ++i)
-    if (t + i * kFewWaves < turns) put(t + i * kFewWaves, v[i]);
-  for (t += HELD * kFewWaves; t < turns; t += kFewWaves) put(t, get(t));
-  __syncthreads();
+    for (int i = 0; i < HELD; ++i)
+      if (wave + i * kFewWaves < turns) put(wave + i * kFewWaves, v[i]);
+    for (int t = wave + HELD * kFewWaves; t < turns; t += kFewWaves) put(t, get(t, c0));
+    __syncthreads();
+  };
+  rest(0);
 
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
   auto use = [&](const MoeChunk& m, const Unit& u) {
-    const int c = u.c, e = expert(u);
+    const int e = expert(u);
     // row l16 is part l16 / 4 of token l16 % 4, its first place with this expert
     const uint64_t same = __ballot(id == e);
     const int token = l16 % 4, part = l16 / 4;
     const uint32_t own = token < g.T && part < kHParts ? (uint32_t)(same >> (token * k)) & (uint32_t)((uint64_t(1) << k) - 1) : 0u;
     const int row = own == 0 ? 0 : part * places + token * k + __builtin_ctz(own);
-    const char* from = own == 0 ? hs : hs + (row * chunks + c) * kRowBytes + 16 * quad;
+    const char* from = own == 0 ? hs : hs + (row * range + u.c) * kRowBytes + 16 * quad;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bool ok = own != 0 && 4 * quad + j < blocks - 16 * c;
+      const bool ok = own != 0 && 4 * quad + j < blocks - 16 * (u.c0 + u.c);
       const float sc = scale_f32((m.s >> (8 * j)) & 255);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -978,14 +992,23 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeArgs g,
       }
     }
   };
-  while (u0.x < experts) {
-    use(w[0], u0);
-    u0 = after(u1);
-    request(w[0], u0);
-    if (u1.x >= experts) break;
-    use(w[1], u1);
-    u1 = after(u0);
-    request(w[1], u1);
+  // pairs of units, the next pair's weights on their way; after the last of some chunks the first of the next
+  for (;;) {
+    Unit n0 = after(u1);
+    const bool end = n0.x >= experts;
+    if (TWICE && end) n0 = begin, n0.c0 = u0.c0 + range;
+    const Unit n1 = after(n0);
+    if (u0.x < experts) use(w[0], u0);
+    request(w[0], n0);
+    if (u1.x < experts) use(w[1], u1);
+    request(w[1], n1);
+    if (end) {
+      if (!TWICE || n0.c0 >= chunks) break;
+      first_turns(n0.c0);
+      __syncthreads();
+      rest(n0.c0);
+    }
+    u0 = n0, u1 = n1;
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) sums[wave][4 * quad + r][l16] = acc[r];
@@ -1108,9 +1131,13 @@ template <int XP> static hipError_t moe_t(const MoeArgs& a, const MoePlan& p, co
   if (e != hipSuccess) return e;
   const int places = a.T * a.top_k;
   const int chunks = mx4_chunks(a.I);
-  if (a.T <= 4 && places <= 64 && (int64_t)places * kHParts * chunks * kRowBytes <= kFewLds)
-    return launch_kernel(moe_down_few_kernel, dim3((unsigned)((a.D + 15) / 16)), dim3(64 * kFewWaves), s, a, o,
-                         (uint32_t)((65536 + chunks - 1) / chunks), kFewWaves / chunks, kFewWaves % chunks);
+  // (in two turns and by the other kernels, us: 3 tokens, 8 of 128 experts of 2048 x 768, 26.6 and 30.6; 4 tokens 31.1 and
+  // 30.7; one token, 2 of 8 experts of 4096 x 14336, 41.3 and 42.0)
+  auto fits = [&](int range) { return (int64_t)places * kHParts * range * kRowBytes <= kFewLds; };
+  const int range = fits(chunks) ? chunks : (chunks + 1) / 2;
+  if (a.T <= 4 && places <= 64 && fits(range))
+    return launch_kernel(range == chunks ? moe_down_few_kernel<false> : moe_down_few_kernel<true>, dim3((unsigned)((a.D + 15) / 16)), dim3(64 * kFewWaves), s, a, o, range,
+                         (uint32_t)((65536 + range - 1) / range), kFewWaves / range, kFewWaves % range);
   const HeldPlan& held = p.down;
   const bool join = held.groups == 0 && a.T <= 16;
   if (held.groups != 0)
