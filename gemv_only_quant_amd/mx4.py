@@ -70,6 +70,12 @@ def _blocks(K):
     return -(-K // 32)
 
 
+def _values(B):
+    """Values of rows of B blocks of codes: all of them count, but the library's sizes end at 2^20 - 1, whose
+    last block is whole too."""
+    return 32 * B - (B == 1 << 15)
+
+
 def _bytes_matrix(fn, name, t, shape=None):
     """As _matrix, for bytes."""
     if isinstance(t, torch.Tensor) and t.dtype != torch.uint8:
@@ -166,8 +172,8 @@ def mx4_pack(codes, scales):
     pc, ldc, ps, lds, B = _coded(fn, codes, scales)
     index = _one_gpu(fn, codes, scales)
     E = batch[0] if batch else 1
-    W = torch.empty((*batch, mx4_packed_bytes(N, 32 * B)), dtype=torch.uint8, device=codes.device)
-    _run(index, _lib.qmm_mx4_pack, pc, ldc, ps, lds, W.data_ptr(), E, N, 32 * B)
+    W = torch.empty((*batch, mx4_packed_bytes(N, _values(B))), dtype=torch.uint8, device=codes.device)
+    _run(index, _lib.qmm_mx4_pack, pc, ldc, ps, lds, W.data_ptr(), E, N, _values(B))
     return W
 
 
@@ -182,7 +188,7 @@ def mx4_gemm(x, W, N, sx=None, out=None, out_dtype=torch.float32):
         if sx is None:
             _refuse(fn, "uint8 x needs its scales (sx)")
         px, ldx, ps, lds, B = _coded(fn, x, sx)
-        code, K = QMM_MX4, 32 * B
+        code, K = QMM_MX4, _values(B)
     else:
         px, ldx = _matrix(fn, "x", x)
         if sx is not None:

@@ -83,3 +83,21 @@ def test_mixture_of_many_experts(T, k):
     m4.assert_close(y, ref, bound, f"experts {T}")
     del packed
     free()
+
+
+@pytest.mark.parametrize("K", [(1 << 20) - 1, (1 << 20) - 31, (1 << 20) - 32])
+def test_longest_rows(K):
+    """K up to 2^20 - 1, through every call."""
+    m, n = 2, 3
+    q, s = m4.weight(n, K, 1)
+    x = m4.tokens(m, K, 2, torch.bfloat16)
+    W = qmm.mx4_pack(q.cuda(), s.cuda())
+    assert W.numel() == qmm.mx4_packed_bytes(n, K)
+    cq, cs = qmm.mx4_quantize(x.cuda())
+    rq, rs = m4.quantize_ref(x)
+    assert torch.equal(cq.cpu(), rq) and torch.equal(cs.cpu(), rs)
+    xv, wv = m4.values_ref(rq, rs, K), m4.values_ref(q, s, K)
+    assert torch.equal(qmm.mx4_dequantize(cq, cs, K).cpu().double(), xv)
+    bound = m4.gemm_bound(xv, wv, torch.float32)
+    m4.assert_close(qmm.mx4_gemm(cq, W, n, sx=cs), xv @ wv.t(), bound, "codes")
+    m4.assert_close(qmm.mx4_gemm(x.cuda(), W, n), xv @ wv.t(), bound, "values")

@@ -212,3 +212,16 @@ def test_route_reference_worked_example():
     assert ids.tolist() == [[1, 3, 0], [1, -1, -1]]
     assert torch.allclose(w, torch.tensor([[3, 3, 1], [7, 0, 0]]).double() / 7, rtol=1e-6)
     assert torch.allclose(m4.route_ref(lg, 1, False)[1], torch.tensor([[3 / 7], [1.0]]).double(), rtol=1e-6)
+
+
+def test_binding_takes_the_longest_rows():
+    """Sizes up to 2^20 - 1: their last block is whole in the codes, 2^20 values."""
+    K = (1 << 20) - 1
+    codes, scales = torch.zeros((2, 1 << 19), dtype=torch.uint8), torch.zeros((2, 1 << 15), dtype=torch.uint8)
+    W = torch.zeros(qmm.mx4_packed_bytes(3, K), dtype=torch.uint8)
+    assert W.numel() == 4352 * 2048
+    raises(lambda: qmm.mx4_gemm(codes, W, 3, sx=scales), "GPU tensors")
+    raises(lambda: qmm.mx4_gemm(torch.zeros(2, K), W, 3), "GPU tensors")
+    raises(lambda: qmm.mx4_pack(codes, scales), "GPU tensors")
+    raises(lambda: qmm.mx4_dequantize(codes, scales, K), "GPU tensors")
+    assert L.qmm_mx4_workspace_bytes(2, K, qmm.QMM_MX4) == 4352 * 2048
