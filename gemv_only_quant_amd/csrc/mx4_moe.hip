@@ -1078,8 +1078,9 @@ MoePlan plan_moe(int T, int D, int I, int E, int top_k, int x_dtype) {
   // (held in LDS or not, 18 tiles a workgroup: 45 and 39 us; 22 tiles: 41 and 48)
   const auto plan_up = p.xparts == 1 ? plan_held<1> : p.xparts == 2 ? plan_held<2> : plan_held<3>;
   p.up = plan_up(T, top_k, E, mx4_chunks(D), false, 2 * mx4_blocks(I), 20);
-  // (10 tiles a workgroup: 23 us and 5 of additions, else 23; 16 tiles: 27 and 5, else 36 and 5; 22 tiles: 28 and 5, else 49)
-  p.down = plan_held<kHParts>(T, top_k, E, mx4_chunks(I), true, p.Dz / 32, 14);
+  // (64 tokens; held in LDS or not, 10 tiles a workgroup: 26 and 31 us; 16 tiles: 34 and 44; 22 tiles: 39 and 56.  16 tokens,
+  // 13 tiles, where the additions then take a launch more: 79 and 79 for all)
+  p.down = plan_held<kHParts>(T, top_k, E, mx4_chunks(I), true, p.Dz / 32, 10);
   const int64_t z = (int64_t)T * top_k * p.Dz * 4;
   if (p.down.ranges > 1 && z * p.down.ranges > kRangesBytes) p.down = HeldPlan{};
   size_t at = 0;
