@@ -9,7 +9,6 @@
 namespace qmm {
 
 // Data types as in qmm.h / qmm_int8.h / qmm_mx4.h: 0 fp16, 1 bf16, 2 fp32, 4 mx4.
-constexpr int kTypeMx4 = 4;
 
 // ---- layouts ---------------------------------------------------------------
 constexpr int kBlock = 32;  // values that share a scale

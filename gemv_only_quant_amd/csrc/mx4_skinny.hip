@@ -299,15 +299,16 @@ template <int MT, int PS, int KW> static hipError_t packed_y(const Mx4Args& a, h
   }
   return e;
 }
-// Strips of a workgroup: 4, or 2, as long as most CUs have one; x is read again for each.  (K = 4096, us, 1, 2 and 4 strips:
-// 16 x 4096 8.5, 9.1, 9.4; 16 x 6144 11.9, 9.4, 9.7; 16 x 12288 16.0, 13.9, 10.7; 64 x 4096 11.3, 10.1, 13.0; 64 x 6144 17.5,
-// 10.8, 13.4; 64 x 12288 24.4, 16.8, 14.6.)
+// Up to 32 rows.  Strips of a workgroup: 4, or 2, as long as most CUs have one; x is read again for each.  (K = 4096, us, 1, 2
+// and 4 strips: 16 x 4096 8.5, 9.1, 9.4; 16 x 6144 11.9, 9.4, 9.7; 16 x 12288 16.0, 13.9, 10.7.)
 template <int MT> static hipError_t packed_m(const Mx4Args& a, hipStream_t s) {
   const int strips = (a.N + 15) / 16;
   if (strips >= 4 * 192) return packed_y<MT, 4, 4>(a, s);
-  if (strips >= 2 * 192) return packed_y<MT, 2, MT == 4 ? 4 : 8>(a, s);
+  if (strips >= 2 * 192) return packed_y<MT, 2, 8>(a, s);
   return packed_y<MT, 1, MT == 1 ? 16 : 8>(a, s);
 }
+// Blocks of 64 rows: 2 strips while they are all on the chip at once, else 4 (K = 4096, us, 2 and 4: 64 x 4096 10.1, 13.0; 64 x
+// 6144 10.8, 13.4; 64 x 12288 16.8, 14.6; 1 strip 11.3, 17.5 and 24.4).
 hipError_t launch_mx4_skinny(const Mx4Args& a, hipStream_t s) {
   if (a.M <= 16) return packed_m<1>(a, s);
   if (a.M <= 32) return packed_m<2>(a, s);
