@@ -3,7 +3,8 @@
 //
 //   h[t][j] = w[t][j] act(Wg_e x[t]) * (Wu_e x[t]),  y[t] = sum_j Wd_e h[t][j]
 //
-// Bound by reading the weights of the experts that some token chose, once.  The products run on the 16-bit matrix cores: a
+// Bound by reading the weights of the experts that some token chose: once for each 32 tokens of an expert (bf16 x), 16 (fp16) or
+// 10 to 15 (fp32, and h), which is what a workgroup's products hold.  The products run on the 16-bit matrix cores: a
 // code times its scale is exact in bf16, whose exponents reach as far as the scales', and an activation of more bits is a
 // sum of bf16 parts (fp16: 2, fp32 and h: 3, exact), rows of the product beside each other, whose sums are
 // added in fp32.  The other rows are an expert's further tokens, so most of the time parts cost nothing.
@@ -12,11 +13,11 @@
 // differs is how rows and weights come to a wave (us from one launch to the next, bf16 if not said):
 //
 //  few     up to 4 tokens: each workgroup of the first half makes the choices itself, one of the second has its columns of y
-//          whole.  Two launches, bound by their latencies: one token, 8 of 128 experts of 2048 x 768, 13.5 (17.4 by three
-//          launches, each part a product of its own)
+//          whole.  Two launches, bound by their latencies: one token, 8 of 128 experts of 2048 x 768, 14.0 (16.1 with the
+//          next forms' second half)
 //  held    many columns for each CU: a workgroup holds an expert's rows in LDS, a wave has whole tiles and no barrier between
-//          them.  64 tokens, 64 experts of 2048 x 1408, 6 each, fp16: 80 (4.0 TB/s of weights; by the next form 101); 16
-//          tokens, 8 experts of 4096 x 14336, 2 each: 137 (5.5 TB/s; 152)
+//          them.  64 tokens, 64 experts of 2048 x 1408, 6 each, fp16: 87 (3.4 TB/s of weights; second half by the
+//          next form 97); 16 tokens, 8 experts of 4096 x 14336, 2 each: 142 (5.2 TB/s; 154)
 //  other   K over a workgroup's waves, rows through each wave's own LDS: 5 tokens, 16 experts of 1001 x 777, 4 each, fp32: 18
 #include <math.h>
 
@@ -894,7 +895,7 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs 
 
 // The same for up to 4 tokens and 64 choices whose h fits LDS, at once or in two turns: a workgroup has 16 columns of y whole, its 16 waves taking
 // chunks of all chosen experts in turn; nothing is left to add across workgroups (one token, 8 of 128 experts of 2048 x 768:
-// 6.8 us, by the next kernel 9.3).
+// 7.0 us, by the kernel before 8.7).
 constexpr int kFewWaves = 16, kFewLds = 140 << 10;
 
 // `range` chunks of a row are in LDS at once: all, or (TWICE) half of them.
@@ -1106,8 +1107,8 @@ template <int XP> static hipError_t moe_t(const MoeArgs& a, const MoePlan& p, co
   auto each = [&](int tiles) { return (int)(((int64_t)tiles * slots + 1535) / 1536); };
   const int up = 2 * mx4_blocks(a.I), down = p.Dz / 32, per_up = each(up), per_down = each(down);
   const int xg = (a.T * (p.Dp / 8) + 255) / 256, gd = (down + per_down - 1) / per_down;
-  // where every workgroup makes the choices, all are on the chip at once (4 tokens, 8 of 128 experts of 2048 x 768: 30.4 us, in
-  // three rounds 35.9)
+  // where every workgroup makes the choices, all are on the chip at once (4 tokens, 8 of 128 experts of 2048 x 768: 31.4 us, in
+  // three rounds 36.5)
   const int per_few = (int)(((int64_t)up * slots + 511) / 512);
   hipError_t e = hipSuccess;
   if (a.T <= 4) {

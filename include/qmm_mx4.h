@@ -27,7 +27,7 @@
  *    bytes for codes and scales), M and N at most 2^31 - 1025
  *    (QMM_ERR_UNSUPPORTED beyond).
  *  - Outputs are fully overwritten (the elements of their rows; nothing between
- *    rows is touched) and must not overlap inputs.  An empty sum is zero.  A
+ *    rows is touched but the padding of qmm_mx4_quantize's scales) and must not overlap inputs.  An empty sum is zero.  A
  *    call without outputs is a no-op.
  *  - Results are the same from run to run, bit for bit.
  */
@@ -54,8 +54,8 @@ extern "C" {
  * block that holds an infinity or a NaN has scale byte 255 and codes 0: it
  * stands for NaNs.
  * ldc is a multiple of 16 and codes start on 16 bytes.  The bytes of a row of
- * scales from B up to the next multiple of 4 or to its end, whichever is less,
- * are set to 0.
+ * scales from B up to the next multiple of 4 or to lds, whichever is less, are
+ * its padding: they are set to 0, the last row's too (lds = B has none).
  */
 QMM_API qmm_status qmm_mx4_quantize(const void* x, int x_dtype, int64_t ldx, uint8_t* codes,
                                     int64_t ldc, uint8_t* scales, int64_t lds, int M, int K,
