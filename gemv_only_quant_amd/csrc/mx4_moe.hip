@@ -893,9 +893,9 @@ __global__ __launch_bounds__(64 * kHeldWaves) void moe_down_held_kernel(MoeArgs 
   }
 }
 
-// The same for up to 4 tokens and 64 choices whose h fits LDS, at once or in two turns: a workgroup has 16 columns of y whole, its 16 waves taking
-// chunks of all chosen experts in turn; nothing is left to add across workgroups (one token, 8 of 128 experts of 2048 x 768:
-// 7.0 us, by the kernel before 8.7).
+// The same for up to 4 tokens and 64 choices whose h fits LDS, at once or in two turns: a workgroup has 16 columns of y
+// whole, its 16 waves taking chunks of all chosen experts in turn; nothing is left to add across workgroups (one token, 8 of
+// 128 experts of 2048 x 768: 7.0 us, by the kernel before 8.7).
 constexpr int kFewWaves = 16, kFewLds = 140 << 10;
 
 // `range` chunks of a row are in LDS at once: all, or (TWICE) half of them.
@@ -1121,7 +1121,9 @@ template <int XP> static hipError_t moe_t(const MoeArgs& a, const MoePlan& p, co
     if (e != hipSuccess) return e;
     const HeldPlan& held = p.up;
     if (held.groups != 0) {
-      e = launch_kernel(held.groups == 1 ? moe_up_held_kernel<XP, 1> : held.groups == 2 ? moe_up_held_kernel<XP, 2> : moe_up_held_kernel<XP, kHeldGroups<XP>>,
+      e = launch_kernel(held.groups == 1   ? moe_up_held_kernel<XP, 1>
+                        : held.groups == 2 ? moe_up_held_kernel<XP, 2>
+                                           : moe_up_held_kernel<XP, kHeldGroups<XP>>,
                         dim3((unsigned)((up + held.per - 1) / held.per), (unsigned)slots), dim3(64 * kHeldWaves), s, a, o, p.Dp,
                         p.Ip, pairs, held.per);
     } else {
@@ -1143,7 +1145,9 @@ template <int XP> static hipError_t moe_t(const MoeArgs& a, const MoePlan& p, co
   const HeldPlan& held = p.down;
   const bool join = held.groups == 0 && a.T <= 16;
   if (held.groups != 0)
-    e = launch_kernel(held.groups == 1 ? moe_down_held_kernel<1> : held.groups == 2 ? moe_down_held_kernel<2> : moe_down_held_kernel<kHeldGroups<kHParts>>,
+    e = launch_kernel(held.groups == 1   ? moe_down_held_kernel<1>
+                      : held.groups == 2 ? moe_down_held_kernel<2>
+                                         : moe_down_held_kernel<kHeldGroups<kHParts>>,
                       dim3((unsigned)((down + held.per - 1) / held.per), (unsigned)slots, (unsigned)held.ranges), dim3(64 * kHeldWaves), s, a,
                       o, p.Ip, pairs, p.Dz, held.per, held.range);
   else
